@@ -33,6 +33,8 @@ E4M3, E5M2 = 0, 1
 SCALE_F32, SCALE_UE8M0 = 0, 1
 OUT_F32, OUT_BF16 = 0, 1
 K_MAJOR, MN_MAJOR = 0, 1
+ACT_NONE, ACT_RELU, ACT_RELU2, ACT_SILU, ACT_GELU_TANH, ACT_GELU = 0, 1, 2, 3, 4, 5
+NORM_TENSOR, NORM_GROUP, NORM_MX = 0, 1, 2
 
 _vp, _i64, _int, _d = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_double
 _SIGS = {
@@ -68,6 +70,12 @@ _SIGS = {
     "fp8_quantize_token_group32": [_vp, _int, _i64, _i64, _int, _int, _vp, _vp, _vp],
     "fp8_quantize_block32_f32": [_vp, _int, _i64, _i64, _int, _vp, _vp, _vp],
     "fp8_gemm_group32": [_vp, _vp, _vp, _vp, _i64, _i64, _i64, _vp, _i64, _vp],
+    "fp8_rmsnorm_quantize": [_vp, _vp],
+    "fp8_rmsnorm_backward": [_vp, _vp],
+    "fp8_gemm_tensor_epilogue": [_vp, _vp, _vp],
+    "fp8_gemm_tensor_act_backward": [_vp, _vp, _vp],
+    "fp8_gemm_group_epilogue": [_vp, _vp, _vp, _vp, _int, _i64, _i64, _i64, _vp, _vp, _vp, _i64,
+                                _vp],
     "fp8_get_last_device_error": [ctypes.POINTER(ctypes.c_int), _vp],
     "fp8_set_option": [_int, _int],
 }
@@ -80,7 +88,13 @@ _lib.fp8_status_string.restype = ctypes.c_char_p
 _lib.fp8_version.argtypes = []
 _lib.fp8_version.restype = ctypes.c_char_p
 
-EXPORTED = tuple(_SIGS) + ("fp8_status_string", "fp8_version")
+_SIZES = ("fp8_rmsnorm_backward_workspace", "fp8_act_backward_workspace")
+for _name in _SIZES:
+    _fn = getattr(_lib, _name)
+    _fn.argtypes = [_i64, _i64]
+    _fn.restype = _i64
+
+EXPORTED = tuple(_SIGS) + _SIZES + ("fp8_status_string", "fp8_version")
 
 
 class Fp8Error(RuntimeError):
@@ -437,6 +451,202 @@ def fp8_adamw_multi(items, step, lr=1e-4, beta1=0.9, beta2=0.999, eps=1e-8, weig
     arr = (AdamwItem * len(items))(*items) if items else None
     _call("fp8_adamw_multi", ctypes.cast(arr, _vp) if arr is not None else None, len(items),
           _p(step), int(bool(advance)), lr, beta1, beta2, eps, weight_decay, _stream(stream))
+
+
+# ------------------------------------- RMS norm, linear layer's epilogue --
+
+def _rows(t):
+    """(device pointer, row pitch) of a 2-D CUDA tensor with contiguous rows
+    (None -> NULL)."""
+    if t is None:
+        return None, 0
+    if not t.is_cuda:
+        raise ValueError("expected a CUDA tensor")
+    if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] != 1):
+        raise ValueError("expected a matrix with contiguous rows")
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def _shaped(t, shape, dtype, what):
+    if t is not None and (tuple(t.shape) != shape or t.dtype != dtype):
+        raise ValueError("%s must be %s %s" % (what, dtype, shape))
+
+
+def _scratch(nbytes, device, stream):
+    """Scratch of one call: torch hands the memory on in the current stream's
+    order, so a call on another stream brings its own."""
+    if stream is not None:
+        raise ValueError("a call on an explicit stream needs an explicit workspace")
+    return torch.empty(max(16, nbytes), dtype=torch.uint8, device=device)
+
+
+class RmsNorm(ctypes.Structure):
+    """fp8_rmsnorm_t (include/fp8gemm.h)."""
+    _fields_ = [("x", _vp), ("residual", _vp), ("w", _vp), ("dt", _int), ("w_dt", _int),
+                ("M", _i64), ("K", _i64), ("ld_x", _i64), ("ld_residual", _i64), ("eps", _d),
+                ("mode", _int), ("fmt", _int), ("sfmt", _int), ("scale", _vp), ("q", _vp),
+                ("scales", _vp), ("sum_out", _vp), ("ld_sum", _i64), ("y_out", _vp),
+                ("ld_y", _i64), ("inv_rms", _vp), ("amax_out", _vp)]
+
+
+class RmsNormGrad(ctypes.Structure):
+    """fp8_rmsnorm_grad_t (include/fp8gemm.h)."""
+    _fields_ = [("dy", _vp), ("r", _vp), ("w", _vp), ("d_residual", _vp), ("inv_rms", _vp),
+                ("dy_dt", _int), ("dt", _int), ("w_dt", _int), ("M", _i64), ("K", _i64),
+                ("ld_dy", _i64), ("ld_r", _i64), ("ld_dres", _i64), ("ld_dx", _i64), ("dx", _vp),
+                ("dw", _vp), ("accumulate_dw", _int), ("q", _vp), ("fmt", _int), ("scale", _vp),
+                ("amax_out", _vp), ("workspace", _vp), ("workspace_bytes", _i64)]
+
+
+class LinearEpilogue(ctypes.Structure):
+    """fp8_linear_epilogue_t (include/fp8gemm.h)."""
+    _fields_ = [("act", _int), ("residual", _vp), ("residual_dt", _int), ("ld_residual", _i64),
+                ("pre", _vp), ("ld_pre", _i64), ("q", _vp), ("q_fmt", _int), ("q_scale", _vp),
+                ("q_amax", _vp)]
+
+
+class ActGradEpilogue(ctypes.Structure):
+    """fp8_act_grad_epilogue_t (include/fp8gemm.h)."""
+    _fields_ = [("act", _int), ("pre", _vp), ("ld_pre", _i64), ("q", _vp), ("q_fmt", _int),
+                ("q_scale", _vp), ("q_amax", _vp), ("dbias", _vp), ("accumulate_dbias", _int),
+                ("workspace", _vp), ("workspace_bytes", _i64)]
+
+
+def fp8_rmsnorm_quantize(x, w, eps, fmt, q, *, residual=None, sum_out=None, scale=None,
+                         amax_out=None, scales=None, sfmt=SCALE_F32, local=None, y_out=None,
+                         inv_rms=None, stream=None):
+    """r = x + residual (-> sum_out), y = r / rms(r) * w (-> y_out, bf16) and
+    the codes q of y: per tensor under `scale` (amax_out: max |y|), per 1x128
+    group (`scales`, sfmt), or one-level MX (`local` words).  w: [K] gains, or
+    None for ones; inv_rms: fp32 [M], kept for fp8_rmsnorm_backward."""
+    m, k = x.shape
+    if (scale is not None) + (scales is not None) + (local is not None) != 1:
+        raise ValueError("one of scale, scales and local selects the quantization")
+    mode = NORM_TENSOR if scale is not None else NORM_GROUP if scales is not None else NORM_MX
+    dt = _in_dt(x)
+    _shaped(residual, (m, k), x.dtype, "residual")
+    _shaped(sum_out, (m, k), x.dtype, "sum_out")
+    _shaped(y_out, (m, k), torch.bfloat16, "y_out")
+    _shaped(inv_rms, (m,), torch.float32, "inv_rms")
+    if w is not None and w.numel() != k or q.numel() != m * k:
+        raise ValueError("w must have K elements and q M * K")
+    px, ldx = _rows(x)
+    pr, ldr = _rows(residual)
+    ps, lds = _rows(sum_out)
+    py, ldy = _rows(y_out)
+    d = RmsNorm(px, pr, _p(w), dt, dt if w is None else _in_dt(w), m, k, ldx, ldr, eps, mode, fmt,
+                sfmt, _p(scale), _p(q), _p(scales if local is None else local), ps, lds, py, ldy,
+                _p(inv_rms), _p(amax_out))
+    _call("fp8_rmsnorm_quantize", ctypes.addressof(d), _stream(stream))
+
+
+def fp8_rmsnorm_backward_workspace(m, k):
+    """Bytes of scratch that fp8_rmsnorm_backward needs for dw."""
+    return _lib.fp8_rmsnorm_backward_workspace(m, k)
+
+
+def fp8_rmsnorm_backward(dy, r, inv_rms, w, dx, *, d_residual=None, dw=None, accumulate_dw=False,
+                         q=None, fmt=E5M2, scale=None, amax_out=None, workspace=None, stream=None):
+    """dx = gradient of x and of residual, through the norm and (d_residual)
+    past it; dw: fp32 [K]; q: the codes of dx under `scale`, amax_out its
+    max |dx|.  r, inv_rms: as fp8_rmsnorm_quantize wrote them.  workspace
+    (with dw): device scratch, allocated on the current stream when None."""
+    m, k = r.shape
+    _shaped(dy, (m, k), dy.dtype, "dy")
+    _shaped(dx, (m, k), r.dtype, "dx")
+    _shaped(d_residual, (m, k), r.dtype, "d_residual")
+    _shaped(inv_rms, (m,), torch.float32, "inv_rms")
+    _shaped(dw, (k,), torch.float32, "dw")
+    if w is not None and w.numel() != k or q is not None and q.numel() != m * k:
+        raise ValueError("w must have K elements and q M * K")
+    if dw is not None and workspace is None:
+        workspace = _scratch(fp8_rmsnorm_backward_workspace(m, k), r.device, stream)
+    py, ldy = _rows(dy)
+    pr, ldr = _rows(r)
+    pe, lde = _rows(d_residual)
+    px, ldx = _rows(dx)
+    d = RmsNormGrad(py, pr, _p(w), pe, _p(inv_rms), _in_dt(dy), _in_dt(r),
+                    IN_F32 if w is None else _in_dt(w), m, k, ldy, ldr, lde, ldx, px, _p(dw),
+                    int(bool(accumulate_dw)), _p(q), fmt, _p(scale), _p(amax_out), _p(workspace),
+                    0 if workspace is None else workspace.numel() * workspace.element_size())
+    _call("fp8_rmsnorm_backward", ctypes.addressof(d), _stream(stream))
+
+
+def _epilogue_problem(a, fa, b, fb, sa, sb, out, a_layout, b_layout, bias):
+    m, k = a.shape if a_layout == K_MAJOR else a.shape[::-1]
+    n, kb = b.shape if b_layout == K_MAJOR else b.shape[::-1]
+    if kb != k:
+        raise ValueError("operands of different K")
+    _shaped(bias, (n,), torch.float32, "bias")
+    c, ldc = _rows(out)
+    if out is not None and (out.shape != (m, n) or out.dtype not in (torch.bfloat16, torch.float32)):
+        raise ValueError("out must be bf16 or fp32 [M, N]")
+    dt = OUT_F32 if out is not None and out.dtype == torch.float32 else OUT_BF16
+    return m, n, GemmProblem(_p(a), _p(b), _p(sa), _p(sb), m, n, k, fa, fb, dt, 0, c, ldc, a_layout,
+                             b_layout, _p(bias), None, None)
+
+
+def _linear_epilogue(m, n, act, residual, pre_out, q=None, q_fmt=E4M3, q_scale=None, q_amax=None):
+    pr, ldr = _rows(residual)
+    pp, ldp = _rows(pre_out)
+    _shaped(pre_out, (m, n), torch.bfloat16, "pre_out")
+    if residual is not None and tuple(residual.shape) != (m, n):
+        raise ValueError("residual must be [M, N]")
+    if q is not None and q.numel() != m * n:
+        raise ValueError("q must have M * N codes")
+    dt = OUT_BF16 if residual is None or _in_dt(residual) == IN_BF16 else OUT_F32
+    return LinearEpilogue(act, pr, dt, ldr, pp, ldp, _p(q), q_fmt, _p(q_scale), _p(q_amax))
+
+
+def fp8_gemm_tensor_epilogue(a, fa, b, fb, sa, sb, out, *, bias=None, act=ACT_NONE, residual=None,
+                             pre_out=None, q=None, q_fmt=E4M3, q_scale=None, q_amax=None,
+                             a_layout=K_MAJOR, b_layout=K_MAJOR, stream=None):
+    """Per-tensor GEMM with y = act(z) + residual, z = sa sb A B^T + bias, in
+    its epilogue: out (bf16, fp32, or None with q) <- y, pre_out <- bf16(z),
+    q <- codes of y under q_scale, q_amax <- max |y|."""
+    m, n, p = _epilogue_problem(a, fa, b, fb, sa, sb, out, a_layout, b_layout, bias)
+    e = _linear_epilogue(m, n, act, residual, pre_out, q, q_fmt, q_scale, q_amax)
+    _call("fp8_gemm_tensor_epilogue", ctypes.addressof(p), ctypes.addressof(e), _stream(stream))
+
+
+def fp8_gemm_group_epilogue(a, sa, b, sb, sfmt, out, *, bias=None, act=ACT_NONE, residual=None,
+                            pre_out=None, stream=None):
+    """Per-K-group GEMM with the same epilogue; out bf16."""
+    m, k = a.shape
+    n = b.shape[0]
+    _shaped(out, (m, n), torch.bfloat16, "out")
+    _shaped(bias, (n,), torch.float32, "bias")
+    e = _linear_epilogue(m, n, act, residual, pre_out)
+    c, ldc = _rows(out)
+    _call("fp8_gemm_group_epilogue", _p(a), _p(sa), _p(b), _p(sb), sfmt, m, n, k, _p(bias),
+          ctypes.addressof(e), c, ldc, _stream(stream))
+
+
+def fp8_act_backward_workspace(m, n):
+    """Bytes of scratch that fp8_gemm_tensor_act_backward needs for dbias."""
+    return _lib.fp8_act_backward_workspace(m, n)
+
+
+def fp8_gemm_tensor_act_backward(a, fa, b, fb, sa, sb, pre, act, *, out=None, q=None, q_fmt=E5M2,
+                                 q_scale=None, q_amax=None, dbias=None, accumulate_dbias=False,
+                                 workspace=None, a_layout=K_MAJOR, b_layout=K_MAJOR, stream=None):
+    """dz = (sa sb A B^T) * act'(pre) in the GEMM's epilogue: out (bf16 or
+    fp32) and/or q <- codes of dz under q_scale (q_amax: max |dz|); dbias:
+    fp32 [N] column sums.  workspace (with dbias): device scratch, allocated
+    on the current stream when None."""
+    m, n, p = _epilogue_problem(a, fa, b, fb, sa, sb, out, a_layout, b_layout, None)
+    _shaped(pre, (m, n), torch.bfloat16, "pre")
+    _shaped(dbias, (n,), torch.float32, "dbias")
+    if q is not None and q.numel() != m * n:
+        raise ValueError("q must have M * N codes")
+    if dbias is not None and workspace is None:
+        workspace = _scratch(fp8_act_backward_workspace(m, n), pre.device, stream)
+    pp, ldp = _rows(pre)
+    e = ActGradEpilogue(act, pp, ldp, _p(q), q_fmt, _p(q_scale), _p(q_amax), _p(dbias),
+                        int(bool(accumulate_dbias)), _p(workspace),
+                        0 if workspace is None else workspace.numel() * workspace.element_size())
+    _call("fp8_gemm_tensor_act_backward", ctypes.addressof(p), ctypes.addressof(e),
+          _stream(stream))
 
 
 def fp8_get_last_device_error(stream=None):

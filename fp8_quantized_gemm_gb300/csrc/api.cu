@@ -15,6 +15,7 @@
 
 #include "fp8gemm.h"
 #include "kernels.h"
+#include "norm.h"
 #include "support.h"
 
 namespace {
@@ -218,7 +219,9 @@ int get_workspace(cudaStream_t st, size_t need, void **out, int slot) {
   return FP8_OK;
 }
 
-int run_gemm(int mode, const uint8_t *a, const uint8_t *b, GemmArgs &args, cudaStream_t st) {
+// ep: the linear layer's epilogue (nullable).
+int run_gemm(int mode, const uint8_t *a, const uint8_t *b, GemmArgs &args, cudaStream_t st,
+             const fp8k::LinearEp *ep = nullptr) {
   DeviceState *d = nullptr;
   int rc = device_state(&d);
   if (rc != FP8_OK) return rc;
@@ -236,6 +239,8 @@ int run_gemm(int mode, const uint8_t *a, const uint8_t *b, GemmArgs &args, cudaS
     if ((rc = encode_gemm_operand(&tmb, b, args.b_mn, args.K, args.N,
                                   fp8k::gemm_pair_b_rows())) != FP8_OK)
       return rc;
+    if (ep != nullptr)
+      return to_status(fp8k::launch_gemm_pair_epilogue(tma, tmb, args, *ep, false, d->sms, st));
     CUtensorMap tmc{};
     args.tma_store = use_tma_store(args.c, args.ldc, args.out_dt, args.accumulate) ? 1 : 0;
     if (args.tma_store &&
@@ -248,7 +253,7 @@ int run_gemm(int mode, const uint8_t *a, const uint8_t *b, GemmArgs &args, cudaS
       fp8k::gemm_pair_promote_eligible(args.M, args.N, args.K, d->sms)) {
     if ((rc = encode_operand(&tmb, b, args.K, args.N, fp8k::gemm_pair_promote_b_rows())) != FP8_OK)
       return rc;
-    return to_status(fp8k::launch_gemm_pair_promote(tma, tmb, args, d->sms, st));
+    return to_status(fp8k::launch_gemm_pair_promote(tma, tmb, args, d->sms, st, ep));
   }
   // multicast pairs of vertically adjacent tiles share each B box: measured
   // faster for 128-wide tiles (the FP32-promotion mode, and the block-scaled
@@ -262,7 +267,9 @@ int run_gemm(int mode, const uint8_t *a, const uint8_t *b, GemmArgs &args, cudaS
   if ((rc = encode_gemm_operand(&tmb, b, args.b_mn, args.K, args.N,
                                 args.multicast ? bn / 2 : bn)) != FP8_OK)
     return rc;
-  return to_status(fp8k::launch_gemm(mode, tma, tmb, args, d->sms, st));
+  return to_status(ep != nullptr
+                       ? fp8k::launch_gemm_epilogue(mode, tma, tmb, args, *ep, d->sms, st)
+                       : fp8k::launch_gemm(mode, tma, tmb, args, d->sms, st));
 }
 
 int check_gemm_common(const uint8_t *a, const uint8_t *b, int64_t M, int64_t N, int64_t K,
@@ -322,8 +329,7 @@ int check_tensor_problem(const fp8_gemm_problem_t &p) {
   return FP8_OK;
 }
 
-// One validated per-tensor problem through the regular launch path.
-int run_tensor_problem(const fp8_gemm_problem_t &p, cudaStream_t st) {
+GemmArgs tensor_args(const fp8_gemm_problem_t &p) {
   GemmArgs args{};
   args.M = p.M; args.N = p.N; args.K = p.K; args.fa = p.fa; args.fb = p.fb;
   args.out_dt = p.out_dt; args.accumulate = p.accumulate; args.ldc = p.ldc; args.c = p.c;
@@ -331,7 +337,146 @@ int run_tensor_problem(const fp8_gemm_problem_t &p, cudaStream_t st) {
   args.a_mn = p.a_layout == FP8_MN_MAJOR;
   args.b_mn = p.b_layout == FP8_MN_MAJOR;
   args.bias = p.bias;
+  return args;
+}
+
+// One validated per-tensor problem through the regular launch path.
+int run_tensor_problem(const fp8_gemm_problem_t &p, cudaStream_t st) {
+  GemmArgs args = tensor_args(p);
   return run_gemm(fp8k::kScaleTensor, p.a, p.b, args, st);
+}
+
+// ------------------------------------- linear epilogue and RMS norm calls --
+// SMs the norm gradient's scratch is sized for (more are left idle by it).
+constexpr int kNormSms = 152;
+
+bool aligned_to(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+// A nullable [rows, ld] operand read and written in 16-byte vectors of eight
+// elements (fp32: two).
+int check_rows(const void *p, int64_t ld, int64_t cols) {
+  if (p == nullptr) return FP8_OK;
+  if (ld < cols) return FP8_ERR_INVALID_ARG;
+  return aligned16(p) && ld % 8 == 0 ? FP8_OK : FP8_ERR_MISALIGNED;
+}
+
+// A per-tensor problem taken by the epilogue calls: no other epilogue, and an
+// output that may be missing when there are codes.
+int check_epilogue_problem(const fp8_gemm_problem_t &p, bool codes) {
+  if (p.adamw != nullptr || p.swiglu != nullptr || p.accumulate != 0) return FP8_ERR_UNSUPPORTED;
+  if (p.c != nullptr || !codes) return check_tensor_problem(p);
+  fp8_gemm_problem_t t = p;
+  t.c = const_cast<uint8_t *>(p.a);  // stands for an output: checked, not used
+  t.out_dt = FP8_OUT_BF16;
+  t.ldc = p.N;
+  return check_tensor_problem(t);
+}
+
+// Validates and converts the public epilogue descriptor (N output columns).
+int linear_epilogue(const fp8_linear_epilogue_t &e, int64_t N, fp8k::LinearEp *out) {
+  if (e.act < FP8_ACT_NONE || e.act > FP8_ACT_GELU) return FP8_ERR_INVALID_ARG;
+  if (e.residual != nullptr) {
+    if (e.residual_dt != FP8_OUT_F32 && e.residual_dt != FP8_OUT_BF16) return FP8_ERR_INVALID_ARG;
+    if (e.ld_residual < N) return FP8_ERR_INVALID_ARG;
+    if (!aligned_to(e.residual, e.residual_dt == FP8_OUT_F32 ? 4 : 2)) return FP8_ERR_MISALIGNED;
+  }
+  if (e.pre != nullptr) {
+    if (e.ld_pre < N) return FP8_ERR_INVALID_ARG;
+    if (!aligned_to(e.pre, 2)) return FP8_ERR_MISALIGNED;
+  }
+  if (e.q != nullptr) {
+    if (e.q_scale == nullptr || e.q_amax == e.q_scale || !valid_fmt(e.q_fmt))
+      return FP8_ERR_INVALID_ARG;
+    if (!aligned_to(e.q_scale, 4) || !aligned_to(e.q_amax, 4)) return FP8_ERR_MISALIGNED;
+  } else if (e.q_amax != nullptr) {
+    return FP8_ERR_UNSUPPORTED;
+  }
+  fp8k::LinearEp l{};
+  l.act = e.act;
+  l.res = e.residual;
+  l.res_dt = e.residual_dt;
+  l.ld_res = e.ld_residual;
+  l.res_vec = vector_store_ok(e.residual, e.ld_residual, e.residual_dt);
+  l.pre = e.pre;
+  l.ld_pre = e.ld_pre;
+  l.pre_vec = vector_store_ok(e.pre, e.ld_pre, FP8_OUT_BF16);
+  l.q = e.q;
+  l.q_fmt = e.q_fmt;
+  l.q_scale = e.q_scale;
+  l.q_amax = reinterpret_cast<uint32_t *>(e.q_amax);
+  l.q_vec = aligned16(e.q) && N % 16 == 0 ? 1 : 0;
+  *out = l;
+  return FP8_OK;
+}
+
+int clear_amax(const fp8k::LinearEp &ep, cudaStream_t st) {
+  if (ep.q_amax == nullptr) return FP8_OK;
+  return to_status(cudaMemsetAsync(ep.q_amax, 0, sizeof(uint32_t), st));
+}
+
+// The per-K-group GEMM, plain (ep null) or with the linear layer's epilogue.
+int run_group(const uint8_t *a, const void *sa, const uint8_t *b, const void *sb, int sfmt,
+              int64_t M, int64_t N, int64_t K, const float *bias, void *c, int64_t ldc,
+              const fp8k::LinearEp *ep, fp8_stream_t stream) {
+  int rc = check_gemm_common(a, b, M, N, K, 128);
+  if (rc != FP8_OK) return rc;
+  if (sa == nullptr || sb == nullptr) return FP8_ERR_INVALID_ARG;
+  if (sfmt != FP8_SCALE_F32 && sfmt != FP8_SCALE_UE8M0) return FP8_ERR_INVALID_ARG;
+  if ((rc = check_output(c, N, ldc, FP8_OUT_BF16)) != FP8_OK) return rc;
+  GemmArgs args{};
+  args.M = M; args.N = N; args.K = K; args.fa = FP8_E4M3; args.fb = FP8_E4M3;
+  args.out_dt = FP8_OUT_BF16; args.ldc = ldc; args.c = c; args.sa = sa; args.sb = sb;
+  args.bias = bias;
+  const int mode = sfmt == FP8_SCALE_F32 ? fp8k::kScaleGroupF32 : fp8k::kScaleGroupUe8m0;
+  if (ep == nullptr && g_use_gemv && fp8k::gemv_group_eligible(M, K)) {
+    // one row: a stream over the weights on the CUDA cores
+    DeviceState *d = nullptr;
+    if ((rc = device_state(&d)) != FP8_OK) return rc;
+    return to_status(
+        fp8k::launch_gemv_group(a, sa, b, sb, sfmt, M, N, K, bias, c, (cudaStream_t)stream));
+  }
+  if ((g_use_skinny || ep != nullptr) && fp8k::gemm_skinny_rows(M) != 0) {
+    // 1-128 rows: the weights stream through the few-row kernel (its tile
+    // is 128 weight rows x the activation rows padded to 16, 32 or 64; two
+    // 64-row halves beyond 64)
+    DeviceState *d = nullptr;
+    if ((rc = device_state(&d)) != FP8_OK) return rc;
+    args.err = d->err;
+    args.wait_limit_ns = g_wait_limit_ns;
+    args.vec_store = vector_store_ok(c, ldc, FP8_OUT_BF16);
+    args.ksplit = fp8k::gemm_skinny_ksplit(M, N, K, d->sms);
+    CUtensorMap tmw, tmx;
+    if ((rc = encode_operand(&tmw, b, K, N, 128)) != FP8_OK) return rc;
+    if ((rc = encode_operand(&tmx, a, K, M, fp8k::gemm_skinny_rows(M))) != FP8_OK) return rc;
+    return to_status(fp8k::launch_gemm_skinny(sfmt == FP8_SCALE_F32 ? 0 : 1, tmw, tmx, args,
+                                              (cudaStream_t)stream, ep));
+  }
+  if (mode == fp8k::kScaleGroupUe8m0 && M > 128) {
+    // Beyond one row tile: the UE8M0 scales become E8M0 words (four equal
+    // bytes per 128-wide K slice) that the block-scaled GEMM bulk-copies per
+    // stage, in place of the per-stage byte loads of the group mode.  Same
+    // products, same FP32 accumulation: the tensor core applies 2^e to each
+    // 1x32 sub-block of the group instead of the group as a whole.  (At
+    // K 7168, N 2048 the words measured equal at M = 64-128, slower at
+    // M = 16 (the conversion's launch) and faster from M = 256 on.)
+    DeviceState *d = nullptr;
+    if ((rc = device_state(&d)) != FP8_OK) return rc;
+    const size_t G = (size_t)(K / 128);
+    const size_t mpad = (size_t)(M + 127) / 128 * 128, npad = (size_t)(N + 127) / 128 * 128;
+    void *w = nullptr;
+    if ((rc = get_workspace((cudaStream_t)stream, G * (mpad + npad) * 4, &w, kWsWords)) != FP8_OK)
+      return rc;
+    uint32_t *la = static_cast<uint32_t *>(w), *lb = la + G * mpad;
+    if ((rc = to_status(fp8k::launch_ue8m0_words(static_cast<const uint8_t *>(sa),
+                                                 static_cast<const uint8_t *>(sb), M, N, K, la, lb,
+                                                 d->sms, (cudaStream_t)stream))) != FP8_OK)
+      return rc;
+    args.sa = la;
+    args.sb = lb;
+    args.ga = args.gb = nullptr;
+    return run_gemm(fp8k::kScaleMx, a, b, args, (cudaStream_t)stream, ep);
+  }
+  return run_gemm(mode, a, b, args, (cudaStream_t)stream, ep);
 }
 
 }  // namespace
@@ -728,65 +873,171 @@ int fp8_gemm_group_bias(const uint8_t *a, const void *sa, const uint8_t *b, cons
                         int sfmt, int64_t M, int64_t N, int64_t K, const float *bias, void *c,
                         int64_t ldc, fp8_stream_t stream) {
   const NvtxRange nvtx_range(__func__);
-  int rc = check_gemm_common(a, b, M, N, K, 128);
+  return run_group(a, sa, b, sb, sfmt, M, N, K, bias, c, ldc, nullptr, stream);
+}
+
+int fp8_gemm_group_epilogue(const uint8_t *a, const void *sa, const uint8_t *b, const void *sb,
+                            int sfmt, int64_t M, int64_t N, int64_t K, const float *bias,
+                            const fp8_linear_epilogue_t *epilogue, void *c, int64_t ldc,
+                            fp8_stream_t stream) {
+  const NvtxRange nvtx_range(__func__);
+  if (epilogue == nullptr || c == nullptr) return FP8_ERR_INVALID_ARG;
+  if (epilogue->q != nullptr) return FP8_ERR_UNSUPPORTED;
+  fp8k::LinearEp ep;
+  const int rc = linear_epilogue(*epilogue, N, &ep);
   if (rc != FP8_OK) return rc;
-  if (sa == nullptr || sb == nullptr) return FP8_ERR_INVALID_ARG;
-  if (sfmt != FP8_SCALE_F32 && sfmt != FP8_SCALE_UE8M0) return FP8_ERR_INVALID_ARG;
-  if ((rc = check_output(c, N, ldc, FP8_OUT_BF16)) != FP8_OK) return rc;
-  GemmArgs args{};
-  args.M = M; args.N = N; args.K = K; args.fa = FP8_E4M3; args.fb = FP8_E4M3;
-  args.out_dt = FP8_OUT_BF16; args.ldc = ldc; args.c = c; args.sa = sa; args.sb = sb;
-  args.bias = bias;
-  const int mode = sfmt == FP8_SCALE_F32 ? fp8k::kScaleGroupF32 : fp8k::kScaleGroupUe8m0;
-  if (g_use_gemv && fp8k::gemv_group_eligible(M, K)) {
-    // one row: a stream over the weights on the CUDA cores
-    DeviceState *d = nullptr;
-    if ((rc = device_state(&d)) != FP8_OK) return rc;
-    return to_status(
-        fp8k::launch_gemv_group(a, sa, b, sb, sfmt, M, N, K, bias, c, (cudaStream_t)stream));
+  return run_group(a, sa, b, sb, sfmt, M, N, K, bias, c, ldc, &ep, stream);
+}
+
+int fp8_gemm_tensor_epilogue(const fp8_gemm_problem_t *problem,
+                             const fp8_linear_epilogue_t *epilogue, fp8_stream_t stream) {
+  const NvtxRange nvtx_range(__func__);
+  if (problem == nullptr || epilogue == nullptr) return FP8_ERR_INVALID_ARG;
+  int rc = check_epilogue_problem(*problem, epilogue->q != nullptr);
+  if (rc != FP8_OK) return rc;
+  fp8k::LinearEp ep;
+  if ((rc = linear_epilogue(*epilogue, problem->N, &ep)) != FP8_OK) return rc;
+  DeviceState *d = nullptr;
+  if ((rc = device_state(&d)) != FP8_OK) return rc;
+  const cudaStream_t st = (cudaStream_t)stream;
+  if ((rc = clear_amax(ep, st)) != FP8_OK) return rc;
+  GemmArgs args = tensor_args(*problem);
+  return run_gemm(fp8k::kScaleTensor, problem->a, problem->b, args, st, &ep);
+}
+
+int64_t fp8_act_backward_workspace(int64_t M, int64_t N) {
+  return M < 1 || N < 1 || M >= kMaxDim || N >= kMaxDim ? 0 : (M + 31) / 32 * N * 4;
+}
+
+int fp8_gemm_tensor_act_backward(const fp8_gemm_problem_t *problem,
+                                 const fp8_act_grad_epilogue_t *epilogue, fp8_stream_t stream) {
+  const NvtxRange nvtx_range(__func__);
+  if (problem == nullptr || epilogue == nullptr) return FP8_ERR_INVALID_ARG;
+  const fp8_gemm_problem_t &p = *problem;
+  const fp8_act_grad_epilogue_t &e = *epilogue;
+  int rc = check_epilogue_problem(p, e.q != nullptr);
+  if (rc != FP8_OK) return rc;
+  if (e.pre == nullptr) return FP8_ERR_INVALID_ARG;
+  if (p.bias != nullptr) return FP8_ERR_UNSUPPORTED;
+  if (e.accumulate_dbias != 0 && e.accumulate_dbias != 1) return FP8_ERR_INVALID_ARG;
+  fp8_linear_epilogue_t f{};
+  f.act = e.act;
+  f.pre = const_cast<void *>(e.pre);  // only read
+  f.ld_pre = e.ld_pre;
+  f.q = e.q; f.q_fmt = e.q_fmt; f.q_scale = e.q_scale; f.q_amax = e.q_amax;
+  fp8k::LinearEp ep;
+  if ((rc = linear_epilogue(f, p.N, &ep)) != FP8_OK) return rc;
+  if (e.dbias != nullptr) {
+    if (e.workspace == nullptr || e.workspace_bytes < fp8_act_backward_workspace(p.M, p.N))
+      return FP8_ERR_INVALID_ARG;
+    if (!aligned16(e.workspace) || !aligned_to(e.dbias, 4)) return FP8_ERR_MISALIGNED;
+    ep.part = static_cast<float *>(e.workspace);
   }
-  if (g_use_skinny && fp8k::gemm_skinny_rows(M) != 0) {
-    // 1-128 rows: the weights stream through the few-row kernel (its tile
-    // is 128 weight rows x the activation rows padded to 16, 32 or 64; two
-    // 64-row halves beyond 64)
-    DeviceState *d = nullptr;
-    if ((rc = device_state(&d)) != FP8_OK) return rc;
-    args.err = d->err;
-    args.wait_limit_ns = g_wait_limit_ns;
-    args.vec_store = vector_store_ok(c, ldc, FP8_OUT_BF16);
-    args.ksplit = fp8k::gemm_skinny_ksplit(M, N, K, d->sms);
-    CUtensorMap tmw, tmx;
-    if ((rc = encode_operand(&tmw, b, K, N, 128)) != FP8_OK) return rc;
-    if ((rc = encode_operand(&tmx, a, K, M, fp8k::gemm_skinny_rows(M))) != FP8_OK) return rc;
-    return to_status(fp8k::launch_gemm_skinny(sfmt == FP8_SCALE_F32 ? 0 : 1, tmw, tmx, args,
-                                              (cudaStream_t)stream));
+  DeviceState *d = nullptr;
+  if ((rc = device_state(&d)) != FP8_OK) return rc;
+  const cudaStream_t st = (cudaStream_t)stream;
+  if ((rc = clear_amax(ep, st)) != FP8_OK) return rc;
+  GemmArgs args = tensor_args(p);
+  args.err = d->err;
+  args.wait_limit_ns = g_wait_limit_ns;
+  args.ksplit = 1;
+  args.vec_store = vector_store_ok(args.c, args.ldc, args.out_dt);
+  CUtensorMap tma, tmb;
+  if ((rc = encode_gemm_operand(&tma, p.a, args.a_mn, p.K, p.M, 128)) != FP8_OK) return rc;
+  if ((rc = encode_gemm_operand(&tmb, p.b, args.b_mn, p.K, p.N, fp8k::gemm_pair_b_rows())) !=
+      FP8_OK)
+    return rc;
+  rc = to_status(fp8k::launch_gemm_pair_epilogue(tma, tmb, args, ep, true, d->sms, st));
+  if (rc != FP8_OK || e.dbias == nullptr) return rc;
+  return to_status(fp8k::launch_column_sum(ep.part, (p.M + 31) / 32, p.N, e.accumulate_dbias,
+                                           e.dbias, st));
+}
+
+int fp8_rmsnorm_quantize(const fp8_rmsnorm_t *norm, fp8_stream_t stream) {
+  const NvtxRange nvtx_range(__func__);
+  if (norm == nullptr) return FP8_ERR_INVALID_ARG;
+  const fp8_rmsnorm_t &n = *norm;
+  if (n.M < 0 || n.K < 1 || n.M >= kMaxDim || n.K >= kMaxDim) return FP8_ERR_INVALID_ARG;
+  if (!valid_in(n.dt) || !valid_in(n.w_dt) || !valid_fmt(n.fmt) || !(n.eps >= 0.0))
+    return FP8_ERR_INVALID_ARG;
+  if (n.mode != FP8_NORM_TENSOR && n.mode != FP8_NORM_GROUP && n.mode != FP8_NORM_MX)
+    return FP8_ERR_INVALID_ARG;
+  if (n.mode == FP8_NORM_GROUP && n.sfmt != FP8_SCALE_F32 && n.sfmt != FP8_SCALE_UE8M0)
+    return FP8_ERR_INVALID_ARG;
+  if (n.M > 0 && (n.x == nullptr || n.q == nullptr)) return FP8_ERR_INVALID_ARG;
+  if (n.mode == FP8_NORM_TENSOR) {
+    if (n.scale == nullptr || n.amax_out == n.scale) return FP8_ERR_INVALID_ARG;
+  } else {
+    if (n.amax_out != nullptr) return FP8_ERR_UNSUPPORTED;
+    if (n.M > 0 && n.scales == nullptr) return FP8_ERR_INVALID_ARG;
   }
-  if (mode == fp8k::kScaleGroupUe8m0 && M > 128) {
-    // Beyond one row tile: the UE8M0 scales become E8M0 words (four equal
-    // bytes per 128-wide K slice) that the block-scaled GEMM bulk-copies per
-    // stage, in place of the per-stage byte loads of the group mode.  Same
-    // products, same FP32 accumulation: the tensor core applies 2^e to each
-    // 1x32 sub-block of the group instead of the group as a whole.  (At
-    // K 7168, N 2048 the words measured equal at M = 64-128, slower at
-    // M = 16 (the conversion's launch) and faster from M = 256 on.)
-    DeviceState *d = nullptr;
-    if ((rc = device_state(&d)) != FP8_OK) return rc;
-    const size_t G = (size_t)(K / 128);
-    const size_t mpad = (size_t)(M + 127) / 128 * 128, npad = (size_t)(N + 127) / 128 * 128;
-    void *w = nullptr;
-    if ((rc = get_workspace((cudaStream_t)stream, G * (mpad + npad) * 4, &w, kWsWords)) != FP8_OK)
-      return rc;
-    uint32_t *la = static_cast<uint32_t *>(w), *lb = la + G * mpad;
-    if ((rc = to_status(fp8k::launch_ue8m0_words(static_cast<const uint8_t *>(sa),
-                                                 static_cast<const uint8_t *>(sb), M, N, K, la, lb,
-                                                 d->sms, (cudaStream_t)stream))) != FP8_OK)
-      return rc;
-    args.sa = la;
-    args.sb = lb;
-    args.ga = args.gb = nullptr;
-    return run_gemm(fp8k::kScaleMx, a, b, args, (cudaStream_t)stream);
+  if (n.K % (n.mode == FP8_NORM_MX ? 128 : 16) != 0) return FP8_ERR_MISALIGNED;
+  if (n.K > fp8k::kNormMaxK) return FP8_ERR_UNSUPPORTED;
+  int rc = check_rows(n.x, n.ld_x, n.K);
+  if (rc == FP8_OK) rc = check_rows(n.residual, n.ld_residual, n.K);
+  if (rc == FP8_OK) rc = check_rows(n.sum_out, n.ld_sum, n.K);
+  if (rc == FP8_OK) rc = check_rows(n.y_out, n.ld_y, n.K);
+  if (rc != FP8_OK) return rc;
+  const bool bytes = n.mode == FP8_NORM_GROUP && n.sfmt == FP8_SCALE_UE8M0;
+  if (!aligned16(n.w) || !aligned16(n.q) || !aligned_to(n.scales, bytes ? 1 : 4) ||
+      !aligned_to(n.inv_rms, 4) || !aligned_to(n.amax_out, 4) || !aligned_to(n.scale, 4))
+    return FP8_ERR_MISALIGNED;
+  DeviceState *d = nullptr;
+  if ((rc = device_state(&d)) != FP8_OK) return rc;
+  fp8k::NormArgs a{};
+  a.x = n.x; a.res = n.residual; a.w = n.w; a.sum = n.sum_out; a.y = n.y_out; a.q = n.q;
+  a.scale = n.scale; a.scales = n.scales; a.inv_rms = n.inv_rms;
+  a.amax = reinterpret_cast<uint32_t *>(n.amax_out);
+  a.M = n.M; a.K = n.K; a.ldx = n.ld_x; a.ldr = n.ld_residual; a.ld_sum = n.ld_sum; a.ld_y = n.ld_y;
+  a.eps = (float)n.eps; a.inv_k = (float)(1.0 / (double)n.K);
+  a.fmt = n.fmt; a.sfmt = n.sfmt; a.w_dt = n.w_dt;
+  return to_status(fp8k::launch_rmsnorm(a, n.dt, n.mode, d->sms, (cudaStream_t)stream));
+}
+
+int64_t fp8_rmsnorm_backward_workspace(int64_t M, int64_t K) {
+  if (M < 1 || K < 1 || K % 16 != 0 || K > fp8k::kNormMaxK) return 0;
+  return fp8k::rmsnorm_grad_blocks(M, K, kNormSms) * K * 4;
+}
+
+int fp8_rmsnorm_backward(const fp8_rmsnorm_grad_t *grad, fp8_stream_t stream) {
+  const NvtxRange nvtx_range(__func__);
+  if (grad == nullptr) return FP8_ERR_INVALID_ARG;
+  const fp8_rmsnorm_grad_t &n = *grad;
+  if (n.M < 0 || n.K < 1 || n.M >= kMaxDim || n.K >= kMaxDim) return FP8_ERR_INVALID_ARG;
+  if (!valid_in(n.dt) || !valid_in(n.dy_dt) || !valid_in(n.w_dt)) return FP8_ERR_INVALID_ARG;
+  if (n.M > 0 && (n.dy == nullptr || n.r == nullptr || n.inv_rms == nullptr || n.dx == nullptr))
+    return FP8_ERR_INVALID_ARG;
+  if (n.accumulate_dw != 0 && n.accumulate_dw != 1) return FP8_ERR_INVALID_ARG;
+  if (n.q != nullptr) {
+    if (n.scale == nullptr || n.amax_out == n.scale || !valid_fmt(n.fmt)) return FP8_ERR_INVALID_ARG;
+  } else if (n.amax_out != nullptr) {
+    return FP8_ERR_UNSUPPORTED;
   }
-  return run_gemm(mode, a, b, args, (cudaStream_t)stream);
+  if (n.K % 16 != 0) return FP8_ERR_MISALIGNED;
+  if (n.K > fp8k::kNormMaxK) return FP8_ERR_UNSUPPORTED;
+  int rc = check_rows(n.dy, n.ld_dy, n.K);
+  if (rc == FP8_OK) rc = check_rows(n.r, n.ld_r, n.K);
+  if (rc == FP8_OK) rc = check_rows(n.d_residual, n.ld_dres, n.K);
+  if (rc == FP8_OK) rc = check_rows(n.dx, n.ld_dx, n.K);
+  if (rc != FP8_OK) return rc;
+  if (n.dw != nullptr && n.M > 0 &&
+      (n.workspace == nullptr || n.workspace_bytes < fp8_rmsnorm_backward_workspace(n.M, n.K)))
+    return FP8_ERR_INVALID_ARG;
+  if (!aligned16(n.w) || !aligned16(n.q) || !aligned16(n.workspace) || !aligned_to(n.dw, 4) ||
+      !aligned_to(n.inv_rms, 4) || !aligned_to(n.amax_out, 4) || !aligned_to(n.scale, 4))
+    return FP8_ERR_MISALIGNED;
+  DeviceState *d = nullptr;
+  if ((rc = device_state(&d)) != FP8_OK) return rc;
+  fp8k::NormGradArgs a{};
+  a.dy = n.dy; a.r = n.r; a.w = n.w; a.dres = n.d_residual; a.inv_rms = n.inv_rms; a.dx = n.dx;
+  a.parts = n.dw != nullptr ? static_cast<float *>(n.workspace) : nullptr;
+  a.q = n.q; a.scale = n.scale; a.amax = reinterpret_cast<uint32_t *>(n.amax_out);
+  a.M = n.M; a.K = n.K; a.ld_dy = n.ld_dy; a.ld_r = n.ld_r; a.ld_dres = n.ld_dres; a.ld_dx = n.ld_dx;
+  a.inv_k = (float)(1.0 / (double)n.K);
+  a.fmt = n.fmt; a.w_dt = n.w_dt;
+  return to_status(fp8k::launch_rmsnorm_grad(a, n.dt, n.dy_dt, n.dw, n.accumulate_dw,
+                                             d->sms < kNormSms ? d->sms : kNormSms,
+                                             (cudaStream_t)stream));
 }
 
 int fp8_gemm_group_experts(const uint8_t *a, const void *sa, const uint8_t *b, const void *sb,

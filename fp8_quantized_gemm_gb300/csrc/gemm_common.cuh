@@ -204,17 +204,18 @@ __device__ __forceinline__ float4 ld_shared_cluster_f4(uint32_t addr) {
 // The reduction of a split cluster: CTA `rank` of the `ks` CTAs sums rows
 // [rank * R / ks, (rank + 1) * R / ks) of the tile (R its valid rows) over
 // every CTA's partial tile, in split order (the same order, hence the same
-// sums, as the global-workspace reduction), scales by alpha and stores.
+// sums, as the global-workspace reduction), scales by alpha and hands up to
+// four columns at a time to put(row, col, n, values).
 // Every thread of the CTA takes part: thread t owns float4 column t % (BN/4)
 // and rows t / (BN/4), + nthr / (BN/4), ...; each step issues the remote
 // loads of kStep rows of all KS splits (about 16 in flight per thread)
 // before summing any, since a distributed-shared-memory load has a long
 // latency.
-template <int BN, int KS>
+template <int BN, int KS, typename Put>
 __device__ __forceinline__ void cluster_reduce_ks(const GemmArgs &a, uint32_t base, int64_t m0,
                                                   int64_t n0, int64_t r0, int64_t r1,
                                                   int64_t cols, float alpha, uint32_t rank,
-                                                  int tid, int nthr) {
+                                                  int tid, int nthr, Put &put) {
   constexpr int kCg = BN / 4;
   constexpr int kStep = KS >= 16 ? 1 : 16 / KS;
   const int rstride = nthr / kCg;
@@ -246,16 +247,16 @@ __device__ __forceinline__ void cluster_reduce_ks(const GemmArgs &a, uint32_t ba
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[i] *= alpha;
-        store4(a, m0 + r, n0 + c, n, acc);
+        put(m0 + r, n0 + c, n, acc);
       }
     }
   }
 }
 
-template <int BN>
+template <int BN, typename Put>
 __device__ __forceinline__ void cluster_reduce(const GemmArgs &a, const float *part, int64_t m0,
                                                int64_t n0, int64_t tile_rows, float alpha,
-                                               uint32_t rank, int ks, int tid, int nthr) {
+                                               uint32_t rank, int ks, int tid, int nthr, Put put) {
   const int64_t rows = a.M - m0 < tile_rows ? a.M - m0 : tile_rows;
   const int64_t cols = a.N - n0 < BN ? a.N - n0 : BN;
   if (rows <= 0 || cols <= 0) return;
@@ -263,13 +264,13 @@ __device__ __forceinline__ void cluster_reduce(const GemmArgs &a, const float *p
   const uint32_t base = smem_u32(part);
   static_assert(kMaxClusterSplit == 8, "split counts below");
   switch (ks) {
-    case 2: cluster_reduce_ks<BN, 2>(a, base, m0, n0, r0, r1, cols, alpha, rank, tid, nthr); break;
-    case 3: cluster_reduce_ks<BN, 3>(a, base, m0, n0, r0, r1, cols, alpha, rank, tid, nthr); break;
-    case 4: cluster_reduce_ks<BN, 4>(a, base, m0, n0, r0, r1, cols, alpha, rank, tid, nthr); break;
-    case 5: cluster_reduce_ks<BN, 5>(a, base, m0, n0, r0, r1, cols, alpha, rank, tid, nthr); break;
-    case 6: cluster_reduce_ks<BN, 6>(a, base, m0, n0, r0, r1, cols, alpha, rank, tid, nthr); break;
-    case 7: cluster_reduce_ks<BN, 7>(a, base, m0, n0, r0, r1, cols, alpha, rank, tid, nthr); break;
-    default: cluster_reduce_ks<BN, 8>(a, base, m0, n0, r0, r1, cols, alpha, rank, tid, nthr); break;
+    case 2: cluster_reduce_ks<BN, 2>(a, base, m0, n0, r0, r1, cols, alpha, rank, tid, nthr, put); break;
+    case 3: cluster_reduce_ks<BN, 3>(a, base, m0, n0, r0, r1, cols, alpha, rank, tid, nthr, put); break;
+    case 4: cluster_reduce_ks<BN, 4>(a, base, m0, n0, r0, r1, cols, alpha, rank, tid, nthr, put); break;
+    case 5: cluster_reduce_ks<BN, 5>(a, base, m0, n0, r0, r1, cols, alpha, rank, tid, nthr, put); break;
+    case 6: cluster_reduce_ks<BN, 6>(a, base, m0, n0, r0, r1, cols, alpha, rank, tid, nthr, put); break;
+    case 7: cluster_reduce_ks<BN, 7>(a, base, m0, n0, r0, r1, cols, alpha, rank, tid, nthr, put); break;
+    default: cluster_reduce_ks<BN, 8>(a, base, m0, n0, r0, r1, cols, alpha, rank, tid, nthr, put); break;
   }
 }
 

@@ -46,6 +46,7 @@
 #include "elementwise.cuh"
 #include "gemm_common.cuh"
 #include "kernels.h"
+#include "linear_epilogue.cuh"
 #include "quant_common.cuh"
 
 namespace fp8k {
@@ -55,10 +56,12 @@ namespace fp8k {
 // PairGroup::band_rows.
 constexpr int64_t kPairBandRows = 8;
 
-template <int BN, int STAGES>
+// EW: epilogue warps, EW / 4 per TMEM lane quadrant, each with 4 BN / EW of the
+// tile's columns.
+template <int BN, int STAGES, int EW>
 struct PairCfg {
   static constexpr int BM = 128, BK = 128;  // rows per CTA (256 per pair)
-  static constexpr int kEpiWarps = 4;
+  static constexpr int kEpiWarps = EW;
   static constexpr int kThreads = 64 + 32 * kEpiWarps;
   static constexpr uint32_t kABytes = BM * BK;
   static constexpr uint32_t kBBytes = (BN / 2) * BK;
@@ -69,7 +72,7 @@ struct PairCfg {
   static constexpr int kNumBars = 2 * STAGES + 2 * kAccBufs + 1;
   // TMA-store staging: per epilogue warp two 32-row x 128-byte boxes
   static constexpr uint32_t kOutBox = 32 * 128;
-  static constexpr uint32_t kOutBytes = kEpiWarps * 2 * kOutBox;
+  static constexpr uint32_t kOutBytes = EW == 4 ? kEpiWarps * 2 * kOutBox : 0;  // EW 8: linear epilogues
   static constexpr uint32_t kSmem = 1024 + kTileBytes + kOutBytes + 8 * kNumBars + 16;
   static_assert(kTmemCols <= 512, "TMEM budget");
   static_assert(kSmem <= 227 * 1024, "shared-memory budget");
@@ -219,10 +222,13 @@ __device__ __forceinline__ void gated_row32(const GemmArgs &a, int64_t row, int6
   qd[1] = make_uint4(c[2].x, c[2].y, c[3].x, c[3].y);
 }
 
-template <int BN, int STAGES>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<BN, STAGES>::kThreads, 1)
-    gemm_pair_kernel(const __grid_constant__ PairGroup grp) {
-  using C = PairCfg<BN, STAGES>;
+// LINEAR 0: the group's problems with their own epilogues.  1, 2: one problem
+// with the linear layer's epilogue (linear_epilogue.cuh), forward or gradient.
+template <int BN, int STAGES, int EW, int LINEAR>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<BN, STAGES, EW>::kThreads, 1)
+    gemm_pair_kernel(const __grid_constant__ PairGroup grp, const EpParam<LINEAR != 0> epp) {
+  using C = PairCfg<BN, STAGES, EW>;
+  static_assert(LINEAR != 0 || EW == 4, "the group epilogues take whole rows of the tile");
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -390,6 +396,50 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<BN, STAGES>:
       }
     }
     __syncwarp();
+  } else if constexpr (LINEAR != 0) {
+    // ----------------------------------------- linear layer's epilogue (both)
+    constexpr bool kGrad = LINEAR == 2;
+    constexpr int kCols = 4 * BN / EW;
+    const uint32_t q = warp & 3u;
+    const int64_t col0 = (int64_t)((warp - 2) >> 2) * kCols;
+    const uint32_t lane_base = tmem + ((32u * q) << 16) + (uint32_t)col0;
+    const uint32_t acce_leader0 = mapa_shared(acce_bar(0), 0);
+    const GemmArgs &a = grp.args[0];
+    const LinearEp &e = epp.e;
+    const float alpha = *static_cast<const float *>(a.sa) * *static_cast<const float *>(a.sb);
+    const ScaleDiv d = epilogue_scale(e);
+    uint32_t key = 0, j = 0;
+    for (int64_t gt = pair; gt < num_tiles; gt += npairs, ++j) {
+      const TileRef tr = tile_ref(gt);
+      const int64_t row0 = tr.m0 + rank * C::BM + 32 * q, n0 = tr.n0 + col0;
+      const uint32_t buf = j & 1u, use = j >> 1;
+      RowIn in;
+      fetch_row32<kGrad>(a, e, row0 + lane, n0, in);
+      if (!mbar_wait_warp(accf_bar(buf), use & 1u, abort_flag, err, 3)) break;
+      tc_fence_after();
+#pragma unroll 1
+      for (int c = 0; c < kCols; c += 32) {
+        uint32_t r[32];
+        FP8K_TMEM_LD_X32(lane_base + buf * BN + (uint32_t)c, r);
+        const RowIn cur = in;
+        if (c + 32 < kCols) fetch_row32<kGrad>(a, e, row0 + lane, n0 + c + 32, in);
+        tmem_ld_wait();
+        if (c + 32 == kCols) {  // this warp's columns are read out
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster_relaxed(acce_leader0 + 8u * buf);
+        }
+        float v[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]) * alpha;
+        if constexpr (kGrad)
+          grad_row32(a, e, row0, n0 + c, v, cur, d, key);
+        else
+          linear_row32(a, e, row0 + lane, n0 + c, v, cur, d, key);
+      }
+    }
+    __syncwarp();
+    flush_amax(e, key);
   } else {
     // ------------------------------------------------------ epilogue (both)
     const uint32_t q = warp & 3u;
@@ -597,9 +647,9 @@ int64_t gemm_pair_tiles_of(const GemmArgs &a) {
 cudaError_t launch_gemm_pair_group(const CUtensorMap *tma, const CUtensorMap *tmb,
                                    const CUtensorMap *tmc, const CUtensorMap *tmb2,
                                    const GemmArgs *args, int count, int sms, cudaStream_t st) {
-  using C = PairCfg<kPairBN, kPairStages>;
+  using C = PairCfg<kPairBN, kPairStages, 4>;
   if (count < 1 || count > kMaxGroup) return cudaErrorInvalidValue;
-  auto kern = gemm_pair_kernel<kPairBN, kPairStages>;
+  auto kern = gemm_pair_kernel<kPairBN, kPairStages, 4, 0>;
   static bool attr_done[64] = {};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -631,8 +681,42 @@ cudaError_t launch_gemm_pair_group(const CUtensorMap *tma, const CUtensorMap *tm
   for (int i = count; i < kMaxGroup; ++i) g.tile_begin[i + 1] = g.tile_begin[count];
   const int64_t tiles = g.tile_begin[count];
   const int64_t pairs = tiles < sms / 2 ? tiles : sms / 2;
-  kern<<<(unsigned)(2 * pairs), C::kThreads, C::kSmem, st>>>(g);
+  kern<<<(unsigned)(2 * pairs), C::kThreads, C::kSmem, st>>>(g, EpParam<false>{});
   return cudaGetLastError();
+}
+
+template <int LINEAR>
+static cudaError_t run_pair_epilogue(const PairGroup &g, const LinearEp &ep, int sms,
+                                     cudaStream_t st) {
+  using C = PairCfg<kPairBN, kPairStages, 8>;
+  auto kern = gemm_pair_kernel<kPairBN, kPairStages, 8, LINEAR>;
+  static bool attr_done[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!attr_done[dev]) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
+    if (e != cudaSuccess) return e;
+    attr_done[dev] = true;
+  }
+  const int64_t tiles = g.tile_begin[g.count];
+  const int64_t pairs = tiles < sms / 2 ? tiles : sms / 2;
+  kern<<<(unsigned)(2 * pairs), C::kThreads, C::kSmem, st>>>(g, EpParam<true>{ep});
+  return cudaGetLastError();
+}
+
+cudaError_t launch_gemm_pair_epilogue(const CUtensorMap &tma, const CUtensorMap &tmb,
+                                      const GemmArgs &args, const LinearEp &ep, bool grad,
+                                      int sms, cudaStream_t st) {
+  PairGroup g{};
+  g.count = 1;
+  g.band_rows = gemm_pair_band_rows();
+  g.tma[0] = tma;
+  g.tmb[0] = tmb;
+  g.args[0] = args;
+  for (int i = 1; i <= kMaxGroup; ++i) g.tile_begin[i] = gemm_pair_tiles_of(args);
+  return grad ? run_pair_epilogue<2>(g, ep, sms, st) : run_pair_epilogue<1>(g, ep, sms, st);
 }
 
 cudaError_t launch_gemm_pair(const CUtensorMap &tma, const CUtensorMap &tmb,

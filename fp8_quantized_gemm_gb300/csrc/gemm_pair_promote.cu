@@ -30,6 +30,7 @@
 #include "expert_tiles.cuh"
 #include "gemm_common.cuh"
 #include "kernels.h"
+#include "linear_epilogue.cuh"
 
 namespace fp8k {
 
@@ -64,10 +65,11 @@ struct PromoteCfg {
   static_assert(128 % kCols == 0 && BN % kCols == 0, "one 128-column B block of scales per warp");
 };
 
-template <int BN, int STAGES, int EPI, bool EXPERTS>
+template <int BN, int STAGES, int EPI, bool EXPERTS, bool LINEAR>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PromoteCfg<BN, STAGES, EPI>::kThreads, 1)
     gemm_pair_promote_kernel(const __grid_constant__ CUtensorMap tma,
-                             const __grid_constant__ CUtensorMap tmb, const GemmArgs args) {
+                             const __grid_constant__ CUtensorMap tmb, const GemmArgs args,
+                             const EpParam<LINEAR> epp) {
   using C = PromoteCfg<BN, STAGES, EPI>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(
@@ -320,7 +322,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PromoteCfg<BN, STAGE
 #pragma unroll
         for (int i = 0; i < 32; ++i) v[i] = acc[32 * c + i];
         // (store_row32 itself skips rows past M; expert rows end earlier)
-        if (!EXPERTS || orow < to.row_end) store_row32(args, orow, to.n0 + col0 + 32 * c, v);
+        if constexpr (LINEAR) {
+          // (no operand fetched a chunk ahead: the accumulators hold the registers)
+          RowIn in;
+          fetch_row32<false>(args, epp.e, orow, to.n0 + col0 + 32 * c, in);
+          uint32_t key = 0;  // no codes here
+          linear_row32(args, epp.e, orow, to.n0 + col0 + 32 * c, v, in, ScaleDiv(1.0f), key);
+        } else {
+          if (!EXPERTS || orow < to.row_end) store_row32(args, orow, to.n0 + col0 + 32 * c, v);
+        }
       }
     }
   }
@@ -365,11 +375,12 @@ bool gemm_pair_promote_eligible(int64_t M, int64_t N, int64_t K, int sms) {
   return tiles >= sms / 4;
 }
 
-template <bool EXPERTS>
+template <bool EXPERTS, bool LINEAR>
 static cudaError_t run_pair_promote(const CUtensorMap &tma, const CUtensorMap &tmb,
-                                    const GemmArgs &args, int sms, cudaStream_t st) {
+                                    const GemmArgs &args, const EpParam<LINEAR> &epp, int sms,
+                                    cudaStream_t st) {
   using C = PromoteC;
-  auto kern = gemm_pair_promote_kernel<kPromoteBN, kPromoteStages, kPromoteEpiWarps, EXPERTS>;
+  auto kern = gemm_pair_promote_kernel<kPromoteBN, kPromoteStages, kPromoteEpiWarps, EXPERTS, LINEAR>;
   static bool attr_done[64] = {};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -385,18 +396,21 @@ static cudaError_t run_pair_promote(const CUtensorMap &tma, const CUtensorMap &t
   const int64_t row_tiles = (args.M + 255) / 256 + (EXPERTS ? args.experts : 0);
   const int64_t tiles = row_tiles * ((args.N + C::BN - 1) / C::BN);
   const int64_t pairs = tiles < sms / 2 ? tiles : sms / 2;
-  kern<<<(unsigned)(2 * pairs), C::kThreads, C::kSmem, st>>>(tma, tmb, args);
+  kern<<<(unsigned)(2 * pairs), C::kThreads, C::kSmem, st>>>(tma, tmb, args, epp);
   return cudaGetLastError();
 }
 
 cudaError_t launch_gemm_pair_promote(const CUtensorMap &tma, const CUtensorMap &tmb,
-                                     const GemmArgs &args, int sms, cudaStream_t st) {
+                                     const GemmArgs &args, int sms, cudaStream_t st,
+                                     const LinearEp *ep) {
   if (args.K % 128 != 0 || args.a_mn || args.b_mn || args.ksplit != 1) return cudaErrorInvalidValue;
   if (args.experts > 0) {
     if (args.experts > kMaxExperts || args.offsets == nullptr) return cudaErrorInvalidValue;
-    return run_pair_promote<true>(tma, tmb, args, sms, st);
+    if (ep != nullptr) return cudaErrorInvalidValue;
+    return run_pair_promote<true>(tma, tmb, args, EpParam<false>{}, sms, st);
   }
-  return run_pair_promote<false>(tma, tmb, args, sms, st);
+  if (ep != nullptr) return run_pair_promote<false>(tma, tmb, args, EpParam<true>{*ep}, sms, st);
+  return run_pair_promote<false>(tma, tmb, args, EpParam<false>{}, sms, st);
 }
 
 }  // namespace fp8k

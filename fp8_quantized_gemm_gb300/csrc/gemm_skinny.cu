@@ -52,6 +52,7 @@
 #include "common.cuh"
 #include "gemm_common.cuh"
 #include "kernels.h"
+#include "linear_epilogue.cuh"
 
 namespace fp8k {
 
@@ -102,10 +103,19 @@ __device__ __forceinline__ float skinny_scale_value(uint32_t raw) {
     return exp2_int((int)raw - 127);
 }
 
-template <int SFMT, int MP>
+// One finished result z (scaled, with its bias).
+template <bool EPI>
+__device__ __forceinline__ void put_skinny(const GemmArgs &a, const EpParam<EPI> &epp, int64_t m,
+                                           int64_t n, float z) {
+  if constexpr (EPI) z = linear_value(epp.e, m, n, z);
+  static_cast<__nv_bfloat16 *>(a.c)[m * a.ldc + n] = __float2bfloat16_rn(z);
+}
+
+template <int SFMT, int MP, bool EPI>
 __global__ void __launch_bounds__(SkinnyCfg<MP>::kThreads, 1)
     gemm_skinny_kernel(const __grid_constant__ CUtensorMap tmw,
-                       const __grid_constant__ CUtensorMap tmx, const GemmArgs args) {
+                       const __grid_constant__ CUtensorMap tmx, const GemmArgs args,
+                       const EpParam<EPI> epp) {
   using C = SkinnyCfg<MP>;
   const uint32_t warp = threadIdx.x >> 5;
   const uint32_t lane = lane_id();
@@ -291,11 +301,10 @@ __global__ void __launch_bounds__(SkinnyCfg<MP>::kThreads, 1)
       const int64_t n = n0 + nl;
       if (ok && n < args.N) {
         const float bn = args.bias != nullptr ? __ldg(args.bias + n) : 0.0f;
-        __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(args.c) + mb * args.ldc;
 #pragma unroll
         for (int c = 0; c < C::kCols; ++c) {
           const int64_t m = mcol0 + c;
-          if (m < Mh) out[m * args.ldc + n] = __float2bfloat16_rn(acc[c] + bn);
+          if (m < Mh) put_skinny(args, epp, mb + m, n, acc[c] + bn);
         }
       }
     } else {
@@ -320,7 +329,6 @@ __global__ void __launch_bounds__(SkinnyCfg<MP>::kThreads, 1)
     // (consecutive output columns), warps groups of four activation rows
     const int rows = (int)Mh;
     const int own = 128 - (int)rank * W < W ? 128 - (int)rank * W : W;
-    __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(args.c) + mb * args.ldc;
     for (int m4 = (int)warp * 4; m4 < rows; m4 += C::kThreads / 32 * 4) {
       for (int j = (int)lane; j < own; j += 32) {
         const int64_t n = n0 + (int64_t)rank * W + j;
@@ -335,7 +343,7 @@ __global__ void __launch_bounds__(SkinnyCfg<MP>::kThreads, 1)
           const float r[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            if (m4 + i < rows) out[(int64_t)(m4 + i) * args.ldc + n] = __float2bfloat16_rn(r[i] + bn);
+            if (m4 + i < rows) put_skinny(args, epp, mb + m4 + i, n, r[i] + bn);
         }
       }
     }
@@ -357,12 +365,12 @@ int gemm_skinny_rows(int64_t M) {
 
 static int64_t skinny_halves(int64_t M) { return M > 64 ? (M + 63) / 64 : 1; }
 
-template <int SFMT, int MP>
+template <int SFMT, int MP, bool EPI>
 static cudaError_t skinny_attr(int dev) {
   static bool done[64] = {};
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (done[dev]) return cudaSuccess;
-  const cudaError_t e = cudaFuncSetAttribute(gemm_skinny_kernel<SFMT, MP>,
+  const cudaError_t e = cudaFuncSetAttribute(gemm_skinny_kernel<SFMT, MP, EPI>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              (int)SkinnyCfg<MP>::kSmem);
   if (e == cudaSuccess) done[dev] = true;
@@ -375,7 +383,7 @@ template <int MP>
 static int skinny_active_clusters(int size) {
   using C = SkinnyCfg<MP>;
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || skinny_attr<0, MP>(dev) != cudaSuccess) return 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || skinny_attr<0, MP, false>(dev) != cudaSuccess) return 0;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -388,7 +396,7 @@ static int skinny_active_clusters(int size) {
   cfg.blockDim = dim3(C::kThreads);
   cfg.dynamicSmemBytes = C::kSmem;
   int n = 0;
-  return cudaOccupancyMaxActiveClusters(&n, gemm_skinny_kernel<0, MP>, &cfg) == cudaSuccess ? n
+  return cudaOccupancyMaxActiveClusters(&n, gemm_skinny_kernel<0, MP, false>, &cfg) == cudaSuccess ? n
                                                                                           : 0;
 }
 
@@ -423,14 +431,14 @@ int gemm_skinny_ksplit(int64_t M, int64_t N, int64_t K, int sms) {
   return ks;
 }
 
-template <int SFMT, int MP>
+template <int SFMT, int MP, bool EPI>
 static cudaError_t run_skinny(const CUtensorMap &tmw, const CUtensorMap &tmx, const GemmArgs &args,
-                              cudaStream_t st) {
+                              const EpParam<EPI> &epp, cudaStream_t st) {
   using C = SkinnyCfg<MP>;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if ((e = skinny_attr<SFMT, MP>(dev)) != cudaSuccess) return e;
+  if ((e = skinny_attr<SFMT, MP, EPI>(dev)) != cudaSuccess) return e;
   const int ks = args.ksplit;
   if (ks < 1 || ks > kMaxClusterSplit || ks > args.K / 128)
     return cudaErrorInvalidValue;
@@ -449,22 +457,30 @@ static cudaError_t run_skinny(const CUtensorMap &tmw, const CUtensorMap &tmx, co
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = ks > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, gemm_skinny_kernel<SFMT, MP>, tmw, tmx, args);
+  return cudaLaunchKernelEx(&cfg, gemm_skinny_kernel<SFMT, MP, EPI>, tmw, tmx, args, epp);
+}
+
+template <int SFMT, bool EPI>
+static cudaError_t skinny_rows(const CUtensorMap &tmw, const CUtensorMap &tmx,
+                               const GemmArgs &args, const EpParam<EPI> &epp, cudaStream_t st) {
+  switch (gemm_skinny_rows(args.M)) {
+    case 16: return run_skinny<SFMT, 16, EPI>(tmw, tmx, args, epp, st);
+    case 32: return run_skinny<SFMT, 32, EPI>(tmw, tmx, args, epp, st);
+    default: return run_skinny<SFMT, 64, EPI>(tmw, tmx, args, epp, st);
+  }
 }
 
 cudaError_t launch_gemm_skinny(int sfmt, const CUtensorMap &tmw, const CUtensorMap &tmx,
-                               const GemmArgs &args, cudaStream_t st) {
-  const int mp = gemm_skinny_rows(args.M);
-  if (mp == 0 || args.K % 128 != 0 || args.out_dt != 1 || args.accumulate != 0)
+                               const GemmArgs &args, cudaStream_t st, const LinearEp *ep) {
+  if (gemm_skinny_rows(args.M) == 0 || args.K % 128 != 0 || args.out_dt != 1 ||
+      args.accumulate != 0)
     return cudaErrorInvalidValue;
-  switch (mp) {
-    case 16:
-      return sfmt == 0 ? run_skinny<0, 16>(tmw, tmx, args, st) : run_skinny<1, 16>(tmw, tmx, args, st);
-    case 32:
-      return sfmt == 0 ? run_skinny<0, 32>(tmw, tmx, args, st) : run_skinny<1, 32>(tmw, tmx, args, st);
-    default:
-      return sfmt == 0 ? run_skinny<0, 64>(tmw, tmx, args, st) : run_skinny<1, 64>(tmw, tmx, args, st);
+  if (ep != nullptr) {
+    const EpParam<true> p{*ep};
+    return sfmt == 0 ? skinny_rows<0>(tmw, tmx, args, p, st) : skinny_rows<1>(tmw, tmx, args, p, st);
   }
+  const EpParam<false> p{};
+  return sfmt == 0 ? skinny_rows<0>(tmw, tmx, args, p, st) : skinny_rows<1>(tmw, tmx, args, p, st);
 }
 
 }  // namespace fp8k

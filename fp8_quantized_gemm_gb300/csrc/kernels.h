@@ -167,6 +167,22 @@ struct GemmArgs {
 };
 constexpr int kMaxExperts = 256;
 
+// The linear layer's epilogue (linear_epilogue.cuh), beside GemmArgs::bias
+// and GemmArgs::c (nullable with codes).
+struct LinearEp {
+  int act;                  // Act (activation.cuh)
+  const void *res;          // nullable, [M, ld_res]; forward only
+  int res_dt;               // 0 = f32, 1 = bf16
+  void *pre;                // bf16 [M, ld_pre]: written (forward, nullable) or read (gradient)
+  uint8_t *q;               // nullable codes [M, N]
+  int q_fmt;
+  const float *q_scale;
+  uint32_t *q_amax;         // nullable (cleared by the caller)
+  float *part;              // nullable, gradient only: [ceil(M / 32)][N] column sums
+  int64_t ld_res, ld_pre;
+  int res_vec, pre_vec, q_vec;  // 1: base and pitch allow 16-byte access
+};
+
 // Wait bound the API passes to kernels (fp8_set_option FP8_OPT_WAIT_LIMIT_NS).
 uint64_t wait_limit_ns();
 
@@ -188,10 +204,16 @@ constexpr int64_t kSkinnyMaxRows = 128;
 int gemm_skinny_rows(int64_t M);
 int gemm_skinny_ksplit(int64_t M, int64_t N, int64_t K, int sms);
 cudaError_t launch_gemm_skinny(int sfmt, const CUtensorMap &tmw, const CUtensorMap &tmx,
-                               const GemmArgs &args, cudaStream_t st);
+                               const GemmArgs &args, cudaStream_t st,
+                               const LinearEp *ep = nullptr);
 
 cudaError_t launch_gemm(int mode, const CUtensorMap &tma, const CUtensorMap &tmb,
                         const GemmArgs &args, int sms, cudaStream_t st);
+// The same with the linear layer's epilogue (gemm_epilogue.cu): per-tensor
+// scales, FP32 group scales, or block-scale words.
+cudaError_t launch_gemm_epilogue(int mode, const CUtensorMap &tma, const CUtensorMap &tmb,
+                                 const GemmArgs &args, const LinearEp &ep, int sms,
+                                 cudaStream_t st);
 // Expert-grouped per-K-group GEMM (args.experts > 0) with B tiles `bn` wide.
 cudaError_t launch_gemm_experts(int mode, int bn, const CUtensorMap &tma, const CUtensorMap &tmb,
                                 const GemmArgs &args, int sms, cudaStream_t st);
@@ -210,6 +232,11 @@ cudaError_t launch_gemm_pair_group(const CUtensorMap *tma, const CUtensorMap *tm
 int gemm_pair_b_rows();
 // 256-row tiles per band of the CTA-pair tile order (fp8_set_option).
 int64_t gemm_pair_band_rows();
+// One per-tensor problem with the linear layer's epilogue, forward or
+// (grad) through the activation's derivative.
+cudaError_t launch_gemm_pair_epilogue(const CUtensorMap &tma, const CUtensorMap &tmb,
+                                      const GemmArgs &args, const LinearEp &ep, bool grad,
+                                      int sms, cudaStream_t st);
 cudaError_t launch_gemm_pair(const CUtensorMap &tma, const CUtensorMap &tmb,
                              const CUtensorMap &tmc, const GemmArgs &args, int sms,
                              cudaStream_t st);
@@ -223,6 +250,7 @@ cudaError_t launch_gemm_pair(const CUtensorMap &tma, const CUtensorMap &tmb,
 bool gemm_pair_promote_eligible(int64_t M, int64_t N, int64_t K, int sms);
 int gemm_pair_promote_b_rows();
 cudaError_t launch_gemm_pair_promote(const CUtensorMap &tma, const CUtensorMap &tmb,
-                                     const GemmArgs &args, int sms, cudaStream_t st);
+                                     const GemmArgs &args, int sms, cudaStream_t st,
+                                     const LinearEp *ep = nullptr);
 
 }  // namespace fp8k

@@ -498,6 +498,191 @@ FP8_API int fp8_gemm_mx(const uint8_t *a, const uint32_t *la, const float *ga, c
                 const uint32_t *lb, const float *gb, int64_t M, int64_t N, int64_t K,
                 int out_dt, void *c, int64_t ldc, fp8_stream_t stream);
 
+/* ------------------------------------------ linear layer's epilogue --
+ * The products of a transformer block with what follows them folded into the
+ * GEMM's epilogue, so that the fp32 results never reach memory.  Not
+ * described on the pages (support arithmetic around their GEMMs); plain
+ * definitions, formed in fp32 and rounded once per stored copy:
+ *
+ *   z = result + bias[n]       result: the GEMM's scaled sum
+ *   pre <- bf16(z)
+ *   y = act(z) + residual[m,n]
+ *   c <- y (bf16 or fp32)      q <- codes of y / q_scale (clipped, RNE)
+ *   q_amax <- max |y|
+ *
+ *   FP8_ACT_RELU max(z, 0); RELU2 max(z, 0)^2; SILU z / (1 + e^-z);
+ *   GELU z Phi(z); GELU_TANH z (1 + tanh(sqrt(2/pi)(z + 0.044715 z^3))) / 2.
+ *
+ * residual  nullable [M, ld_residual] of residual_dt (fp8_out_dtype_t); may
+ *           be c itself (same type and pitch).
+ * pre       nullable bf16 [M, ld_pre]: the activation's argument, which
+ *           fp8_gemm_tensor_act_backward reads.
+ * q         nullable codes [M, N] of q_fmt under the scale q_scale[0] fixed
+ *           before the call (delayed scaling, [Flax] 2.3); q_amax (nullable;
+ *           cleared by the call) must not alias q_scale.
+ * c may be null when q is given.  Rows are aligned to their element size;
+ * 16-byte aligned bases and pitches (and N % 16 == 0 for q) take the vector
+ * paths.
+ */
+typedef enum {
+  FP8_ACT_NONE = 0,
+  FP8_ACT_RELU = 1,
+  FP8_ACT_RELU2 = 2,
+  FP8_ACT_SILU = 3,
+  FP8_ACT_GELU_TANH = 4,
+  FP8_ACT_GELU = 5
+} fp8_act_t;
+
+typedef struct {
+  int act; /* fp8_act_t */
+  const void *residual;
+  int residual_dt;
+  int64_t ld_residual;
+  void *pre;
+  int64_t ld_pre;
+  uint8_t *q;
+  int q_fmt;
+  const float *q_scale;
+  float *q_amax;
+} fp8_linear_epilogue_t;
+
+/* fp8_gemm_tensor_epilogue: one per-tensor problem (layouts, formats, bias as
+ * in fp8_gemm_problem_t; accumulate 0, no adamw / swiglu) with the epilogue.
+ * Both descriptors are HOST pointers, read during the call only. */
+FP8_API int fp8_gemm_tensor_epilogue(const fp8_gemm_problem_t *problem,
+                                     const fp8_linear_epilogue_t *epilogue, fp8_stream_t stream);
+
+/* fp8_gemm_group_epilogue: fp8_gemm_group_bias with the epilogue; bf16 c
+ * (required), no codes (q null, else FP8_ERR_UNSUPPORTED: the next product's
+ * 1x128 scales depend on the whole group).  1-128 rows always run the few-row
+ * kernel. */
+FP8_API int fp8_gemm_group_epilogue(const uint8_t *a, const void *sa, const uint8_t *b,
+                                    const void *sb, int sfmt, int64_t M, int64_t N, int64_t K,
+                                    const float *bias, const fp8_linear_epilogue_t *epilogue,
+                                    void *c, int64_t ldc, fp8_stream_t stream);
+
+/* fp8_gemm_tensor_act_backward: the data gradient of the next product taken
+ * through the activation, in the GEMM's epilogue:
+ *   dz = result * act'(pre)     result: sa sb A B^T of the problem, e.g. the
+ *                               codes of dy [M, K] times those of W [K, N]
+ *                               (b_layout FP8_MN_MAJOR)
+ *   c <- dz (nullable with q)   q, q_amax as above (E5M2 for gradients)
+ *   dbias[n] (+)= sum_m dz[m,n] in fp32, in a fixed order (no atomics)
+ *   act        as above; the derivative is taken at the stored bf16 pre
+ *              (relu and relu2: slope 0 at z = 0).
+ *   dbias      nullable device fp32 [N]; accumulate_dbias 1 adds to it.
+ *   workspace  device scratch for dbias, 16-byte aligned, of at least
+ *              fp8_act_backward_workspace(M, N) bytes; calls that can run at
+ *              the same time need distinct scratch.
+ * The problem has no bias, accumulate 0, no adamw / swiglu.  Runs on CTA pairs
+ * whatever the shape. */
+typedef struct {
+  int act;
+  const void *pre; /* bf16 [M, ld_pre] */
+  int64_t ld_pre;
+  uint8_t *q;
+  int q_fmt;
+  const float *q_scale;
+  float *q_amax;
+  float *dbias;
+  int accumulate_dbias;
+  void *workspace;
+  int64_t workspace_bytes;
+} fp8_act_grad_epilogue_t;
+FP8_API int64_t fp8_act_backward_workspace(int64_t M, int64_t N);
+FP8_API int fp8_gemm_tensor_act_backward(const fp8_gemm_problem_t *problem,
+                                         const fp8_act_grad_epilogue_t *epilogue,
+                                         fp8_stream_t stream);
+
+/* -------------------------------------------------- RMS norm, FP8 output --
+ * fp8_rmsnorm_quantize: the norm ahead of an FP8 product, with the residual's
+ * addition (support arithmetic, not on the pages).  Per row:
+ *   r = x + residual, rounded to the stream's type dt;  sum_out <- r
+ *   inv = 1 / sqrt(mean(r^2) + eps);                    inv_rms[m] <- inv
+ *   y = (r * inv) * w, in fp32;                         y_out <- bf16(y)
+ *   q <- the codes and scales that the quantize call of `mode` gives for the
+ *        fp32 tensor y:
+ *     FP8_NORM_TENSOR  fp8_quantize_tensor with `scale`; amax_out (nullable,
+ *                      cleared by the call, not `scale` itself) <- max |y|
+ *     FP8_NORM_GROUP   fp8_quantize_token_group: scales [ceil(K/128), M] of
+ *                      sfmt, K % 16 == 0
+ *     FP8_NORM_MX      fp8_quantize_mx1: scales = its packed E8M0 words
+ *                      (rows padded to 128), K % 128 == 0
+ *   x, residual (nullable), sum_out (nullable)  [M, pitch] of dt
+ *            (fp8_in_dtype_t); sum_out may be x or residual (same pitch).
+ *   w        gains [K] of w_dt; null: ones.
+ *   q        [M, K] codes, contiguous; scales as the mode says.
+ *   y_out (nullable) [M, ld_y] bf16;  inv_rms (nullable) fp32 [M].
+ * All 16-byte aligned (inv_rms, amax_out, scale: 4); pitches in elements, >= K
+ * and multiples of 8; K % 16 == 0, K <= 16384 (FP8_ERR_UNSUPPORTED beyond).
+ * M == 0 writes only amax_out (0).  A row of zeros gives zero codes and unit
+ * scales while eps > 0.  A non-finite value reaches its row's codes as a NaN.
+ * Launched with programmatic stream serialization, as the per-group calls.
+ */
+typedef enum { FP8_NORM_TENSOR = 0, FP8_NORM_GROUP = 1, FP8_NORM_MX = 2 } fp8_norm_mode_t;
+
+typedef struct {
+  const void *x;
+  const void *residual;
+  const void *w;
+  int dt;
+  int w_dt;
+  int64_t M, K;
+  int64_t ld_x, ld_residual;
+  double eps;
+  int mode, fmt, sfmt;
+  const float *scale;
+  uint8_t *q;
+  void *scales;
+  void *sum_out;
+  int64_t ld_sum;
+  void *y_out;
+  int64_t ld_y;
+  float *inv_rms;
+  float *amax_out;
+} fp8_rmsnorm_t;
+FP8_API int fp8_rmsnorm_quantize(const fp8_rmsnorm_t *norm, fp8_stream_t stream);
+
+/* fp8_rmsnorm_backward: the norm's gradient (y's quantization passes the
+ * gradient through unchanged).  With g = dy * w and xhat = r * inv_rms:
+ *   dx = inv_rms (g - xhat * mean(g * xhat)) + d_residual
+ *   dw[k] (+)= sum_m dy * xhat, in fp32, in a fixed order (no atomics)
+ *   dx is the gradient of x and of residual alike; d_residual (nullable) is
+ *   the gradient that reaches r past the norm.
+ *   dy [M, ld_dy] of dy_dt; r (the forward's sum), d_residual, dx of dt, dx
+ *   may be d_residual, or dy of the same type (same pitch); inv_rms fp32 [M]
+ *   as the forward wrote it.
+ *   dw      nullable fp32 [K]; accumulate_dw 1 adds to it.
+ *   q       nullable: codes [M, K] (fmt, E5M2 for gradients) of the fp32 dx
+ *           under the scale fixed before the call, amax_out (nullable) its
+ *           max |dx|: the next layer's dy, quantized with delayed scaling.
+ *   workspace  device scratch for dw, 16-byte aligned, at least
+ *           fp8_rmsnorm_backward_workspace(M, K) bytes; calls that can run at
+ *           the same time need distinct scratch.
+ * Alignment, pitches and K as for fp8_rmsnorm_quantize.  M == 0 zeroes dw
+ * (unless it accumulates) and amax_out. */
+typedef struct {
+  const void *dy;
+  const void *r;
+  const void *w;
+  const void *d_residual;
+  const float *inv_rms;
+  int dy_dt, dt, w_dt;
+  int64_t M, K;
+  int64_t ld_dy, ld_r, ld_dres, ld_dx;
+  void *dx;
+  float *dw;
+  int accumulate_dw;
+  uint8_t *q;
+  int fmt;
+  const float *scale;
+  float *amax_out;
+  void *workspace;
+  int64_t workspace_bytes;
+} fp8_rmsnorm_grad_t;
+FP8_API int64_t fp8_rmsnorm_backward_workspace(int64_t M, int64_t K);
+FP8_API int fp8_rmsnorm_backward(const fp8_rmsnorm_grad_t *grad, fp8_stream_t stream);
+
 /* -------------------------------------------------- delayed-state update --
  * fp8_delayed_state_update: one amax-history step of delayed scaling
  * ([Flax] 2.3 compute_amax_history / update_fp8_meta), on device, no host
