@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -454,31 +455,12 @@ def fp8_adamw_multi(items, step, lr=1e-4, beta1=0.9, beta2=0.999, eps=1e-8, weig
 
 
 # ------------------------------------- RMS norm, linear layer's epilogue --
-
-def _rows(t):
-    """(device pointer, row pitch) of a 2-D CUDA tensor with contiguous rows
-    (None -> NULL)."""
-    if t is None:
-        return None, 0
-    if not t.is_cuda:
-        raise ValueError("expected a CUDA tensor")
-    if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] != 1):
-        raise ValueError("expected a matrix with contiguous rows")
-    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
-
-
-def _shaped(t, shape, dtype, what):
-    if t is not None and (tuple(t.shape) != shape or t.dtype != dtype):
-        raise ValueError("%s must be %s %s" % (what, dtype, shape))
-
-
-def _scratch(nbytes, device, stream):
-    """Scratch of one call: torch hands the memory on in the current stream's
-    order, so a call on another stream brings its own."""
-    if stream is not None:
-        raise ValueError("a call on an explicit stream needs an explicit workspace")
-    return torch.empty(max(16, nbytes), dtype=torch.uint8, device=device)
-
+#
+# These calls sit between others on a decoded token's path, where a kernel
+# takes a few microseconds: their descriptors are packed with struct (native
+# alignment, the C layout) instead of being built field by field, and the
+# current stream is read through torch's raw accessor.  ctypes forms of the
+# descriptors, for callers that fill them themselves, have the same layout.
 
 class RmsNorm(ctypes.Structure):
     """fp8_rmsnorm_t (include/fp8gemm.h)."""
@@ -512,6 +494,91 @@ class ActGradEpilogue(ctypes.Structure):
                 ("workspace", _vp), ("workspace_bytes", _i64)]
 
 
+def _packer(cls):
+    """struct packer of a descriptor class (checked against its layout)."""
+    code = {_vp: "P", _int: "i", _i64: "q", _d: "d"}
+    fmt = "@" + "".join(code.get(t, "P") for _, t in cls._fields_) + "0q"
+    s = struct.Struct(fmt)
+    assert s.size == ctypes.sizeof(cls)
+    return s.pack
+
+
+_pack_norm, _pack_norm_grad = _packer(RmsNorm), _packer(RmsNormGrad)
+_pack_epilogue, _pack_act_grad = _packer(LinearEpilogue), _packer(ActGradEpilogue)
+_pack_problem = _packer(GemmProblem)
+_c_norm, _c_norm_grad = _lib.fp8_rmsnorm_quantize, _lib.fp8_rmsnorm_backward
+_c_tensor_epilogue = _lib.fp8_gemm_tensor_epilogue
+_c_group_epilogue = _lib.fp8_gemm_group_epilogue
+_c_act_backward = _lib.fp8_gemm_tensor_act_backward
+_raw_stream, _get_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+_BF16, _F32 = torch.bfloat16, torch.float32
+
+
+def _flat(t):
+    """Device pointer of a contiguous CUDA tensor (None -> 0)."""
+    if t is None:
+        return 0
+    if not t.is_cuda or not t.is_contiguous():
+        raise ValueError("expected a contiguous CUDA tensor")
+    return t.data_ptr()
+
+
+def _rows(t, shape, dtype, what):
+    """(device pointer, row pitch) of a CUDA matrix with contiguous rows, of
+    the given shape and type (None -> NULL)."""
+    if t is None:
+        return 0, 0
+    if t.shape != shape or t.dtype != dtype or not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor, %s %s" % (what, dtype, tuple(shape)))
+    ld, step = t.stride()
+    if step != 1 and shape[1] != 1:
+        raise ValueError("%s must have contiguous rows" % what)
+    return t.data_ptr(), ld if shape[0] > 1 and ld >= shape[1] else max(ld, shape[1])
+
+
+def _vector(t, n, what):
+    """Device pointer of n contiguous fp32 values (None -> 0)."""
+    if t is None:
+        return 0
+    if t.dtype != _F32 or t.numel() != n:
+        raise ValueError("%s must be fp32 [%d]" % (what, n))
+    return _flat(t)
+
+
+def _codes(t, n, what):
+    if t is None:
+        return 0
+    if t.element_size() != 1 or t.numel() != n:
+        raise ValueError("%s must hold %d one-byte codes" % (what, n))
+    return _flat(t)
+
+
+def _gain(w, k):
+    """(device pointer, type) of the norm's gains (None: ones)."""
+    if w is None:
+        return 0, IN_F32
+    if w.numel() != k:
+        raise ValueError("w must have %d elements" % k)
+    return _flat(w), _in_dt(w)
+
+
+def _on(stream):
+    return _raw_stream(_get_device()) if stream is None else _stream(stream)
+
+
+def _check(name, rc):
+    if rc != FP8_OK:
+        raise Fp8Error(name, rc)
+
+
+def _scratch(nbytes, device, stream):
+    """Scratch of one call: torch hands the memory on in the current stream's
+    order, so a call on another stream brings its own."""
+    if stream is not None:
+        raise ValueError("a call on an explicit stream needs an explicit workspace")
+    return torch.empty(max(16, nbytes), dtype=torch.uint8, device=device)
+
+
 def fp8_rmsnorm_quantize(x, w, eps, fmt, q, *, residual=None, sum_out=None, scale=None,
                          amax_out=None, scales=None, sfmt=SCALE_F32, local=None, y_out=None,
                          inv_rms=None, stream=None):
@@ -519,25 +586,25 @@ def fp8_rmsnorm_quantize(x, w, eps, fmt, q, *, residual=None, sum_out=None, scal
     the codes q of y: per tensor under `scale` (amax_out: max |y|), per 1x128
     group (`scales`, sfmt), or one-level MX (`local` words).  w: [K] gains, or
     None for ones; inv_rms: fp32 [M], kept for fp8_rmsnorm_backward."""
-    m, k = x.shape
+    shape, t = x.shape, x.dtype
+    m, k = shape
     if (scale is not None) + (scales is not None) + (local is not None) != 1:
         raise ValueError("one of scale, scales and local selects the quantization")
-    mode = NORM_TENSOR if scale is not None else NORM_GROUP if scales is not None else NORM_MX
-    dt = _in_dt(x)
-    _shaped(residual, (m, k), x.dtype, "residual")
-    _shaped(sum_out, (m, k), x.dtype, "sum_out")
-    _shaped(y_out, (m, k), torch.bfloat16, "y_out")
-    _shaped(inv_rms, (m,), torch.float32, "inv_rms")
-    if w is not None and w.numel() != k or q.numel() != m * k:
-        raise ValueError("w must have K elements and q M * K")
-    px, ldx = _rows(x)
-    pr, ldr = _rows(residual)
-    ps, lds = _rows(sum_out)
-    py, ldy = _rows(y_out)
-    d = RmsNorm(px, pr, _p(w), dt, dt if w is None else _in_dt(w), m, k, ldx, ldr, eps, mode, fmt,
-                sfmt, _p(scale), _p(q), _p(scales if local is None else local), ps, lds, py, ldy,
-                _p(inv_rms), _p(amax_out))
-    _call("fp8_rmsnorm_quantize", ctypes.addressof(d), _stream(stream))
+    px, ldx = _rows(x, shape, t, "x")
+    pr, ldr = _rows(residual, shape, t, "residual")
+    ps, lds = _rows(sum_out, shape, t, "sum_out")
+    py, ldy = _rows(y_out, shape, _BF16, "y_out")
+    pw, wdt = _gain(w, k)
+    if scale is not None:
+        mode, psc = NORM_TENSOR, 0
+    elif scales is not None:
+        mode, psc = NORM_GROUP, _flat(scales)
+    else:
+        mode, psc = NORM_MX, _flat(local)
+    d = _pack_norm(px, pr, pw, _in_dt(x), wdt, m, k, ldx, ldr, eps, mode, fmt, sfmt,
+                   _vector(scale, 1, "scale"), _codes(q, m * k, "q"), psc, ps, lds, py, ldy,
+                   _vector(inv_rms, m, "inv_rms"), _vector(amax_out, 1, "amax_out"))
+    _check("fp8_rmsnorm_quantize", _c_norm(d, _on(stream)))
 
 
 def fp8_rmsnorm_backward_workspace(m, k):
@@ -551,51 +618,48 @@ def fp8_rmsnorm_backward(dy, r, inv_rms, w, dx, *, d_residual=None, dw=None, acc
     past it; dw: fp32 [K]; q: the codes of dx under `scale`, amax_out its
     max |dx|.  r, inv_rms: as fp8_rmsnorm_quantize wrote them.  workspace
     (with dw): device scratch, allocated on the current stream when None."""
-    m, k = r.shape
-    _shaped(dy, (m, k), dy.dtype, "dy")
-    _shaped(dx, (m, k), r.dtype, "dx")
-    _shaped(d_residual, (m, k), r.dtype, "d_residual")
-    _shaped(inv_rms, (m,), torch.float32, "inv_rms")
-    _shaped(dw, (k,), torch.float32, "dw")
-    if w is not None and w.numel() != k or q is not None and q.numel() != m * k:
-        raise ValueError("w must have K elements and q M * K")
+    shape, t = r.shape, r.dtype
+    m, k = shape
     if dw is not None and workspace is None:
         workspace = _scratch(fp8_rmsnorm_backward_workspace(m, k), r.device, stream)
-    py, ldy = _rows(dy)
-    pr, ldr = _rows(r)
-    pe, lde = _rows(d_residual)
-    px, ldx = _rows(dx)
-    d = RmsNormGrad(py, pr, _p(w), pe, _p(inv_rms), _in_dt(dy), _in_dt(r),
-                    IN_F32 if w is None else _in_dt(w), m, k, ldy, ldr, lde, ldx, px, _p(dw),
-                    int(bool(accumulate_dw)), _p(q), fmt, _p(scale), _p(amax_out), _p(workspace),
-                    0 if workspace is None else workspace.numel() * workspace.element_size())
-    _call("fp8_rmsnorm_backward", ctypes.addressof(d), _stream(stream))
+    py, ldy = _rows(dy, shape, dy.dtype, "dy")
+    pr, ldr = _rows(r, shape, t, "r")
+    pe, lde = _rows(d_residual, shape, t, "d_residual")
+    px, ldx = _rows(dx, shape, t, "dx")
+    pw, wdt = _gain(w, k)
+    d = _pack_norm_grad(py, pr, pw, pe, _vector(inv_rms, m, "inv_rms"), _in_dt(dy), _in_dt(r), wdt,
+                        m, k, ldy, ldr, lde, ldx, px, _vector(dw, k, "dw"),
+                        int(bool(accumulate_dw)), _codes(q, m * k, "q"), fmt,
+                        _vector(scale, 1, "scale"), _vector(amax_out, 1, "amax_out"),
+                        _flat(workspace), 0 if workspace is None else workspace.nbytes)
+    _check("fp8_rmsnorm_backward", _c_norm_grad(d, _on(stream)))
 
 
 def _epilogue_problem(a, fa, b, fb, sa, sb, out, a_layout, b_layout, bias):
-    m, k = a.shape if a_layout == K_MAJOR else a.shape[::-1]
-    n, kb = b.shape if b_layout == K_MAJOR else b.shape[::-1]
+    """(M, N) shape and packed fp8_gemm_problem_t of an epilogue call."""
+    m, k = a.shape
+    n, kb = b.shape
+    if a_layout != K_MAJOR:
+        m, k = k, m
+    if b_layout != K_MAJOR:
+        n, kb = kb, n
     if kb != k:
         raise ValueError("operands of different K")
-    _shaped(bias, (n,), torch.float32, "bias")
-    c, ldc = _rows(out)
-    if out is not None and (out.shape != (m, n) or out.dtype not in (torch.bfloat16, torch.float32)):
-        raise ValueError("out must be bf16 or fp32 [M, N]")
-    dt = OUT_F32 if out is not None and out.dtype == torch.float32 else OUT_BF16
-    return m, n, GemmProblem(_p(a), _p(b), _p(sa), _p(sb), m, n, k, fa, fb, dt, 0, c, ldc, a_layout,
-                             b_layout, _p(bias), None, None)
+    shape = (m, n)
+    dt = OUT_BF16 if out is None or out.dtype == _BF16 else OUT_F32
+    c, ldc = _rows(out, shape, _BF16 if dt == OUT_BF16 else _F32, "out")
+    return shape, _pack_problem(
+        _codes(a, m * k, "a"), _codes(b, n * k, "b"), _vector(sa, 1, "sa"), _vector(sb, 1, "sb"),
+        m, n, k, fa, fb, dt, 0, c, ldc, a_layout, b_layout, _vector(bias, n, "bias"), 0, 0)
 
 
-def _linear_epilogue(m, n, act, residual, pre_out, q=None, q_fmt=E4M3, q_scale=None, q_amax=None):
-    pr, ldr = _rows(residual)
-    pp, ldp = _rows(pre_out)
-    _shaped(pre_out, (m, n), torch.bfloat16, "pre_out")
-    if residual is not None and tuple(residual.shape) != (m, n):
-        raise ValueError("residual must be [M, N]")
-    if q is not None and q.numel() != m * n:
-        raise ValueError("q must have M * N codes")
-    dt = OUT_BF16 if residual is None or _in_dt(residual) == IN_BF16 else OUT_F32
-    return LinearEpilogue(act, pr, dt, ldr, pp, ldp, _p(q), q_fmt, _p(q_scale), _p(q_amax))
+def _linear_epilogue(shape, act, residual, pre_out, q=None, q_fmt=E4M3, q_scale=None, q_amax=None):
+    f32 = residual is not None and residual.dtype == _F32
+    pr, ldr = _rows(residual, shape, _F32 if f32 else _BF16, "residual")
+    pp, ldp = _rows(pre_out, shape, _BF16, "pre_out")
+    return _pack_epilogue(act, pr, OUT_F32 if f32 else OUT_BF16, ldr, pp, ldp,
+                          _codes(q, shape[0] * shape[1], "q"), q_fmt,
+                          _vector(q_scale, 1, "q_scale"), _vector(q_amax, 1, "q_amax"))
 
 
 def fp8_gemm_tensor_epilogue(a, fa, b, fb, sa, sb, out, *, bias=None, act=ACT_NONE, residual=None,
@@ -604,9 +668,9 @@ def fp8_gemm_tensor_epilogue(a, fa, b, fb, sa, sb, out, *, bias=None, act=ACT_NO
     """Per-tensor GEMM with y = act(z) + residual, z = sa sb A B^T + bias, in
     its epilogue: out (bf16, fp32, or None with q) <- y, pre_out <- bf16(z),
     q <- codes of y under q_scale, q_amax <- max |y|."""
-    m, n, p = _epilogue_problem(a, fa, b, fb, sa, sb, out, a_layout, b_layout, bias)
-    e = _linear_epilogue(m, n, act, residual, pre_out, q, q_fmt, q_scale, q_amax)
-    _call("fp8_gemm_tensor_epilogue", ctypes.addressof(p), ctypes.addressof(e), _stream(stream))
+    shape, p = _epilogue_problem(a, fa, b, fb, sa, sb, out, a_layout, b_layout, bias)
+    e = _linear_epilogue(shape, act, residual, pre_out, q, q_fmt, q_scale, q_amax)
+    _check("fp8_gemm_tensor_epilogue", _c_tensor_epilogue(p, e, _on(stream)))
 
 
 def fp8_gemm_group_epilogue(a, sa, b, sb, sfmt, out, *, bias=None, act=ACT_NONE, residual=None,
@@ -614,12 +678,12 @@ def fp8_gemm_group_epilogue(a, sa, b, sb, sfmt, out, *, bias=None, act=ACT_NONE,
     """Per-K-group GEMM with the same epilogue; out bf16."""
     m, k = a.shape
     n = b.shape[0]
-    _shaped(out, (m, n), torch.bfloat16, "out")
-    _shaped(bias, (n,), torch.float32, "bias")
-    e = _linear_epilogue(m, n, act, residual, pre_out)
-    c, ldc = _rows(out)
-    _call("fp8_gemm_group_epilogue", _p(a), _p(sa), _p(b), _p(sb), sfmt, m, n, k, _p(bias),
-          ctypes.addressof(e), c, ldc, _stream(stream))
+    shape = (m, n)
+    e = _linear_epilogue(shape, act, residual, pre_out)
+    c, ldc = _rows(out, shape, _BF16, "out")
+    _check("fp8_gemm_group_epilogue",
+           _c_group_epilogue(_codes(a, m * k, "a"), _flat(sa), _codes(b, n * k, "b"), _flat(sb), sfmt,
+                             m, n, k, _vector(bias, n, "bias"), e, c, ldc, _on(stream)))
 
 
 def fp8_act_backward_workspace(m, n):
@@ -634,19 +698,16 @@ def fp8_gemm_tensor_act_backward(a, fa, b, fb, sa, sb, pre, act, *, out=None, q=
     fp32) and/or q <- codes of dz under q_scale (q_amax: max |dz|); dbias:
     fp32 [N] column sums.  workspace (with dbias): device scratch, allocated
     on the current stream when None."""
-    m, n, p = _epilogue_problem(a, fa, b, fb, sa, sb, out, a_layout, b_layout, None)
-    _shaped(pre, (m, n), torch.bfloat16, "pre")
-    _shaped(dbias, (n,), torch.float32, "dbias")
-    if q is not None and q.numel() != m * n:
-        raise ValueError("q must have M * N codes")
+    shape, p = _epilogue_problem(a, fa, b, fb, sa, sb, out, a_layout, b_layout, None)
+    m, n = shape
     if dbias is not None and workspace is None:
         workspace = _scratch(fp8_act_backward_workspace(m, n), pre.device, stream)
-    pp, ldp = _rows(pre)
-    e = ActGradEpilogue(act, pp, ldp, _p(q), q_fmt, _p(q_scale), _p(q_amax), _p(dbias),
-                        int(bool(accumulate_dbias)), _p(workspace),
-                        0 if workspace is None else workspace.numel() * workspace.element_size())
-    _call("fp8_gemm_tensor_act_backward", ctypes.addressof(p), ctypes.addressof(e),
-          _stream(stream))
+    pp, ldp = _rows(pre, shape, _BF16, "pre")
+    e = _pack_act_grad(act, pp, ldp, _codes(q, m * n, "q"), q_fmt, _vector(q_scale, 1, "q_scale"),
+                       _vector(q_amax, 1, "q_amax"), _vector(dbias, n, "dbias"),
+                       int(bool(accumulate_dbias)), _flat(workspace),
+                       0 if workspace is None else workspace.nbytes)
+    _check("fp8_gemm_tensor_act_backward", _c_act_backward(p, e, _on(stream)))
 
 
 def fp8_get_last_device_error(stream=None):

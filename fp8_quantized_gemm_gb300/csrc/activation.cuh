@@ -8,7 +8,15 @@
 //
 // with s(z) = 1 / (1 + e^-z); the tanh form uses (1 + tanh u) / 2 = s(2u), so
 // that its left tail keeps its relative accuracy.  A NaN stays a NaN.
+//
+// Two values at a time: the products and sums are packed f32x2 instructions
+// (each half rounded as the scalar instruction), which halves what the
+// epilogue issues.  These GEMMs run at the board's power limit, where every
+// instruction per output element costs clock: the GELU product of 16384 x
+// 14336 x 4096 took 757 us with scalar arithmetic and IEEE quotients.
 #pragma once
+
+#include <type_traits>
 
 #include "common.cuh"
 #include "elementwise.cuh"
@@ -22,80 +30,119 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
 }
-__device__ __forceinline__ float min_nan(float a, float b) {
+// 1 / x; a subnormal result becomes zero (x > 2^126: a vanished logistic value)
+__device__ __forceinline__ float rcp_ftz(float x) {
   float r;
-  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
 
-// 2 sqrt(2/pi) and its product with 0.044715
-constexpr float kGeluC1 = 1.5957691216057308f, kGeluC3 = 0.07135481627159726f;
+// A packed pair of fp32 values.
+struct F2 {
+  uint64_t v;
+  __device__ __forceinline__ F2(uint64_t x) : v(x) {}
+  __device__ __forceinline__ F2(float a, float b) : v(f32x2_pack(a, b)) {}
+  __device__ __forceinline__ explicit F2(float a) : v(f32x2_pack(a, a)) {}
+  __device__ __forceinline__ void get(float &a, float &b) const { f32x2_unpack(v, a, b); }
+};
+__device__ __forceinline__ F2 operator*(F2 a, F2 b) { return f32x2_mul(a.v, b.v); }
+__device__ __forceinline__ F2 operator+(F2 a, F2 b) { return f32x2_add(a.v, b.v); }
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) { return f32x2_fma(a.v, b.v, c.v); }
+template <typename Fn>
+__device__ __forceinline__ F2 each(F2 a, Fn &&f) {
+  float x, y;
+  a.get(x, y);
+  return F2(f(x), f(y));
+}
+__device__ __forceinline__ F2 exp2_2(F2 a) { return each(a, [](float x) { return ex2_approx_ftz(x); }); }
+__device__ __forceinline__ F2 rcp_2(F2 a) { return each(a, [](float x) { return rcp_ftz(x); }); }
+__device__ __forceinline__ F2 abs_2(F2 a) { return each(a, [](float x) { return fabsf(x); }); }
+__device__ __forceinline__ F2 relu_2(F2 a) { return each(a, [](float x) { return max_nan(x, 0.0f); }); }
 
-// Phi(z), the normal distribution function, and E = e^(-z^2/2): with
-// x = |z| / sqrt 2 the tail is Phi(-|z|) = E erfcx(x) / 2, and erfcx(x) / 2
-// is t times a degree-8 polynomial in t = 1 / (1 + 0.4 x) (least squares on
-// Chebyshev nodes with the weights driven to equal relative error: 1.3e-7
+// s(-t / log2 e) = 1 / (1 + 2^t)
+__device__ __forceinline__ F2 logistic2(F2 t) { return rcp_2(exp2_2(t) + F2(1.0f)); }
+
+// -2 sqrt(2/pi) log2 e and its product with 0.044715: the exponent of the
+// tanh form's logistic function is t = z (kT1 + kT3 z^2)
+constexpr float kT1 = -2.3022081985175f, kT3 = -0.10294323959671f;
+// 2 sqrt(2/pi) and 3 x 0.044715 of it: d/dz of its argument
+constexpr float kD1 = 1.5957691216057308f, kD3 = 0.21406444881478f;
+
+// E = e^(-z^2/2), a = |z| and Phi(-a) / E = erfcx(a / sqrt 2) / 2, which is t
+// times a degree-8 polynomial in t = 1 / (1 + 0.4 a / sqrt 2) (least squares
+// on Chebyshev nodes with the weights driven to equal relative error: 1.3e-7
 // over t in (0, 1], that is for every z).
-__device__ __forceinline__ float normal_cdf(float z, float &E) {
-  E = ex2_approx_ftz(__fmul_rn(__fmul_rn(z, z), -0.72134752044448170f));
-  const float t = rcp_approx(__fmaf_rn(fabsf(z), 0.28284271247461901f, 1.0f));
-  float p = 0.025127250701189041f;
-  p = __fmaf_rn(p, t, -0.091437287628650665f);
-  p = __fmaf_rn(p, t, 0.084523670375347137f);
-  p = __fmaf_rn(p, t, -0.0027899211272597313f);
-  p = __fmaf_rn(p, t, 0.070710234344005585f);
-  p = __fmaf_rn(p, t, 0.084272146224975586f);
-  p = __fmaf_rn(p, t, 0.10392123460769653f);
-  p = __fmaf_rn(p, t, 0.11283480376005173f);
-  p = __fmaf_rn(p, t, 0.11283793300390244f);
-  const float tail = __fmul_rn(E, __fmul_rn(p, t));
-  return z < 0.0f ? tail : 1.0f - tail;
+__device__ __forceinline__ F2 normal_tail(F2 z, F2 &a, F2 &E) {
+  a = abs_2(z);
+  E = exp2_2(z * z * F2(-0.72134752044448170f));
+  const F2 t = rcp_2(fma2(a, F2(0.28284271247461901f), F2(1.0f)));
+  F2 p(0.025127250701189041f);
+  p = fma2(p, t, F2(-0.091437287628650665f));
+  p = fma2(p, t, F2(0.084523670375347137f));
+  p = fma2(p, t, F2(-0.0027899211272597313f));
+  p = fma2(p, t, F2(0.070710234344005585f));
+  p = fma2(p, t, F2(0.084272146224975586f));
+  p = fma2(p, t, F2(0.10392123460769653f));
+  p = fma2(p, t, F2(0.11283480376005173f));
+  p = fma2(p, t, F2(0.11283793300390244f));
+  return p * t;
 }
 
 template <int A>
-__device__ __forceinline__ float act_value(float z) {
-  if constexpr (A == kActRelu) return max_nan(z, 0.0f);
+__device__ __forceinline__ F2 act_value2(F2 z) {
+  if constexpr (A == kActRelu) return relu_2(z);
   if constexpr (A == kActRelu2) {
-    const float p = max_nan(z, 0.0f);
-    return __fmul_rn(p, p);
+    const F2 p = relu_2(z);
+    return p * p;
   }
-  if constexpr (A == kActSilu) return __fmul_rn(z, sigmoidf_(z));
-  if constexpr (A == kActGeluTanh)
-    return __fmul_rn(z, sigmoidf_(__fmul_rn(z, __fmaf_rn(kGeluC3, __fmul_rn(z, z), kGeluC1))));
+  if constexpr (A == kActSilu) return z * logistic2(z * F2(kNegLog2e));
+  if constexpr (A == kActGeluTanh) return z * logistic2(z * fma2(z * z, F2(kT3), F2(kT1)));
   if constexpr (A == kActGelu) {
-    float E;
-    return __fmul_rn(z, normal_cdf(z, E));
+    // z Phi(z) = max(z, 0) - |z| Phi(-|z|)
+    F2 a(0.0f), E(0.0f);
+    const F2 q = normal_tail(z, a, E);
+    return fma2(a * F2(-1.0f), E * q, relu_2(z));
   }
   return z;
 }
 
-// The derivative.  Beyond |z| = 100 every one of the smooth activations has
-// slope 0 or 1 in fp32: z is clamped there, so that no product of a vanished
-// factor and an overflowed one is formed.
+// The derivative.  At finite z no product of a vanished factor and an
+// overflowed one is formed: the factors that vanish do so long before the
+// others leave fp32 (the tanh form's z^2 is capped where its slope is 0 or 1).
 template <int A>
-__device__ __forceinline__ float act_slope(float z) {
-  if constexpr (A == kActRelu) return z > 0.0f ? 1.0f : (z == z ? 0.0f : z);
-  if constexpr (A == kActRelu2) return 2.0f * max_nan(z, 0.0f);
-  if constexpr (A == kActNone) return 1.0f;
-  const float c = max_nan(min_nan(z, 100.0f), -100.0f);
+__device__ __forceinline__ F2 act_slope2(F2 z) {
+  if constexpr (A == kActRelu)
+    return each(z, [](float x) { return x > 0.0f ? 1.0f : (x == x ? 0.0f : x); });
+  if constexpr (A == kActRelu2) {
+    const F2 p = relu_2(z);
+    return p + p;
+  }
   if constexpr (A == kActSilu) {
-    const float s = sigmoidf_(c);
-    return __fmul_rn(s, __fmaf_rn(c, 1.0f - s, 1.0f));
+    const F2 s = logistic2(z * F2(kNegLog2e));
+    return s * fma2(z, fma2(s, F2(-1.0f), F2(1.0f)), F2(1.0f));
   }
   if constexpr (A == kActGeluTanh) {
-    const float zz = __fmul_rn(c, c);
-    const float s = sigmoidf_(__fmul_rn(c, __fmaf_rn(kGeluC3, zz, kGeluC1)));
-    const float du = __fmaf_rn(3.0f * kGeluC3, zz, kGeluC1);
-    return __fmaf_rn(__fmul_rn(c, s), __fmul_rn(1.0f - s, du), s);
+    const F2 zz = each(z * z, [](float x) { return fminf(x, 1e6f); });
+    const F2 s = logistic2(z * fma2(zz, F2(kT3), F2(kT1)));
+    return fma2(z * s, fma2(s, F2(-1.0f), F2(1.0f)) * fma2(zz, F2(kD3), F2(kD1)), s);
   }
-  float E;
-  const float cdf = normal_cdf(c, E);
-  return __fmaf_rn(__fmul_rn(c, E), 0.39894228040143268f, cdf);
+  if constexpr (A == kActGelu) {
+    // Phi(z) + z phi(z) = u for z < 0 and 1 - u otherwise, with
+    // u = Phi(-|z|) - |z| phi(z) = E (q - |z| / sqrt(2 pi))
+    F2 a(0.0f), E(0.0f);
+    const F2 q = normal_tail(z, a, E);
+    const F2 u = E * fma2(a, F2(-0.39894228040143268f), q);
+    float u0, u1, z0, z1;
+    u.get(u0, u1);
+    z.get(z0, z1);
+    return F2(z0 < 0.0f ? u0 : 1.0f - u0, z1 < 0.0f ? u1 : 1.0f - u1);
+  }
+  return F2(1.0f);
 }
 
 // Calls f with the activation as a compile-time constant (one uniform branch
-// per call, outside the loop over values).
-template <typename Fn>
+// per call, outside the loop over values); for kActNone only with NONE.
+template <bool NONE = false, typename Fn>
 __device__ __forceinline__ void with_act(int act, Fn &&f) {
   switch (act) {
     case kActRelu: f(std::integral_constant<int, kActRelu>{}); break;
@@ -103,7 +150,9 @@ __device__ __forceinline__ void with_act(int act, Fn &&f) {
     case kActSilu: f(std::integral_constant<int, kActSilu>{}); break;
     case kActGeluTanh: f(std::integral_constant<int, kActGeluTanh>{}); break;
     case kActGelu: f(std::integral_constant<int, kActGelu>{}); break;
-    default: break;
+    default:
+      if constexpr (NONE) f(std::integral_constant<int, kActNone>{});
+      break;
   }
 }
 

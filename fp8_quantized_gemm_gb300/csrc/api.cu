@@ -220,14 +220,18 @@ int get_workspace(cudaStream_t st, size_t need, void **out, int slot) {
 }
 
 // ep: the linear layer's epilogue (nullable).
+// grad: it is the gradient epilogue (per-tensor scales, no split K).
 int run_gemm(int mode, const uint8_t *a, const uint8_t *b, GemmArgs &args, cudaStream_t st,
-             const fp8k::LinearEp *ep = nullptr) {
+             const fp8k::LinearEp *ep = nullptr, bool grad = false) {
   DeviceState *d = nullptr;
   int rc = device_state(&d);
   if (rc != FP8_OK) return rc;
   args.err = d->err;
   args.wait_limit_ns = g_wait_limit_ns;
-  args.ksplit = fp8k::gemm_ksplit(mode, args.M, args.N, args.K, d->sms, true);
+  args.ksplit = grad ? 1
+                : ep != nullptr && mode == fp8k::kScaleTensor
+                    ? fp8k::gemm_epilogue_ksplit(args.M, args.N, args.K, d->sms)
+                    : fp8k::gemm_ksplit(mode, args.M, args.N, args.K, d->sms, true);
   args.ws = nullptr;
   args.counters = nullptr;
   // split K reduces inside a thread-block cluster (no workspace)
@@ -235,12 +239,14 @@ int run_gemm(int mode, const uint8_t *a, const uint8_t *b, GemmArgs &args, cudaS
   args.vec_store = vector_store_ok(args.c, args.ldc, args.out_dt);
   CUtensorMap tma, tmb;
   if ((rc = encode_gemm_operand(&tma, a, args.a_mn, args.K, args.M, 128)) != FP8_OK) return rc;
-  if (args.ksplit == 1 && g_use_pairs && fp8k::gemm_pair_eligible(mode, args.M, args.N, d->sms)) {
+  const bool pairs = ep != nullptr ? fp8k::gemm_pair_epilogue_eligible(mode, args.M, args.N, d->sms)
+                                   : fp8k::gemm_pair_eligible(mode, args.M, args.N, d->sms);
+  if (args.ksplit == 1 && g_use_pairs && pairs) {
     if ((rc = encode_gemm_operand(&tmb, b, args.b_mn, args.K, args.N,
                                   fp8k::gemm_pair_b_rows())) != FP8_OK)
       return rc;
     if (ep != nullptr)
-      return to_status(fp8k::launch_gemm_pair_epilogue(tma, tmb, args, *ep, false, d->sms, st));
+      return to_status(fp8k::launch_gemm_pair_epilogue(tma, tmb, args, *ep, grad, d->sms, st));
     CUtensorMap tmc{};
     args.tma_store = use_tma_store(args.c, args.ldc, args.out_dt, args.accumulate) ? 1 : 0;
     if (args.tma_store &&
@@ -258,7 +264,8 @@ int run_gemm(int mode, const uint8_t *a, const uint8_t *b, GemmArgs &args, cudaS
   // multicast pairs of vertically adjacent tiles share each B box: measured
   // faster for 128-wide tiles (the FP32-promotion mode, and the block-scaled
   // modes at mid-size M), not for the 128 x 256 block-scaled tiles
-  const int bn = fp8k::gemm_tile_n(mode, args.M, args.N, d->sms);
+  const int bn = ep != nullptr ? fp8k::gemm_epilogue_tile_n(mode, args.M, args.N, d->sms)
+                               : fp8k::gemm_tile_n(mode, args.M, args.N, d->sms);
   args.multicast = g_use_multicast && mode != fp8k::kScaleTensor &&
                            mode != fp8k::kScaleGroupF32x32 && bn == 128 &&
                            args.ksplit == 1 && !args.b_mn && args.experts == 0 && args.M > 128
@@ -268,7 +275,7 @@ int run_gemm(int mode, const uint8_t *a, const uint8_t *b, GemmArgs &args, cudaS
                                 args.multicast ? bn / 2 : bn)) != FP8_OK)
     return rc;
   return to_status(ep != nullptr
-                       ? fp8k::launch_gemm_epilogue(mode, tma, tmb, args, *ep, d->sms, st)
+                       ? fp8k::launch_gemm_epilogue(mode, tma, tmb, args, *ep, grad, d->sms, st)
                        : fp8k::launch_gemm(mode, tma, tmb, args, d->sms, st));
 }
 
@@ -372,8 +379,15 @@ int check_epilogue_problem(const fp8_gemm_problem_t &p, bool codes) {
   return check_tensor_problem(t);
 }
 
-// Validates and converts the public epilogue descriptor (N output columns).
-int linear_epilogue(const fp8_linear_epilogue_t &e, int64_t N, fp8k::LinearEp *out) {
+// Rows that lanes may access a 32-byte sector at a time.
+int sector_rows(const void *p, int64_t ld, int64_t elem) {
+  return aligned_to(p, 32) && ld * elem % 32 == 0 ? 1 : 0;
+}
+
+// Validates and converts the public epilogue descriptor (N output columns of
+// c, nullable).
+int linear_epilogue(const fp8_linear_epilogue_t &e, int64_t N, const void *c, int64_t ldc,
+                    int out_dt, fp8k::LinearEp *out) {
   if (e.act < FP8_ACT_NONE || e.act > FP8_ACT_GELU) return FP8_ERR_INVALID_ARG;
   if (e.residual != nullptr) {
     if (e.residual_dt != FP8_OUT_F32 && e.residual_dt != FP8_OUT_BF16) return FP8_ERR_INVALID_ARG;
@@ -396,15 +410,16 @@ int linear_epilogue(const fp8_linear_epilogue_t &e, int64_t N, fp8k::LinearEp *o
   l.res = e.residual;
   l.res_dt = e.residual_dt;
   l.ld_res = e.ld_residual;
-  l.res_vec = vector_store_ok(e.residual, e.ld_residual, e.residual_dt);
+  l.c_vec = sector_rows(c, ldc, out_dt == FP8_OUT_F32 ? 4 : 2);
+  l.res_vec = sector_rows(e.residual, e.ld_residual, e.residual_dt == FP8_OUT_F32 ? 4 : 2);
   l.pre = e.pre;
   l.ld_pre = e.ld_pre;
-  l.pre_vec = vector_store_ok(e.pre, e.ld_pre, FP8_OUT_BF16);
+  l.pre_vec = sector_rows(e.pre, e.ld_pre, 2);
   l.q = e.q;
   l.q_fmt = e.q_fmt;
   l.q_scale = e.q_scale;
   l.q_amax = reinterpret_cast<uint32_t *>(e.q_amax);
-  l.q_vec = aligned16(e.q) && N % 16 == 0 ? 1 : 0;
+  l.q_vec = sector_rows(e.q, N, 1) ? 2 : aligned16(e.q) && N % 16 == 0 ? 1 : 0;
   *out = l;
   return FP8_OK;
 }
@@ -884,7 +899,7 @@ int fp8_gemm_group_epilogue(const uint8_t *a, const void *sa, const uint8_t *b, 
   if (epilogue == nullptr || c == nullptr) return FP8_ERR_INVALID_ARG;
   if (epilogue->q != nullptr) return FP8_ERR_UNSUPPORTED;
   fp8k::LinearEp ep;
-  const int rc = linear_epilogue(*epilogue, N, &ep);
+  const int rc = linear_epilogue(*epilogue, N, c, ldc, FP8_OUT_BF16, &ep);
   if (rc != FP8_OK) return rc;
   return run_group(a, sa, b, sb, sfmt, M, N, K, bias, c, ldc, &ep, stream);
 }
@@ -896,7 +911,8 @@ int fp8_gemm_tensor_epilogue(const fp8_gemm_problem_t *problem,
   int rc = check_epilogue_problem(*problem, epilogue->q != nullptr);
   if (rc != FP8_OK) return rc;
   fp8k::LinearEp ep;
-  if ((rc = linear_epilogue(*epilogue, problem->N, &ep)) != FP8_OK) return rc;
+  if ((rc = linear_epilogue(*epilogue, problem->N, problem->c, problem->ldc, problem->out_dt,
+                            &ep)) != FP8_OK) return rc;
   DeviceState *d = nullptr;
   if ((rc = device_state(&d)) != FP8_OK) return rc;
   const cudaStream_t st = (cudaStream_t)stream;
@@ -926,7 +942,7 @@ int fp8_gemm_tensor_act_backward(const fp8_gemm_problem_t *problem,
   f.ld_pre = e.ld_pre;
   f.q = e.q; f.q_fmt = e.q_fmt; f.q_scale = e.q_scale; f.q_amax = e.q_amax;
   fp8k::LinearEp ep;
-  if ((rc = linear_epilogue(f, p.N, &ep)) != FP8_OK) return rc;
+  if ((rc = linear_epilogue(f, p.N, p.c, p.ldc, p.out_dt, &ep)) != FP8_OK) return rc;
   if (e.dbias != nullptr) {
     if (e.workspace == nullptr || e.workspace_bytes < fp8_act_backward_workspace(p.M, p.N))
       return FP8_ERR_INVALID_ARG;
@@ -938,16 +954,7 @@ int fp8_gemm_tensor_act_backward(const fp8_gemm_problem_t *problem,
   const cudaStream_t st = (cudaStream_t)stream;
   if ((rc = clear_amax(ep, st)) != FP8_OK) return rc;
   GemmArgs args = tensor_args(p);
-  args.err = d->err;
-  args.wait_limit_ns = g_wait_limit_ns;
-  args.ksplit = 1;
-  args.vec_store = vector_store_ok(args.c, args.ldc, args.out_dt);
-  CUtensorMap tma, tmb;
-  if ((rc = encode_gemm_operand(&tma, p.a, args.a_mn, p.K, p.M, 128)) != FP8_OK) return rc;
-  if ((rc = encode_gemm_operand(&tmb, p.b, args.b_mn, p.K, p.N, fp8k::gemm_pair_b_rows())) !=
-      FP8_OK)
-    return rc;
-  rc = to_status(fp8k::launch_gemm_pair_epilogue(tma, tmb, args, ep, true, d->sms, st));
+  rc = run_gemm(fp8k::kScaleTensor, p.a, p.b, args, st, &ep, true);
   if (rc != FP8_OK || e.dbias == nullptr) return rc;
   return to_status(fp8k::launch_column_sum(ep.part, (p.M + 31) / 32, p.N, e.accumulate_dbias,
                                            e.dbias, st));

@@ -405,6 +405,12 @@ __device__ __forceinline__ void tmem_ld_wait() {
                  "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),   \
                  "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]))
 
+#define FP8K_REG_FENCE32(r)    \
+  do {                         \
+    FP8K_REG_FENCE16(r);       \
+    FP8K_REG_FENCE16((r + 16)); \
+  } while (0)
+
 // ------------------------------------------- CTA pairs (cta_group::2) --
 __device__ __forceinline__ uint32_t cluster_ctarank() {
   uint32_t r;

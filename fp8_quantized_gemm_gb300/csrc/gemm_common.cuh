@@ -124,6 +124,17 @@ __device__ __forceinline__ void store4(const GemmArgs &a, int64_t row, int64_t c
   }
 }
 
+// store4 as the last step of cluster_reduce.
+struct StorePut {
+  const GemmArgs &a;
+  struct In {};
+  __device__ __forceinline__ In load(int64_t, int64_t, int) const { return {}; }
+  __device__ __forceinline__ void operator()(int64_t row, int64_t col, int n, const float (&v)[4],
+                                             In) const {
+    store4(a, row, col, n, v);
+  }
+};
+
 // Split K, in the CTA that arrived last for a tile: out = alpha * (sum over
 // the splits, in split order, of the fp32 partials), for the whole
 // tile_rows x tile_cols tile at (m0, n0).  The work is spread over all `nthr`
@@ -205,7 +216,7 @@ __device__ __forceinline__ float4 ld_shared_cluster_f4(uint32_t addr) {
 // [rank * R / ks, (rank + 1) * R / ks) of the tile (R its valid rows) over
 // every CTA's partial tile, in split order (the same order, hence the same
 // sums, as the global-workspace reduction), scales by alpha and hands up to
-// four columns at a time to put(row, col, n, values).
+// four columns at a time to put(row, col, n, values, put.load(row, col, n)).
 // Every thread of the CTA takes part: thread t owns float4 column t % (BN/4)
 // and rows t / (BN/4), + nthr / (BN/4), ...; each step issues the remote
 // loads of kStep rows of all KS splits (about 16 in flight per thread)
@@ -215,7 +226,7 @@ template <int BN, int KS, typename Put>
 __device__ __forceinline__ void cluster_reduce_ks(const GemmArgs &a, uint32_t base, int64_t m0,
                                                   int64_t n0, int64_t r0, int64_t r1,
                                                   int64_t cols, float alpha, uint32_t rank,
-                                                  int tid, int nthr, Put &put) {
+                                                  int tid, int nthr, const Put &put) {
   constexpr int kCg = BN / 4;
   constexpr int kStep = KS >= 16 ? 1 : 16 / KS;
   const int rstride = nthr / kCg;
@@ -225,10 +236,12 @@ __device__ __forceinline__ void cluster_reduce_ks(const GemmArgs &a, uint32_t ba
   const int n = cols - c < 4 ? (int)(cols - c) : 4;
   for (int64_t rb = r0 + tid / kCg; rb < r1; rb += (int64_t)kStep * rstride) {
     float4 p[kStep][KS];
+    typename Put::In in[kStep];  // the rows' other operands, in flight as well
 #pragma unroll
     for (int j = 0; j < kStep; ++j) {
       const int64_t r = rb + (int64_t)j * rstride;
       if (r < r1) {
+        in[j] = put.load(m0 + r, n0 + c, n);
         const uint32_t off = base + (uint32_t)((r * kPartStride<BN> + c) * 4);
 #pragma unroll
         for (int sp = 0; sp < KS; ++sp)  // this CTA's own partial: a local load
@@ -247,7 +260,7 @@ __device__ __forceinline__ void cluster_reduce_ks(const GemmArgs &a, uint32_t ba
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[i] *= alpha;
-        put(m0 + r, n0 + c, n, acc);
+        put(m0 + r, n0 + c, n, acc, in[j]);
       }
     }
   }
@@ -256,7 +269,7 @@ __device__ __forceinline__ void cluster_reduce_ks(const GemmArgs &a, uint32_t ba
 template <int BN, typename Put>
 __device__ __forceinline__ void cluster_reduce(const GemmArgs &a, const float *part, int64_t m0,
                                                int64_t n0, int64_t tile_rows, float alpha,
-                                               uint32_t rank, int ks, int tid, int nthr, Put put) {
+                                               uint32_t rank, int ks, int tid, int nthr, const Put &put) {
   const int64_t rows = a.M - m0 < tile_rows ? a.M - m0 : tile_rows;
   const int64_t cols = a.N - n0 < BN ? a.N - n0 : BN;
   if (rows <= 0 || cols <= 0) return;

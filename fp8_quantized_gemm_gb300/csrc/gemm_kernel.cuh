@@ -56,33 +56,42 @@ constexpr int64_t kBandRows = 16;
 // staging; seven fit beside no expert tables but measured no faster).
 constexpr int kF32Stages = 6;
 
-template <int MODE, int BN, int STAGES>
+// LIN 0: plain stores.  1, 2: the linear layer's epilogue, forward or gradient
+// (linear_epilogue.cuh), on eight warps.
+template <int MODE, int BN, int STAGES, int LIN = 0>
 struct Cfg {
   static constexpr int BM = 128, BK = 128;
   static constexpr bool kBlockScaled = (MODE == kScaleMx || MODE == kScaleGroupUe8m0);
   static constexpr bool kPromote = (MODE == kScaleGroupF32 || MODE == kScaleGroupF32x32);
   // promotion slices per 128-wide K block (one per K=32 MMA with 32-wide groups)
   static constexpr int kSub = MODE == kScaleGroupF32x32 ? 4 : 1;
-  static constexpr int kEpiWarps = kPromote ? 8 : 4;
+  static constexpr int kEpiWarps = kPromote || LIN != 0 ? 8 : 4;
+  // tile columns of an epilogue warp (one or two warps per TMEM lane quadrant)
+  static constexpr int kEpiCols = 4 * BN / kEpiWarps;
   static constexpr int kThreads = 64 + 32 * kEpiWarps;
   static constexpr uint32_t kABytes = BM * BK, kBBytes = BN * BK;
   static constexpr uint32_t kSfaBytes = kBlockScaled ? BM * 4 : 0;
-  static constexpr uint32_t kSfbBytes = kBlockScaled ? BN * 4 : 0;
+  // B scale factors are staged in whole 128-row blocks (a 192-wide tile lies
+  // in two of them, from row 0 or 64 of the first)
+  static constexpr uint32_t kSfbRows = (BN + 127) / 128 * 128;
+  static constexpr uint32_t kSfbBytes = kBlockScaled ? kSfbRows * 4 : 0;
   static constexpr uint32_t kTileBytes = STAGES * (kABytes + kBBytes);
   static constexpr uint32_t kSfBytes = STAGES * (kSfaBytes + kSfbBytes);
   // TMEM accumulators: per-tensor mode double-buffers whole tiles (epilogue of
   // one tile overlaps the MMAs of the next); the promotion mode rings four
   // per-K-slice buffers; the block-scaled modes keep one tile buffer next to
-  // their per-stage scale-factor columns.
-  static constexpr int kAccBufs = kPromote ? 4 : (MODE == kScaleTensor ? 2 : 1);
+  // their per-stage scale-factor columns, or two of 192 columns.
+  static constexpr int kAccBufs = kPromote ? 4 : (MODE == kScaleTensor || BN == 192 ? 2 : 1);
   static constexpr uint32_t kAccCols = kAccBufs * BN;
-  static constexpr uint32_t kSfColsPerStage = kBlockScaled ? 4 + BN / 32 : 0;
+  static constexpr uint32_t kSfColsPerStage = kBlockScaled ? 4 + kSfbRows / 32 : 0;
   static constexpr uint32_t kTmemCols = pow2_cols(kAccCols + STAGES * kSfColsPerStage);
   static constexpr int kNumBars = 2 * STAGES + 2 * kAccBufs + 1;  // + drain
-  static constexpr uint32_t kSmem = 1024 + kTileBytes + kSfBytes + 8 * kNumBars + 16;
+  static constexpr uint32_t kEpBytes = LIN != 0 && !kPromote ? kEpiWarps * kEpStageBytes : 0;  // linear_epilogue.cuh
+  static constexpr uint32_t kSmem = 1024 + kTileBytes + kSfBytes + kEpBytes + 8 * kNumBars + 16;
   static_assert(kTmemCols <= 512, "TMEM budget");
   static_assert(kSmem <= 227 * 1024, "shared-memory budget");
   static_assert(BN % 32 == 0 && BN <= 256, "tile N");
+  static_assert(BN % 128 == 0 || MODE == kScaleMx, "scales in 128-row blocks: MX words only");
 };
 
 // Epilogue factor of the block-scaled mode: the two global factors, or 1
@@ -97,18 +106,19 @@ __device__ __forceinline__ float mx_alpha(const GemmArgs &a) {
 // each CTA loads one half of it and multicasts that half to both, so the L2
 // traffic of B halves; a stage is refilled once both CTAs' MMAs have
 // released it (the commit arrives on both CTAs' empty barriers).
-template <int MODE, int BN, int STAGES, bool EXPERTS, int MC, bool EPI>
-__global__ void __launch_bounds__(Cfg<MODE, BN, STAGES>::kThreads, 1)
+template <int MODE, int BN, int STAGES, bool EXPERTS, int MC, int LIN>
+__global__ void __launch_bounds__(Cfg<MODE, BN, STAGES, LIN>::kThreads, 1)
     gemm_kernel(const __grid_constant__ CUtensorMap tma, const __grid_constant__ CUtensorMap tmb,
-                const GemmArgs args, const EpParam<EPI> epp) {
-  using C = Cfg<MODE, BN, STAGES>;
-  static_assert(!EPI || !EXPERTS, "the epilogue takes plain rows");
+                const GemmArgs args, const EpParam<LIN != 0> epp) {
+  using C = Cfg<MODE, BN, STAGES, LIN>;
+  static_assert(LIN == 0 || !EXPERTS, "the epilogue takes plain rows");
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t *tiles = smem;
   uint8_t *sf = smem + C::kTileBytes;
-  uint64_t *bars = reinterpret_cast<uint64_t *>(sf + C::kSfBytes);
+  uint8_t *ep_stage = sf + C::kSfBytes;
+  uint64_t *bars = reinterpret_cast<uint64_t *>(ep_stage + C::kEpBytes);
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + C::kNumBars);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
@@ -245,12 +255,12 @@ __global__ void __launch_bounds__(Cfg<MODE, BN, STAGES>::kThreads, 1)
   }
 
   // running max |y| and scale of the codes (the linear layer's epilogue)
-  uint32_t key = 0;
+  float amax = 0.0f;
   auto ep_scale = [&]() {
-    if constexpr (EPI)
-      return epilogue_scale(epp.e);
+    if constexpr (LIN != 0)
+      return CodeScale(epp.e);
     else
-      return ScaleDiv(1.0f);
+      return 0;
   };
 
   if (warp == 0) {
@@ -358,7 +368,8 @@ __global__ void __launch_bounds__(Cfg<MODE, BN, STAGES>::kThreads, 1)
         const int64_t b_npad = (b_rows + 127) / 128 * 128;
         const bool a_words = EXPERTS || m0 < a_mpad;
         if constexpr (MODE == kScaleMx) {
-          const int64_t rows = (b_npad - brow) < BN ? (b_npad - brow) : BN;
+          const int64_t left = b_npad - (brow & ~(int64_t)127);
+          const int64_t rows = left < C::kSfbRows ? left : C::kSfbRows;
           sfb_bytes = (uint32_t)rows * 4u;
           tx += (a_words ? C::kSfaBytes : 0u) + sfb_bytes;
         }
@@ -386,7 +397,8 @@ __global__ void __launch_bounds__(Cfg<MODE, BN, STAGES>::kThreads, 1)
           // [tile][K/128][128]
           const uint32_t *la = static_cast<const uint32_t *>(args.sa) +
                                (EXPERTS ? (cur.atile * KB + kb) * 128 : (int64_t)kb * a_mpad + m0);
-          const uint32_t *lb = static_cast<const uint32_t *>(args.sb) + (int64_t)kb * b_npad + brow;
+          const uint32_t *lb = static_cast<const uint32_t *>(args.sb) + (int64_t)kb * b_npad +
+                               (brow & ~(int64_t)127);
           if (a_words) bulk_load(smem_u32(sSfa(s)), la, C::kSfaBytes, full_bar(s));
           bulk_load(smem_u32(sSfb(s)), lb, sfb_bytes, full_bar(s));
         }
@@ -418,6 +430,9 @@ __global__ void __launch_bounds__(Cfg<MODE, BN, STAGES>::kThreads, 1)
       for (int64_t u = u_first; u < num_units && ok; u += u_step, ++j) {
         uint32_t d = tmem;
         const int kb0 = kb_begin(u), kb1 = kb_end(u);
+        // columns of the first B scale block that lie before a 192-wide tile
+        uint32_t sfb_skip = 0;
+        if constexpr (BN == 192) sfb_skip = (uint32_t)(tile_info(unit_tile(u)).n0 & 127) >> 5;
         uint32_t tile_buf = 0;
         if constexpr (!C::kPromote) {
           tile_buf = j % C::kAccBufs;
@@ -474,14 +489,14 @@ __global__ void __launch_bounds__(Cfg<MODE, BN, STAGES>::kThreads, 1)
             const uint32_t sfb_col = sfa_col + 4;
             tmem_cp_32x128b_warpx4(tmem + sfa_col, sdesc_plain(smem_u32(sSfa(s))));
 #pragma unroll
-            for (int jj = 0; jj < BN / 128; ++jj)
+            for (int jj = 0; jj < (int)C::kSfbRows / 128; ++jj)
               tmem_cp_32x128b_warpx4(tmem + sfb_col + 4 * jj,
                                      sdesc_plain(smem_u32(sSfb(s)) + 512 * jj));
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               const uint32_t idesc = idesc_mxf8f6f4(128, BN, args.fa, args.fb, k, k);
               mma_mxf8f6f4(d, adesc + 2 * k, bdesc + 2 * k, idesc, tmem + sfa_col,
-                           tmem + sfb_col, (kb != kb0 || k != 0) ? 1u : 0u);
+                           tmem + sfb_col + sfb_skip, (kb != kb0 || k != 0) ? 1u : 0u);
             }
           } else {
             const uint32_t idesc = idesc_f8f6f4(128, BN, args.fa, args.fb, args.a_mn, args.b_mn);
@@ -531,15 +546,19 @@ __global__ void __launch_bounds__(Cfg<MODE, BN, STAGES>::kThreads, 1)
     const uint32_t lane_base = tmem + ((32u * q) << 16);
     // the linear layer's epilogue: its row operand, fetched a chunk ahead
     RowIn in;
-    const ScaleDiv qd = ep_scale();
-    auto fetch = [&](int64_t r, int64_t c) {
-      if constexpr (EPI) fetch_row32<false>(args, epp.e, r, c, in);
+    const auto qd = ep_scale();
+    uint8_t *stage = ep_stage + (warp - 2) * kEpStageBytes;
+    auto fetch = [&](int64_t r0, int64_t c) {
+      if constexpr (LIN != 0) fetch_chunk<LIN == 2>(args, epp.e, r0, c, stage, in);
     };
-    auto finish = [&](int64_t r, int64_t c, float (&v)[32], const RowIn &cur) {
-      if constexpr (EPI)
-        linear_row32(args, epp.e, r, c, v, cur, qd, key);
-      else
-        store_row32(args, r, c, v);
+    // r: accumulators of row r0 + lane; next(): the forward pass has read them
+    auto finish = [&](int64_t r0, int64_t c, const uint32_t (&r)[32], float alpha,
+                      const RowIn &cur, auto &&next) {
+      float v[32];
+      if constexpr (LIN == 1) scale_bias(args, c, r, alpha, v);
+      next();
+      if constexpr (LIN == 1) linear_chunk(args, epp.e, r0, c, v, cur, qd, stage, amax);
+      if constexpr (LIN == 2) grad_chunk(args, epp.e, r0, c, r, alpha, cur, qd, stage, amax);
     };
     if constexpr (!C::kPromote) {
       float alpha = 1.0f;
@@ -547,6 +566,7 @@ __global__ void __launch_bounds__(Cfg<MODE, BN, STAGES>::kThreads, 1)
         alpha = *static_cast<const float *>(args.sa) * *static_cast<const float *>(args.sb);
       if constexpr (MODE == kScaleMx) alpha = mx_alpha(args);
       uint32_t j = 0;
+      const int c0 = C::kEpiWarps == 8 ? (int)((warp - 2) >> 2) * C::kEpiCols : 0;
       for (int64_t u = u_first; u < num_units; u += u_step, ++j) {
         const int64_t t = unit_tile(u);
         const int split = (int)(u / num_tiles);
@@ -555,32 +575,59 @@ __global__ void __launch_bounds__(Cfg<MODE, BN, STAGES>::kThreads, 1)
         // rows past the tile's expert belong to the next expert: not stored
         const int64_t row = m0 + 32 * q + lane < ti.row_end ? m0 + 32 * q + lane : args.M;
         const uint32_t buf = j % C::kAccBufs, use = j / C::kAccBufs;
-        if (ks == 1) fetch(row, n0);
+        if (ks == 1) fetch(m0 + 32 * q, n0 + c0);
         const bool got = mbar_wait_warp(accf_bar(buf), use & 1u, abort_flag, err, 3);
         if (ks == 1 && !got) break;
         // split K: every epilogue warp learns whether any gave up before the
         // named barriers of the split arrival
         if (ks > 1 && epi_any<C::kEpiWarps * 32>(!got)) break;
         tc_fence_after();
+        auto hand_back = [&]() {
+          tc_fence_before();
+          __syncwarp();
+          // (relaxed: the reads are complete; the stores of the earlier
+          // chunks need not be)
+          if (lane == 0) mbar_arrive_relaxed(acce_bar(buf));
+        };
+        if (LIN != 0 && ks == 1) {
+          // the operands of a chunk are fetched while the previous one is
+          // worked on, and (forward) its accumulators read
+          const int64_t r0 = m0 + 32 * q;
+          const uint32_t tb = lane_base + buf * BN;
+          uint32_t r[32];
+          FP8K_TMEM_LD_X32(tb + (uint32_t)c0, r);
+          tmem_ld_wait();
+          FP8K_REG_FENCE32(r);
 #pragma unroll 1
-        for (int c = 0; c < BN; c += 32) {
+          for (int c = c0; c < c0 + C::kEpiCols; c += 32) {
+            const RowIn cur = in;
+            const bool last = c + 32 == c0 + C::kEpiCols;
+            if (!last) fetch(r0, n0 + c + 32);
+            finish(r0, n0 + c, r, alpha, cur, [&]() {
+              if (last)
+                hand_back();
+              else if (LIN == 1)
+                FP8K_TMEM_LD_X32(tb + (uint32_t)c + 32u, r);
+            });
+            if (!last) {
+              if constexpr (LIN == 2) FP8K_TMEM_LD_X32(tb + (uint32_t)c + 32u, r);
+              tmem_ld_wait();
+              FP8K_REG_FENCE32(r);
+            }
+          }
+          continue;
+        }
+#pragma unroll 1
+        for (int c = c0; c < c0 + C::kEpiCols; c += 32) {
           uint32_t r[32];
           FP8K_TMEM_LD_X32(lane_base + buf * BN + (uint32_t)c, r);
           tmem_ld_wait();
-          if (c + 32 == BN) {  // accumulator fully read: hand it back to the MMA
-            tc_fence_before();
-            __syncwarp();
-            // (relaxed: the reads are complete; the stores of the earlier
-            // chunks need not be)
-            if (lane == 0) mbar_arrive_relaxed(acce_bar(buf));
-          }
+          if (c + 32 == c0 + C::kEpiCols) hand_back();  // accumulator fully read
           float v[32];
           if (ks == 1) {
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]) * alpha;
-            const RowIn cur = in;
-            if (c + 32 < BN) fetch(row, n0 + c + 32);
-            finish(row, n0 + c, v, cur);
+            store_row32(args, row, n0 + c, v);
           } else {
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
@@ -668,20 +715,25 @@ __global__ void __launch_bounds__(Cfg<MODE, BN, STAGES>::kThreads, 1)
         }
         if (ks == 1 && !ok) break;
         if (ks > 1 && epi_any<C::kEpiWarps * 32>(!ok)) break;
+        auto promoted = [&](int64_t c, float (&x)[32]) {
+          if constexpr (LIN != 0) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 16)
+              linear_part16(args, epp.e, row, c + i, *reinterpret_cast<float(*)[16]>(x + i));
+          }
+        };
         float v[32];
 #pragma unroll
         for (int i = 0; i < 32; ++i) v[i] = acc[i];
-        if (ks == 1) {
-          fetch(row, n0 + h * 64);
-          finish(row, n0 + h * 64, v, in);
-        } else if (csplit) stash_partial32_bn<BN>(part, 32 * q + lane, h * 64, v);
+        if (LIN != 0 && ks == 1) promoted(n0 + h * 64, v);
+        else if (ks == 1) store_row32(args, row, n0 + h * 64, v);
+        else if (csplit) stash_partial32_bn<BN>(part, 32 * q + lane, h * 64, v);
         else store_partial32(args, split, row, n0 + h * 64, v);
 #pragma unroll
         for (int i = 0; i < 32; ++i) v[i] = acc[32 + i];
-        if (ks == 1) {
-          fetch(row, n0 + h * 64 + 32);
-          finish(row, n0 + h * 64 + 32, v, in);
-        } else if (csplit) stash_partial32_bn<BN>(part, 32 * q + lane, h * 64 + 32, v);
+        if (LIN != 0 && ks == 1) promoted(n0 + h * 64 + 32, v);
+        else if (ks == 1) store_row32(args, row, n0 + h * 64 + 32, v);
+        else if (csplit) stash_partial32_bn<BN>(part, 32 * q + lane, h * 64 + 32, v);
         else store_partial32(args, split, row, n0 + h * 64 + 32, v);
         if (ks > 1 && !csplit && finish_split(t))
           reduce_split_tile(args, m0, n0, C::BM, BN, 1.0f, (int)threadIdx.x - 64,
@@ -701,21 +753,20 @@ __global__ void __launch_bounds__(Cfg<MODE, BN, STAGES>::kThreads, 1)
       if constexpr (MODE == kScaleTensor)
         alpha = *static_cast<const float *>(args.sa) * *static_cast<const float *>(args.sb);
       if constexpr (MODE == kScaleMx) alpha = mx_alpha(args);
-      const ScaleDiv qd = ep_scale();
-      cluster_reduce<BN>(args, part, m0, n0, C::BM, alpha, cluster_ctarank(), ks,
-                         (int)threadIdx.x, C::kThreads,
-                         [&](int64_t row, int64_t col, int n, float (&v)[4]) {
-                           if constexpr (EPI)
-                             linear4(args, epp.e, row, col, n, v, qd, key);
-                           else
-                             store4(args, row, col, n, v);
-                         });
+      auto reduce = [&](const auto &put) {
+        cluster_reduce<BN>(args, part, m0, n0, C::BM, alpha, cluster_ctarank(), ks,
+                           (int)threadIdx.x, C::kThreads, put);
+      };
+      if constexpr (LIN != 0)
+        reduce(LinearPut{args, epp.e, CodeScale(epp.e), amax});
+      else
+        reduce(StorePut{args});
     }
     cluster_sync();  // no CTA leaves while a peer may still read its partial
   }
   tc_fence_before();
   __syncthreads();
-  if constexpr (EPI) flush_amax(epp.e, key);
+  if constexpr (LIN != 0) flush_amax(epp.e, amax);
   // a multicast pair leaves together: no CTA exits while the other may still
   // write into its shared memory
   if constexpr (MC == 2) cluster_sync();
@@ -724,10 +775,10 @@ __global__ void __launch_bounds__(Cfg<MODE, BN, STAGES>::kThreads, 1)
 
 // Clusters of `size` CTAs of a GEMM kernel variant that can be resident at
 // once.
-template <int MODE, int BN, int STAGES, int MC = 1, bool EPI = false>
+template <int MODE, int BN, int STAGES, int MC = 1, int LIN = 0>
 static int active_clusters(int size) {
-  using C = Cfg<MODE, BN, STAGES>;
-  auto kern = gemm_kernel<MODE, BN, STAGES, false, MC, EPI>;
+  using C = Cfg<MODE, BN, STAGES, LIN>;
+  auto kern = gemm_kernel<MODE, BN, STAGES, false, MC, LIN>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem) !=
       cudaSuccess)
     return 0;
@@ -746,11 +797,11 @@ static int active_clusters(int size) {
   return cudaOccupancyMaxActiveClusters(&n, kern, &cfg) == cudaSuccess ? n : 0;
 }
 
-template <int MODE, int BN, int STAGES, bool EXPERTS = false, int MC = 1, bool EPI = false>
+template <int MODE, int BN, int STAGES, bool EXPERTS = false, int MC = 1, int LIN = 0>
 static cudaError_t run(const CUtensorMap &tma, const CUtensorMap &tmb, const GemmArgs &args,
-                       int sms, cudaStream_t st, const EpParam<EPI> &epp = {}) {
-  using C = Cfg<MODE, BN, STAGES>;
-  auto kern = gemm_kernel<MODE, BN, STAGES, EXPERTS, MC, EPI>;
+                       int sms, cudaStream_t st, const EpParam<LIN != 0> &epp = {}) {
+  using C = Cfg<MODE, BN, STAGES, LIN>;
+  auto kern = gemm_kernel<MODE, BN, STAGES, EXPERTS, MC, LIN>;
   if (EXPERTS != (args.experts > 0)) return cudaErrorInvalidValue;
   if (MC == 2 && (args.ksplit != 1 || args.cluster_split || args.b_mn)) return cudaErrorInvalidValue;
   // the shared-memory opt-in is set once per device (not inside a capture)
@@ -763,7 +814,7 @@ static cudaError_t run(const CUtensorMap &tma, const CUtensorMap &tmb, const Gem
   if (!attr_done[dev]) {
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
     if (e != cudaSuccess) return e;
-    if (MC == 2) mc_clusters[dev] = active_clusters<MODE, BN, STAGES, MC, EPI>(2);
+    if (MC == 2) mc_clusters[dev] = active_clusters<MODE, BN, STAGES, MC, LIN>(2);
     attr_done[dev] = true;
   }
   // (expert-grouped rows: at most one partial row tile per expert more)

@@ -72,7 +72,8 @@ struct PairCfg {
   static constexpr int kNumBars = 2 * STAGES + 2 * kAccBufs + 1;
   // TMA-store staging: per epilogue warp two 32-row x 128-byte boxes
   static constexpr uint32_t kOutBox = 32 * 128;
-  static constexpr uint32_t kOutBytes = EW == 4 ? kEpiWarps * 2 * kOutBox : 0;  // EW 8: linear epilogues
+  // (eight epilogue warps: one 4 KB stage each, linear_epilogue.cuh)
+  static constexpr uint32_t kOutBytes = EW == 4 ? EW * 2 * kOutBox : EW * kEpStageBytes;
   static constexpr uint32_t kSmem = 1024 + kTileBytes + kOutBytes + 8 * kNumBars + 16;
   static_assert(kTmemCols <= 512, "TMEM budget");
   static_assert(kSmem <= 227 * 1024, "shared-memory budget");
@@ -406,40 +407,53 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<BN, STAGES, 
     const uint32_t acce_leader0 = mapa_shared(acce_bar(0), 0);
     const GemmArgs &a = grp.args[0];
     const LinearEp &e = epp.e;
+    uint8_t *stage = out_stage + (warp - 2) * kEpStageBytes;
     const float alpha = *static_cast<const float *>(a.sa) * *static_cast<const float *>(a.sb);
-    const ScaleDiv d = epilogue_scale(e);
-    uint32_t key = 0, j = 0;
+    const CodeScale d(e);
+    float amax = 0.0f;
+    uint32_t j = 0;
     for (int64_t gt = pair; gt < num_tiles; gt += npairs, ++j) {
       const TileRef tr = tile_ref(gt);
       const int64_t row0 = tr.m0 + rank * C::BM + 32 * q, n0 = tr.n0 + col0;
       const uint32_t buf = j & 1u, use = j >> 1;
       RowIn in;
-      fetch_row32<kGrad>(a, e, row0 + lane, n0, in);
+      fetch_chunk<kGrad>(a, e, row0, n0, stage, in);
       if (!mbar_wait_warp(accf_bar(buf), use & 1u, abort_flag, err, 3)) break;
       tc_fence_after();
+      // the operands of a chunk are fetched while the previous one is worked
+      // on, and (forward) its accumulators read
+      uint32_t r[32];
+      FP8K_TMEM_LD_X32(lane_base + buf * BN, r);
+      tmem_ld_wait();
+      FP8K_REG_FENCE32(r);
 #pragma unroll 1
       for (int c = 0; c < kCols; c += 32) {
-        uint32_t r[32];
-        FP8K_TMEM_LD_X32(lane_base + buf * BN + (uint32_t)c, r);
+        const bool last = c + 32 == kCols;
         const RowIn cur = in;
-        if (c + 32 < kCols) fetch_row32<kGrad>(a, e, row0 + lane, n0 + c + 32, in);
-        tmem_ld_wait();
-        if (c + 32 == kCols) {  // this warp's columns are read out
+        if (!last) fetch_chunk<kGrad>(a, e, row0, n0 + c + 32, stage, in);
+        float v[32];
+        if constexpr (!kGrad) scale_bias(a, n0 + c, r, alpha, v);
+        if (last) {  // this warp's columns are read out
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive_cluster_relaxed(acce_leader0 + 8u * buf);
+        } else {
+          if constexpr (!kGrad) FP8K_TMEM_LD_X32(lane_base + buf * BN + (uint32_t)c + 32u, r);
         }
-        float v[32];
-#pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]) * alpha;
         if constexpr (kGrad)
-          grad_row32(a, e, row0, n0 + c, v, cur, d, key);
+          grad_chunk(a, e, row0, n0 + c, r, alpha, cur, d, stage, amax);
         else
-          linear_row32(a, e, row0 + lane, n0 + c, v, cur, d, key);
+          linear_chunk(a, e, row0, n0 + c, v, cur, d, stage, amax);
+        if (!last) {
+          // (the slopes leave no registers for a second chunk of accumulators)
+          if constexpr (kGrad) FP8K_TMEM_LD_X32(lane_base + buf * BN + (uint32_t)c + 32u, r);
+          tmem_ld_wait();
+          FP8K_REG_FENCE32(r);
+        }
       }
     }
     __syncwarp();
-    flush_amax(e, key);
+    flush_amax(e, amax);
   } else {
     // ------------------------------------------------------ epilogue (both)
     const uint32_t q = warp & 3u;
@@ -636,6 +650,11 @@ int64_t gemm_pair_tiles(int64_t M, int64_t N) {
 bool gemm_pair_eligible(int mode, int64_t M, int64_t N, int sms) {
   if (mode != kScaleTensor) return false;
   return gemm_pair_tiles(M, N) * 4 >= sms / 2;
+}
+
+bool gemm_pair_epilogue_eligible(int mode, int64_t M, int64_t N, int sms) {
+  if (mode != kScaleTensor) return false;
+  return gemm_pair_tiles(M, N) * 2 >= sms / 2;
 }
 
 // Tiles of one problem: gated problems cover BN / 2 output columns per tile.

@@ -323,11 +323,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PromoteCfg<BN, STAGE
         for (int i = 0; i < 32; ++i) v[i] = acc[32 * c + i];
         // (store_row32 itself skips rows past M; expert rows end earlier)
         if constexpr (LINEAR) {
-          // (no operand fetched a chunk ahead: the accumulators hold the registers)
-          RowIn in;
-          fetch_row32<false>(args, epp.e, orow, to.n0 + col0 + 32 * c, in);
-          uint32_t key = 0;  // no codes here
-          linear_row32(args, epp.e, orow, to.n0 + col0 + 32 * c, v, in, ScaleDiv(1.0f), key);
+#pragma unroll
+          for (int h = 0; h < 32; h += 16)
+            linear_part16(args, epp.e, orow, to.n0 + col0 + 32 * c + h,
+                          *reinterpret_cast<float(*)[16]>(v + h));
         } else {
           if (!EXPERTS || orow < to.row_end) store_row32(args, orow, to.n0 + col0 + 32 * c, v);
         }

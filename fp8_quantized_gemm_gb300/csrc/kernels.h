@@ -180,7 +180,8 @@ struct LinearEp {
   uint32_t *q_amax;         // nullable (cleared by the caller)
   float *part;              // nullable, gradient only: [ceil(M / 32)][N] column sums
   int64_t ld_res, ld_pre;
-  int res_vec, pre_vec, q_vec;  // 1: base and pitch allow 16-byte access
+  // 1: base and pitch are multiples of 32 bytes (q_vec: 2, or 1 for 16 bytes)
+  int c_vec, res_vec, pre_vec, q_vec;
 };
 
 // Wait bound the API passes to kernels (fp8_set_option FP8_OPT_WAIT_LIMIT_NS).
@@ -211,9 +212,11 @@ cudaError_t launch_gemm(int mode, const CUtensorMap &tma, const CUtensorMap &tmb
                         const GemmArgs &args, int sms, cudaStream_t st);
 // The same with the linear layer's epilogue (gemm_epilogue.cu): per-tensor
 // scales, FP32 group scales, or block-scale words.
+int gemm_epilogue_tile_n(int mode, int64_t M, int64_t N, int sms);  // gemm_tile_n of it
 cudaError_t launch_gemm_epilogue(int mode, const CUtensorMap &tma, const CUtensorMap &tmb,
-                                 const GemmArgs &args, const LinearEp &ep, int sms,
+                                 const GemmArgs &args, const LinearEp &ep, bool grad, int sms,
                                  cudaStream_t st);
+int gemm_epilogue_ksplit(int64_t M, int64_t N, int64_t K, int sms);  // per-tensor scales
 // Expert-grouped per-K-group GEMM (args.experts > 0) with B tiles `bn` wide.
 cudaError_t launch_gemm_experts(int mode, int bn, const CUtensorMap &tma, const CUtensorMap &tmb,
                                 const GemmArgs &args, int sms, cudaStream_t st);
@@ -221,6 +224,7 @@ cudaError_t launch_gemm_experts(int mode, int bn, const CUtensorMap &tma, const 
 // CTA-pair (cta_group::2) variant of the per-tensor GEMM: 256 x 256 tiles, B
 // staged half per CTA (the B tensor map box has gemm_pair_b_rows() rows).
 bool gemm_pair_eligible(int mode, int64_t M, int64_t N, int sms);
+bool gemm_pair_epilogue_eligible(int mode, int64_t M, int64_t N, int sms);
 constexpr int kMaxGroup = 4;  // problems per grouped launch
 // One launch over `count` independent per-tensor problems (longest K first).
 // tmc[i]: the output tensor map of problem i (read when args[i].tma_store).

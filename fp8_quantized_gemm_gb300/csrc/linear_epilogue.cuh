@@ -1,18 +1,26 @@
-// The linear layer's epilogue, applied to a GEMM's scaled fp32 results before
+// The linear layer's epilogue, applied to a GEMM's fp32 accumulators before
 // they leave the chip:
 //
-//   forward   z = result + bias;  pre <- bf16(z);  y = act(z) + residual;
+//   forward   z = alpha acc + bias;  pre <- bf16(z);  y = act(z) + residual;
 //             c <- y in its type, q <- FP8 codes of y / q_scale, amax <- max |y|
-//   gradient  y = result * act'(pre);  c, q, amax as above;
+//   gradient  y = alpha acc act'(pre);  c, q, amax as above;
 //             bias gradient: column sums of y over 32-row pieces
 //
-// Everything is formed in fp32 and rounded once per stored copy.  A thread
-// holds 32 neighbouring columns of one row (the TMEM lane layout), so its
-// operands are whole 32-byte sectors of that row; they are fetched a chunk
-// ahead as raw words (RowIn) while the accumulator is still being waited for.
+// Everything is formed in fp32 and rounded once per stored copy.  A warp
+// takes a chunk of 32 rows x 32 columns, a lane one row of it (the TMEM lane
+// layout).  Where bases and pitches are multiples of 32 bytes a lane reads and
+// writes its own row, a whole sector per access; the operands of the next chunk
+// are fetched as raw words (RowIn) while this one is worked on.  Any other
+// shape passes through 4 KB of the warp's shared memory (its stage), so that
+// the warp touches one row's 32 neighbouring elements at a time: with a lane
+// per row, each scalar access would touch 32 rows (1000 x 2053 x 2064 with an
+// fp32 residual: 42.5 us that way).
+//
+// The codes take y times the correctly rounded reciprocal of the scale: y
+// already carries the accumulation's rounding, which the quotient's last bit
+// does not sharpen, and the exact quotient costs seven more instructions per
+// element (57 us of 757 on the 16384 x 14336 x 4096 product with codes).
 #pragma once
-
-#include <type_traits>
 
 #include "activation.cuh"
 #include "common.cuh"
@@ -31,203 +39,422 @@ struct EpParam<true> {
   LinearEp e;
 };
 
-// 32 operand values of one row, undecoded: 16 words of bf16 pairs or 32 of fp32.
-struct RowIn {
-  uint32_t w[32];
+constexpr uint32_t kEpStageBytes = 32 * 128;  // per epilogue warp, 16-byte aligned
+
+// The codes' scale: multiply by inv where 1 / s is a normal number, divide
+// otherwise.
+struct CodeScale {
+  float s, inv;
+  bool fast;
+  __device__ __forceinline__ explicit CodeScale(const LinearEp &e) {
+    s = e.q != nullptr ? *e.q_scale : 1.0f;
+    inv = __frcp_rn(s);
+    fast = s >= 0x1p-120f && s <= 0x1p120f;
+  }
+  __device__ __forceinline__ F2 quotient(F2 y) const {
+    if (fast) return y * F2(inv);
+    return each(y, [this](float x) { return __fdiv_rn(x, s); });
+  }
 };
 
-// The row operand of the epilogue: pre (gradient) or residual (forward).
-template <bool GRAD>
-__device__ __forceinline__ void fetch_row32(const GemmArgs &a, const LinearEp &e, int64_t row,
-                                            int64_t col0, RowIn &in) {
-  const bool f32 = !GRAD && e.res_dt == 0;
-  const void *src = GRAD ? static_cast<const void *>(e.pre) : e.res;
-  if (src == nullptr || row >= a.M || col0 >= a.N) return;
-  const int64_t off = row * (GRAD ? e.ld_pre : e.ld_res) + col0;
-  const bool full = col0 + 32 <= a.N && (GRAD ? e.pre_vec : e.res_vec);
-  if (!f32) {
-    const uint16_t *p = static_cast<const uint16_t *>(src) + off;
-    if (full) {
+// 32 bf16 operand values of one row, as pairs.
+struct RowIn {
+  uint32_t w[16];
+};
+
+// Element (r, c) of a 32 x 32 fp32 stage: rows of 128 bytes whose 16-byte
+// units are permuted by the row, so that lanes reading or writing their own
+// rows in 16-byte units and lanes walking along one row both spread over the
+// banks.
+__device__ __forceinline__ uint32_t stage_at(int r, int c) {
+  return (uint32_t)(r * 128 + (((c >> 2) ^ (r & 7)) << 4) + (c & 3) * 4);
+}
+__device__ __forceinline__ void stage_put(uint8_t *stage, const float (&v)[32]) {
+  const int lane = (int)lane_id();
+  __syncwarp();  // earlier readers are done
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint4 u = __ldcs(reinterpret_cast<const uint4 *>(p) + i);
-        in.w[4 * i] = u.x; in.w[4 * i + 1] = u.y; in.w[4 * i + 2] = u.z; in.w[4 * i + 3] = u.w;
-      }
-    } else {
+  for (int u = 0; u < 8; ++u)
+    *reinterpret_cast<float4 *>(stage + stage_at(lane, 4 * u)) =
+        make_float4(v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]);
+  __syncwarp();
+}
+
+// 32 bytes, one sector, per lane (32-byte aligned).  Operands are read once
+// and kept out of L1, what there is of it beside the stages: the bias, which
+// every row reads, then stays there.
+__device__ __forceinline__ void ld_sector(const void *p, uint32_t *w) {
+  asm volatile("ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]),
+                 "=r"(w[6]), "=r"(w[7])
+               : "l"(p)
+               : "memory");
+}
+__device__ __forceinline__ void st_sector(void *p, const uint32_t *w) {
+  asm volatile("st.global.v8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::"r"(w[0]), "r"(w[1]),
+               "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]), "l"(p)
+               : "memory");
+}
+
+// Whether lanes access their own rows of a chunk a sector at a time.
+__device__ __forceinline__ bool direct(const GemmArgs &a, int64_t col0, int vec) {
+  return vec && col0 + 32 <= a.N;
+}
+
+// The paths of unaligned or ragged chunks.  They are unrolled no further than
+// their latency needs: fully unrolled, their registers spilled the aligned
+// path's and cost 2% of the 16384 x 14336 x 4096 products.  rows, cols: the
+// chunk's valid part.
+
+// A 32 x 32 chunk of bf16 (size 2) or fp32 values into the stage, as fp32,
+// row by row along the lanes.
+__device__ __forceinline__ void gather_stage(const void *src, int64_t ld, int size, int rows,
+                                                 int cols, uint8_t *stage) {
+  const int lane = (int)lane_id();
+  __syncwarp();
+#pragma unroll 8
+  for (int r = 0; r < 32; ++r) {
+    float t = 0.0f;
+    if (lane < cols && r < rows)
+      t = size == 2 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(src)[r * ld + lane])
+                    : static_cast<const float *>(src)[r * ld + lane];
+    *reinterpret_cast<float *>(stage + stage_at(r, lane)) = t;
+  }
+  __syncwarp();
+}
+
+// The staged fp32 chunk to bf16 or fp32 rows.
+__device__ __forceinline__ void scatter_stage(void *dst, int64_t ld, int size, int rows,
+                                                  int cols, const uint8_t *stage) {
+  const int lane = (int)lane_id();
+  if (lane >= cols) return;
+#pragma unroll 4
+  for (int r = 0; r < 32; ++r) {
+    if (r >= rows) break;
+    const float x = *reinterpret_cast<const float *>(stage + stage_at(r, lane));
+    if (size == 2)
+      static_cast<__nv_bfloat16 *>(dst)[r * ld + lane] = __float2bfloat16_rn(x);
+    else
+      static_cast<float *>(dst)[r * ld + lane] = x;
+  }
+}
+
+// Staged codes, 32 bytes per row.
+__device__ __forceinline__ void scatter_codes(uint8_t *q, int64_t ld, int rows, int cols,
+                                                  const uint8_t *stage) {
+  const int lane = (int)lane_id();
+  if (lane >= cols) return;
+#pragma unroll 4
+  for (int r = 0; r < 32; ++r)
+    if (r < rows) q[r * ld + lane] = stage[32 * r + lane];
+}
+
+__device__ __forceinline__ int left32(int64_t n) { return n < 32 ? (int)n : 32; }
+
+// Four values of this lane's staged row.
+__device__ __forceinline__ float4 stage_row4(const uint8_t *stage, int u) {
+  return *reinterpret_cast<const float4 *>(stage + stage_at((int)lane_id(), 4 * u));
+}
+
+// The bf16 row operand of the chunk at (row0, col0): pre (gradient) or the
+// residual (forward).  Every lane of the warp calls it, a chunk ahead.
+template <bool GRAD>
+__device__ __forceinline__ void fetch_chunk(const GemmArgs &a, const LinearEp &e, int64_t row0,
+                                            int64_t col0, uint8_t *stage, RowIn &in) {
+  const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(GRAD ? e.pre : e.res);
+  if (src == nullptr || row0 >= a.M || col0 >= a.N || (!GRAD && e.res_dt == 0)) return;
+  const int64_t ld = GRAD ? e.ld_pre : e.ld_res, row = row0 + lane_id();
+  if (direct(a, col0, GRAD ? e.pre_vec : e.res_vec)) {
+    if (row >= a.M) return;
+    ld_sector(src + row * ld + col0, in.w);
+    ld_sector(src + row * ld + col0 + 16, in.w + 8);
+    return;
+  }
+  gather_stage(src + row0 * ld + col0, ld, 2, left32(a.M - row0), left32(a.N - col0), stage);
+#pragma unroll
+  for (int u = 0; u < 8; ++u) {
+    const float4 f = stage_row4(stage, u);
+    in.w[2 * u] = __byte_perm(__float_as_uint(f.x), __float_as_uint(f.y), 0x7632);
+    in.w[2 * u + 1] = __byte_perm(__float_as_uint(f.z), __float_as_uint(f.w), 0x7632);
+  }
+}
+
+__device__ __forceinline__ F2 bf16_pair(uint32_t w) {
+  return F2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+
+// One 32 x 32 chunk to a row-major matrix of T.
+template <typename T>
+__device__ __forceinline__ void put_chunk(const GemmArgs &a, T *dst, int64_t ld, int vec,
+                                          int64_t row0, int64_t col0, const float (&v)[32],
+                                          uint8_t *stage) {
+  const int lane = (int)lane_id();
+  if (direct(a, col0, vec)) {
+    if (row0 + lane >= a.M) return;
+    T *p = dst + (row0 + lane) * ld + col0;
+    if constexpr (sizeof(T) == 2) {
+      uint32_t w[16];
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        const uint32_t lo = col0 + 2 * i < a.N ? p[2 * i] : 0u;
-        const uint32_t hi = col0 + 2 * i + 1 < a.N ? p[2 * i + 1] : 0u;
-        in.w[i] = lo | hi << 16;
+        const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t *>(&h);
       }
-    }
-  } else {
-    const uint32_t *p = static_cast<const uint32_t *>(src) + off;
-    if (full) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint4 u = __ldcs(reinterpret_cast<const uint4 *>(p) + i);
-        in.w[4 * i] = u.x; in.w[4 * i + 1] = u.y; in.w[4 * i + 2] = u.z; in.w[4 * i + 3] = u.w;
-      }
+      st_sector(p, w);
+      st_sector(p + 16, w + 8);
     } else {
+      uint32_t w[32];
 #pragma unroll
-      for (int i = 0; i < 32; ++i) in.w[i] = col0 + i < a.N ? p[i] : 0u;
+      for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(v[i]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) st_sector(p + 8 * i, w + 8 * i);
     }
+    return;
   }
+  stage_put(stage, v);
+  scatter_stage(dst + row0 * ld + col0, ld, (int)sizeof(T), left32(a.M - row0), left32(a.N - col0),
+                stage);
 }
 
-__device__ __forceinline__ float bf16_of(const RowIn &in, int i) {
-  return __uint_as_float(i & 1 ? in.w[i >> 1] & 0xFFFF0000u : in.w[i >> 1] << 16);
-}
-
-// 32 bf16 values of one row
-__device__ __forceinline__ void put_bf16x32(__nv_bfloat16 *dst, bool full, int64_t n,
-                                            const float (&v)[32]) {
-  if (full) {
-    uint32_t w[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-      w[i] = *reinterpret_cast<const uint32_t *>(&h);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      reinterpret_cast<uint4 *>(dst)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 32; ++i)
-      if (i < n) dst[i] = __float2bfloat16_rn(v[i]);
-  }
-}
-
-// c, codes and running max |y| of 32 finished values of one row
-__device__ __forceinline__ void put_row32(const GemmArgs &a, const LinearEp &e, int64_t row,
-                                          int64_t col0, const float (&v)[32], const ScaleDiv &d,
-                                          uint32_t &key) {
-  const bool whole = col0 + 32 <= a.N;
+// c, codes and the running max |y| (a NaN stays one) of a finished chunk.
+__device__ __forceinline__ void put_result(const GemmArgs &a, const LinearEp &e, int64_t row0,
+                                           int64_t col0, const float (&v)[32], const CodeScale &d,
+                                           uint8_t *stage, float &amax) {
   if (a.c != nullptr) {
-    if (a.out_dt == 1) {
-      put_bf16x32(static_cast<__nv_bfloat16 *>(a.c) + row * a.ldc + col0, whole && a.vec_store,
-                  a.N - col0, v);
-    } else {
-      float *dst = static_cast<float *>(a.c) + row * a.ldc + col0;
-      if (whole && a.vec_store) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          reinterpret_cast<float4 *>(dst)[i] =
-              make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-          if (col0 + i < a.N) dst[i] = v[i];
-      }
-    }
+    if (a.out_dt == 1)
+      put_chunk(a, static_cast<__nv_bfloat16 *>(a.c), a.ldc, e.c_vec, row0, col0, v, stage);
+    else
+      put_chunk(a, static_cast<float *>(a.c), a.ldc, e.c_vec, row0, col0, v, stage);
   }
   if (e.q == nullptr) return;
-  if (e.q_amax != nullptr) {
+  const int lane = (int)lane_id();
+  const bool row_in = row0 + lane < a.M;
+  if (e.q_amax != nullptr && row_in) {
+    if (col0 + 32 <= a.N) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i)
-      if (whole || col0 + i < a.N) key = max(key, abs_key(v[i]));
+      for (int i = 0; i < 32; i += 2)
+        asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(amax) : "f"(amax), "f"(fabsf(v[i])), "f"(fabsf(v[i + 1])));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if (col0 + i < a.N) amax = max_nan(amax, fabsf(v[i]));
+    }
   }
-  uint8_t *q = e.q + row * a.N + col0;
   uint2 c[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     float y[8];
-    div8(d, v + 8 * j, y);
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) d.quotient(F2(v[8 * j + i], v[8 * j + i + 1])).get(y[i], y[i + 1]);
     c[j] = pack8(e.q_fmt, y);
   }
-  if (whole && e.q_vec) {
-    reinterpret_cast<uint4 *>(q)[0] = make_uint4(c[0].x, c[0].y, c[1].x, c[1].y);
-    reinterpret_cast<uint4 *>(q)[1] = make_uint4(c[2].x, c[2].y, c[3].x, c[3].y);
+  const uint4 lo = make_uint4(c[0].x, c[0].y, c[1].x, c[1].y), hi = make_uint4(c[2].x, c[2].y, c[3].x, c[3].y);
+  if (direct(a, col0, e.q_vec)) {
+    if (!row_in) return;
+    uint8_t *q = e.q + (row0 + lane) * a.N + col0;
+    if (e.q_vec == 2) {
+      const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+      st_sector(q, w);
+    } else {  // N a multiple of 16 (as a GEMM operand's pitch is), not of 32
+      reinterpret_cast<uint4 *>(q)[0] = lo;
+      reinterpret_cast<uint4 *>(q)[1] = hi;
+    }
+    return;
+  }
+  __syncwarp();
+  reinterpret_cast<uint4 *>(stage)[2 * lane] = lo;
+  reinterpret_cast<uint4 *>(stage)[2 * lane + 1] = hi;
+  __syncwarp();
+  scatter_codes(e.q + row0 * a.N + col0, a.N, left32(a.M - row0), left32(a.N - col0), stage);
+}
+
+// z = alpha acc + bias
+__device__ __forceinline__ void scale_bias(const GemmArgs &a, int64_t col0, const uint32_t (&r)[32],
+                                           float alpha, float (&v)[32]) {
+  const F2 al(alpha);
+  auto acc = [&](int i) { return F2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])); };
+  if (a.bias == nullptr || col0 >= a.N) {
+#pragma unroll
+    for (int i = 0; i < 32; i += 2) (acc(i) * al).get(v[i], v[i + 1]);
+  } else if (col0 + 32 <= a.N && (reinterpret_cast<uintptr_t>(a.bias + col0) & 15u) == 0) {
+    const float4 *b4 = reinterpret_cast<const float4 *>(a.bias + col0);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float4 b = __ldg(b4 + i);
+      fma2(acc(4 * i), al, F2(b.x, b.y)).get(v[4 * i], v[4 * i + 1]);
+      fma2(acc(4 * i + 2), al, F2(b.z, b.w)).get(v[4 * i + 2], v[4 * i + 3]);
+    }
   } else {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      const uint32_t w = (i & 4) ? c[i >> 3].y : c[i >> 3].x;
-      if (col0 + i < a.N) q[i] = (uint8_t)(w >> (8 * (i & 3)));
-    }
+    for (int i = 0; i < 32; ++i)
+      v[i] = fmaf(__uint_as_float(r[i]), alpha, col0 + i < a.N ? __ldg(a.bias + col0 + i) : 0.0f);
   }
 }
 
-// Forward epilogue of 32 columns of one row (v: the scaled results; in: the
-// residual of fetch_row32).
-__device__ __forceinline__ void linear_row32(const GemmArgs &a, const LinearEp &e, int64_t row,
+// Forward epilogue of one chunk (v: z of this lane's row; in: the residual of
+// fetch_chunk).  Every lane of the warp calls it.
+__device__ __forceinline__ void linear_chunk(const GemmArgs &a, const LinearEp &e, int64_t row0,
                                              int64_t col0, float (&v)[32], const RowIn &in,
-                                             const ScaleDiv &d, uint32_t &key) {
-  if (row >= a.M || col0 >= a.N) return;
-  if (a.bias != nullptr) {
-    if (col0 + 32 <= a.N && (reinterpret_cast<uintptr_t>(a.bias + col0) & 15u) == 0) {
-      const float4 *b4 = reinterpret_cast<const float4 *>(a.bias + col0);
+                                             const CodeScale &d, uint8_t *stage, float &amax) {
+  if (row0 >= a.M || col0 >= a.N) return;
+  if (e.pre != nullptr)
+    put_chunk(a, static_cast<__nv_bfloat16 *>(e.pre), e.ld_pre, e.pre_vec, row0, col0, v, stage);
+  with_act(e.act, [&](auto act) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float4 b = __ldg(b4 + i);
+    for (int i = 0; i < 32; i += 2)
+      act_value2<decltype(act)::value>(F2(v[i], v[i + 1])).get(v[i], v[i + 1]);
+  });
+  if (e.res != nullptr && e.res_dt == 0) {
+    // fp32: too many registers to hold a chunk ahead
+    const float *src = static_cast<const float *>(e.res);
+    if (direct(a, col0, e.res_vec)) {
+      if (row0 + lane_id() < a.M) {
+#pragma unroll
+        for (int h = 0; h < 32; h += 16) {
+          uint32_t w[16];
+          const float *p = src + (row0 + lane_id()) * e.ld_res + col0 + h;
+          ld_sector(p, w);
+          ld_sector(p + 8, w + 8);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[h + i] += __uint_as_float(w[i]);
+        }
+      }
+    } else {
+      gather_stage(src + row0 * e.ld_res + col0, e.ld_res, 4, left32(a.M - row0),
+                   left32(a.N - col0), stage);
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const float4 f = stage_row4(stage, u);
+        v[4 * u] += f.x; v[4 * u + 1] += f.y; v[4 * u + 2] += f.z; v[4 * u + 3] += f.w;
+      }
+    }
+  } else if (e.res != nullptr) {
+#pragma unroll
+    for (int i = 0; i < 32; i += 2)
+      (F2(v[i], v[i + 1]) + bf16_pair(in.w[i / 2])).get(v[i], v[i + 1]);
+  }
+  put_result(a, e, row0, col0, v, d, stage, amax);
+}
+
+// Gradient epilogue of one chunk (r: the accumulators of this lane's row; in:
+// pre); its 32 rows' column sums go to
+// part[row0 / 32][col0 ...], through the stage: lane l adds 16 rows of the
+// columns 2 (l % 16) and the next, then the two halves of the warp add up.
+__device__ __forceinline__ void grad_chunk(const GemmArgs &a, const LinearEp &e, int64_t row0,
+                                           int64_t col0, const uint32_t (&r)[32], float alpha,
+                                           const RowIn &in, const CodeScale &d, uint8_t *stage,
+                                           float &amax) {
+  if (row0 >= a.M || col0 >= a.N) return;
+  const int lane = (int)lane_id();
+  const F2 al(alpha);
+  float v[32];
+  if (row0 + lane < a.M) {
+    auto scaled = [&](int i) { return F2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])) * al; };
+    // (alpha applied here, pair by pair: as a pass of its own it cost 8 us of
+    // 41 at 2048 x 5120 x 1024, the registers of a second set of values)
+    with_act<true>(e.act, [&](auto act) {
+#pragma unroll
+      for (int i = 0; i < 32; i += 2)
+        (scaled(i) * act_slope2<decltype(act)::value>(bf16_pair(in.w[i / 2]))).get(v[i], v[i + 1]);
+    });
+  } else {  // a row past M adds nothing to the sums
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = 0.0f;
+  }
+  __syncwarp();
+  put_result(a, e, row0, col0, v, d, stage, amax);
+  if (e.part == nullptr) return;
+  stage_put(stage, v);
+  F2 sum(0.0f);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const float2 p = *reinterpret_cast<const float2 *>(
+        stage + stage_at(16 * (lane >> 4) + i, 2 * (lane & 15)));
+    sum = sum + F2(p.x, p.y);
+  }
+  float s0, s1;
+  sum.get(s0, s1);
+  s0 += __shfl_xor_sync(0xffffffffu, s0, 16);
+  s1 += __shfl_xor_sync(0xffffffffu, s1, 16);
+  const int64_t col = col0 + 2 * (lane & 15) + (lane >> 4);  // each half writes one of the pair
+  if (col < a.N) e.part[(row0 >> 5) * a.N + col] = lane < 16 ? s0 : s1;
+}
+
+// Forward epilogue of 16 columns of this lane's row, bf16 c and no codes: for
+// the kernels that keep a tile's accumulators in registers (FP32 group
+// scales), which leave no room for a 32-column chunk and its operands.
+// Unaligned rows take scalar accesses.
+__device__ __forceinline__ void linear_part16(const GemmArgs &a, const LinearEp &e, int64_t row,
+                                              int64_t col0, float (&v)[16]) {
+  if (row >= a.M || col0 >= a.N) return;
+  const bool whole = col0 + 16 <= a.N;
+  const int n = whole ? 16 : (int)(a.N - col0);
+  const __nv_bfloat16 *rb = static_cast<const __nv_bfloat16 *>(e.res) + row * e.ld_res + col0;
+  const float *rf = static_cast<const float *>(e.res) + row * e.ld_res + col0;
+  const bool res_b = e.res != nullptr && e.res_dt == 1;
+  uint32_t w[8];
+  if (res_b) {
+    if (whole && e.res_vec) {
+      ld_sector(rb, w);
+    } else {
+      const uint16_t *p = reinterpret_cast<const uint16_t *>(rb);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        w[i] = (2 * i < n ? p[2 * i] : 0u) | (2 * i + 1 < n ? (uint32_t)p[2 * i + 1] << 16 : 0u);
+    }
+  }
+  if (a.bias != nullptr) {
+    if (whole && (reinterpret_cast<uintptr_t>(a.bias + col0) & 15u) == 0) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float4 b = __ldg(reinterpret_cast<const float4 *>(a.bias + col0) + i);
         v[4 * i] += b.x; v[4 * i + 1] += b.y; v[4 * i + 2] += b.z; v[4 * i + 3] += b.w;
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < 32; ++i)
-        if (col0 + i < a.N) v[i] += __ldg(a.bias + col0 + i);
+      for (int i = 0; i < 16; ++i)
+        if (i < n) v[i] += __ldg(a.bias + col0 + i);
     }
   }
-  if (e.pre != nullptr)
-    put_bf16x32(static_cast<__nv_bfloat16 *>(e.pre) + row * e.ld_pre + col0,
-                col0 + 32 <= a.N && e.pre_vec, a.N - col0, v);
-  with_act(e.act, [&](auto act) {
+  auto put = [&](void *base, int64_t ld, int vec) {
+    __nv_bfloat16 *p = static_cast<__nv_bfloat16 *>(base) + row * ld + col0;
+    if (whole && vec) {
+      uint32_t o[8];
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = act_value<decltype(act)::value>(v[i]);
-  });
-  if (e.res != nullptr) {
-    if (e.res_dt == 0) {
-#pragma unroll
-      for (int i = 0; i < 32; ++i) v[i] += __uint_as_float(in.w[i]);
+      for (int i = 0; i < 8; ++i) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+        o[i] = *reinterpret_cast<const uint32_t *>(&h);
+      }
+      st_sector(p, o);
     } else {
 #pragma unroll
-      for (int i = 0; i < 32; ++i) v[i] += bf16_of(in, i);
+      for (int i = 0; i < 16; ++i)
+        if (i < n) p[i] = __float2bfloat16_rn(v[i]);
     }
+  };
+  if (e.pre != nullptr) put(e.pre, e.ld_pre, e.pre_vec);
+  with_act(e.act, [&](auto act) {
+#pragma unroll
+    for (int i = 0; i < 16; i += 2)
+      act_value2<decltype(act)::value>(F2(v[i], v[i + 1])).get(v[i], v[i + 1]);
+  });
+  if (res_b) {
+#pragma unroll
+    for (int i = 0; i < 16; i += 2) (F2(v[i], v[i + 1]) + bf16_pair(w[i / 2])).get(v[i], v[i + 1]);
+  } else if (e.res != nullptr) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (i < n) v[i] += rf[i];
   }
-  put_row32(a, e, row, col0, v, d, key);
-}
-
-// Gradient epilogue.  Every lane of the warp calls it (rows row0 + lane); the
-// sums of the warp's 32 rows go to part[row0 / 32][col0 + lane] by a
-// transposing reduction: at each of five steps a lane passes on the half of
-// its columns that it does not keep.
-__device__ __forceinline__ void grad_row32(const GemmArgs &a, const LinearEp &e, int64_t row0,
-                                           int64_t col0, float (&v)[32], const RowIn &in,
-                                           const ScaleDiv &d, uint32_t &key) {
-  const uint32_t lane = lane_id();
-  const int64_t row = row0 + lane;
-  if (row0 >= a.M || col0 >= a.N) return;  // the same for the whole warp
-  if (row < a.M) {
-    with_act(e.act, [&](auto act) {
-#pragma unroll
-      for (int i = 0; i < 32; ++i) v[i] *= act_slope<decltype(act)::value>(bf16_of(in, i));
-    });
-    put_row32(a, e, row, col0, v, d, key);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = 0.0f;
-  }
-  if (e.part == nullptr) return;
-  __syncwarp();
-#pragma unroll
-  for (int h = 16; h > 0; h >>= 1) {
-    const bool upper = (lane & h) != 0;
-#pragma unroll
-    for (int i = 0; i < h; ++i) {
-      const float give = upper ? v[i] : v[i + h];
-      const float keep = upper ? v[i + h] : v[i];
-      v[i] = keep + __shfl_xor_sync(0xffffffffu, give, h);
-    }
-  }
-  if (col0 + lane < a.N) e.part[(row0 >> 5) * a.N + col0 + lane] = v[0];
+  put(a.c, a.ldc, e.c_vec);
 }
 
 // pre, activation and residual of one value z = result + bias: returns y.
 __device__ __forceinline__ float linear_value(const LinearEp &e, int64_t row, int64_t col, float z) {
   if (e.pre != nullptr)
     static_cast<__nv_bfloat16 *>(e.pre)[row * e.ld_pre + col] = __float2bfloat16_rn(z);
-  with_act(e.act, [&](auto act) { z = act_value<decltype(act)::value>(z); });
+  with_act(e.act, [&](auto act) {
+    float unused;
+    act_value2<decltype(act)::value>(F2(z)).get(z, unused);
+  });
   if (e.res != nullptr) {
     const int64_t at = row * e.ld_res + col;
     z += e.res_dt == 0 ? static_cast<const float *>(e.res)[at]
@@ -236,39 +463,112 @@ __device__ __forceinline__ float linear_value(const LinearEp &e, int64_t row, in
   return z;
 }
 
-// Forward epilogue of up to four columns of one row (the split-K reductions).
-__device__ __forceinline__ void linear4(const GemmArgs &a, const LinearEp &e, int64_t row,
-                                        int64_t col, int n, float (&v)[4], const ScaleDiv &d,
-                                        uint32_t &key) {
+// Forward epilogue of up to four columns of one row, the last step of
+// cluster_reduce; the residual is loaded with the partial sums.
+struct LinearPut {
+  const GemmArgs &a;
+  const LinearEp &e;
+  const CodeScale d;
+  float &amax;
+  struct In {
+    float r[4];
+  };
+  // address of four elements that may be accessed as one vector
+  static __device__ __forceinline__ bool whole(const void *p, int n, uintptr_t bytes) {
+    return n == 4 && (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0;
+  }
+  __device__ __forceinline__ In load(int64_t row, int64_t col, int n) const {
+    In in = {{0.0f, 0.0f, 0.0f, 0.0f}};
+    if (e.res == nullptr) return in;
+    const int64_t at = row * e.ld_res + col;
+    if (e.res_dt == 0) {
+      const float *p = static_cast<const float *>(e.res) + at;
+      if (whole(p, n, 16)) {
+        const float4 u = *reinterpret_cast<const float4 *>(p);
+        in.r[0] = u.x; in.r[1] = u.y; in.r[2] = u.z; in.r[3] = u.w;
+      } else {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (i >= n) continue;
-    float z = v[i];
-    if (a.bias != nullptr) z += __ldg(a.bias + col + i);
-    z = linear_value(e, row, col + i, z);
-    if (a.c != nullptr) {
-      if (a.out_dt == 1)
-        static_cast<__nv_bfloat16 *>(a.c)[row * a.ldc + col + i] = __float2bfloat16_rn(z);
-      else
-        static_cast<float *>(a.c)[row * a.ldc + col + i] = z;
+        for (int i = 0; i < 4; ++i)
+          if (i < n) in.r[i] = p[i];
+      }
+    } else {
+      const __nv_bfloat16 *p = static_cast<const __nv_bfloat16 *>(e.res) + at;
+      if (whole(p, n, 8)) {
+        const uint2 u = *reinterpret_cast<const uint2 *>(p);
+        bf16_pair(u.x).get(in.r[0], in.r[1]);
+        bf16_pair(u.y).get(in.r[2], in.r[3]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (i < n) in.r[i] = __bfloat162float(p[i]);
+      }
     }
-    if (e.q != nullptr) {
-      key = max(key, abs_key(z));
-      const float y = d.fast ? d.div<true>(z) : d.div<false>(z);
-      e.q[row * a.N + col + i] = (uint8_t)cvt_fp8x2(e.q_fmt, y, 0.0f);
+    return in;
+  }
+  static __device__ __forceinline__ void put_bf16(__nv_bfloat16 *p, int n, const float (&v)[4]) {
+    if (whole(p, n, 8)) {
+      *reinterpret_cast<uint2 *>(p) = f32x4_to_bf16(make_float4(v[0], v[1], v[2], v[3]));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i < n) p[i] = __float2bfloat16_rn(v[i]);
     }
   }
-}
+  __device__ __forceinline__ void operator()(int64_t row, int64_t col, int n, float (&v)[4],
+                                             const In &in) const {
+    if (a.bias != nullptr) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i < n) v[i] += __ldg(a.bias + col + i);
+    }
+    if (e.pre != nullptr)
+      put_bf16(static_cast<__nv_bfloat16 *>(e.pre) + row * e.ld_pre + col, n, v);
+    with_act(e.act, [&](auto act) {
+#pragma unroll
+      for (int i = 0; i < 4; i += 2)
+        act_value2<decltype(act)::value>(F2(v[i], v[i + 1])).get(v[i], v[i + 1]);
+    });
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] += in.r[i];
+    if (a.c != nullptr) {
+      if (a.out_dt == 1) {
+        put_bf16(static_cast<__nv_bfloat16 *>(a.c) + row * a.ldc + col, n, v);
+      } else {
+        float *p = static_cast<float *>(a.c) + row * a.ldc + col;
+        if (whole(p, n, 16)) {
+          *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (i < n) p[i] = v[i];
+        }
+      }
+    }
+    if (e.q == nullptr) return;
+    float y[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < n) amax = max_nan(amax, fabsf(v[i]));
+#pragma unroll
+    for (int i = 0; i < 4; i += 2) d.quotient(F2(v[i], v[i + 1])).get(y[i], y[i + 1]);
+    const uint32_t lo = cvt_fp8x2(e.q_fmt, y[0], y[1]), hi = cvt_fp8x2(e.q_fmt, y[2], y[3]);
+    const uint32_t c = __byte_perm(lo, hi, 0x5410);
+    uint8_t *q = e.q + row * a.N + col;
+    if (whole(q, n, 4)) {
+      *reinterpret_cast<uint32_t *>(q) = c;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i < n) q[i] = (uint8_t)(c >> (8 * i));
+    }
+  }
+};
 
-// The CTA's running max |y| (any warp; every lane calls).
-__device__ __forceinline__ void flush_amax(const LinearEp &e, uint32_t key) {
+// The warp's running max |y| into the call's (every lane calls).
+__device__ __forceinline__ void flush_amax(const LinearEp &e, float amax) {
   if (e.q == nullptr || e.q_amax == nullptr) return;
-  key = warp_max_u32(key);
+  const uint32_t key = warp_max_u32(__float_as_uint(amax));
   if (lane_id() == 0 && key != 0u) atomicMax(e.q_amax, key);
-}
-
-__device__ __forceinline__ ScaleDiv epilogue_scale(const LinearEp &e) {
-  return ScaleDiv(e.q != nullptr ? *e.q_scale : 1.0f);
 }
 
 }  // namespace fp8k

@@ -521,7 +521,7 @@ FP8_API int fp8_gemm_mx(const uint8_t *a, const uint32_t *la, const float *ga, c
  *           before the call (delayed scaling, [Flax] 2.3); q_amax (nullable;
  *           cleared by the call) must not alias q_scale.
  * c may be null when q is given.  Rows are aligned to their element size;
- * 16-byte aligned bases and pitches (and N % 16 == 0 for q) take the vector
+ * bases and pitches of multiples of 32 bytes (for q: of 16) take the vector
  * paths.
  */
 typedef enum {
@@ -574,8 +574,7 @@ FP8_API int fp8_gemm_group_epilogue(const uint8_t *a, const void *sa, const uint
  *   workspace  device scratch for dbias, 16-byte aligned, of at least
  *              fp8_act_backward_workspace(M, N) bytes; calls that can run at
  *              the same time need distinct scratch.
- * The problem has no bias, accumulate 0, no adamw / swiglu.  Runs on CTA pairs
- * whatever the shape. */
+ * The problem has no bias, accumulate 0, no adamw / swiglu. */
 typedef struct {
   int act;
   const void *pre; /* bf16 [M, ld_pre] */

@@ -151,7 +151,8 @@ def group_operands(m, n, k, sfmt):
 
 @pytest.mark.parametrize("m,n,k", [(1, 1, 128), (1, 2048, 7168), (17, 65, 384), (33, 1283, 1024),
                                    (100, 300, 2048), (200, 384, 1024), (300, 1100, 512),
-                                   (2051, 1283, 256), (1500, 2600, 256)])
+                                   (2051, 1283, 256), (1500, 2600, 256),
+                                   (2200, 2600, 384)])
 @pytest.mark.parametrize("sfmt", [0, 1])
 @pytest.mark.parametrize("name,bias,res,pad,pre", [
     ("none", True, "bf16", 0, False), ("silu", False, "f32", 3, True),
