@@ -528,29 +528,31 @@ def _rows(t, shape, dtype, what):
     the given shape and type (None -> NULL)."""
     if t is None:
         return 0, 0
-    if t.shape != shape or t.dtype != dtype or not t.is_cuda:
+    if t.dtype != dtype or t.shape != shape or not t.is_cuda:
         raise ValueError("%s must be a CUDA tensor, %s %s" % (what, dtype, tuple(shape)))
+    if t.is_contiguous():
+        return t.data_ptr(), shape[1]
     ld, step = t.stride()
-    if step != 1 and shape[1] != 1:
+    if (step != 1 and shape[1] != 1) or (ld < shape[1] and shape[0] > 1):
         raise ValueError("%s must have contiguous rows" % what)
-    return t.data_ptr(), ld if shape[0] > 1 and ld >= shape[1] else max(ld, shape[1])
+    return t.data_ptr(), max(ld, shape[1])
 
 
 def _vector(t, n, what):
     """Device pointer of n contiguous fp32 values (None -> 0)."""
     if t is None:
         return 0
-    if t.dtype != _F32 or t.numel() != n:
-        raise ValueError("%s must be fp32 [%d]" % (what, n))
-    return _flat(t)
+    if t.dtype != _F32 or t.numel() != n or not t.is_cuda or not t.is_contiguous():
+        raise ValueError("%s must be contiguous CUDA fp32 [%d]" % (what, n))
+    return t.data_ptr()
 
 
 def _codes(t, n, what):
     if t is None:
         return 0
-    if t.element_size() != 1 or t.numel() != n:
-        raise ValueError("%s must hold %d one-byte codes" % (what, n))
-    return _flat(t)
+    if t.element_size() != 1 or t.numel() != n or not t.is_cuda or not t.is_contiguous():
+        raise ValueError("%s must hold %d contiguous one-byte CUDA codes" % (what, n))
+    return t.data_ptr()
 
 
 def _gain(w, k):

@@ -20,16 +20,12 @@
 
 #include "common.cuh"
 #include "elementwise.cuh"
+#include "pairs.cuh"
 
 namespace fp8k {
 
 enum Act : int { kActNone = 0, kActRelu = 1, kActRelu2 = 2, kActSilu = 3, kActGeluTanh = 4, kActGelu = 5 };
 
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
 // 1 / x; a subnormal result becomes zero (x > 2^126: a vanished logistic value)
 __device__ __forceinline__ float rcp_ftz(float x) {
   float r;
@@ -37,23 +33,6 @@ __device__ __forceinline__ float rcp_ftz(float x) {
   return r;
 }
 
-// A packed pair of fp32 values.
-struct F2 {
-  uint64_t v;
-  __device__ __forceinline__ F2(uint64_t x) : v(x) {}
-  __device__ __forceinline__ F2(float a, float b) : v(f32x2_pack(a, b)) {}
-  __device__ __forceinline__ explicit F2(float a) : v(f32x2_pack(a, a)) {}
-  __device__ __forceinline__ void get(float &a, float &b) const { f32x2_unpack(v, a, b); }
-};
-__device__ __forceinline__ F2 operator*(F2 a, F2 b) { return f32x2_mul(a.v, b.v); }
-__device__ __forceinline__ F2 operator+(F2 a, F2 b) { return f32x2_add(a.v, b.v); }
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) { return f32x2_fma(a.v, b.v, c.v); }
-template <typename Fn>
-__device__ __forceinline__ F2 each(F2 a, Fn &&f) {
-  float x, y;
-  a.get(x, y);
-  return F2(f(x), f(y));
-}
 __device__ __forceinline__ F2 exp2_2(F2 a) { return each(a, [](float x) { return ex2_approx_ftz(x); }); }
 __device__ __forceinline__ F2 rcp_2(F2 a) { return each(a, [](float x) { return rcp_ftz(x); }); }
 __device__ __forceinline__ F2 abs_2(F2 a) { return each(a, [](float x) { return fabsf(x); }); }

@@ -356,6 +356,8 @@ int run_tensor_problem(const fp8_gemm_problem_t &p, cudaStream_t st) {
 // ------------------------------------- linear epilogue and RMS norm calls --
 // SMs the norm gradient's scratch is sized for (more are left idle by it).
 constexpr int kNormSms = 152;
+// Slots for the maxima of the activation gradient's epilogue warps.
+constexpr int64_t kGradTops = 160 * fp8k::kEpWarps;
 
 bool aligned_to(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
@@ -426,7 +428,7 @@ int linear_epilogue(const fp8_linear_epilogue_t &e, int64_t N, const void *c, in
 
 int clear_amax(const fp8k::LinearEp &ep, cudaStream_t st) {
   if (ep.q_amax == nullptr) return FP8_OK;
-  return to_status(cudaMemsetAsync(ep.q_amax, 0, sizeof(uint32_t), st));
+  return to_status(fp8k::launch_clear_word(ep.q_amax, st));
 }
 
 // The per-K-group GEMM, plain (ep null) or with the linear layer's epilogue.
@@ -922,7 +924,8 @@ int fp8_gemm_tensor_epilogue(const fp8_gemm_problem_t *problem,
 }
 
 int64_t fp8_act_backward_workspace(int64_t M, int64_t N) {
-  return M < 1 || N < 1 || M >= kMaxDim || N >= kMaxDim ? 0 : (M + 31) / 32 * N * 4;
+  if (M < 1 || N < 1 || M >= kMaxDim || N >= kMaxDim) return 0;
+  return (M + 31) / 32 * N * 4 + kGradTops * 4;  // column sums, then the warps' maxima
 }
 
 int fp8_gemm_tensor_act_backward(const fp8_gemm_problem_t *problem,
@@ -952,12 +955,19 @@ int fp8_gemm_tensor_act_backward(const fp8_gemm_problem_t *problem,
   DeviceState *d = nullptr;
   if ((rc = device_state(&d)) != FP8_OK) return rc;
   const cudaStream_t st = (cudaStream_t)stream;
-  if ((rc = clear_amax(ep, st)) != FP8_OK) return rc;
+  // the column sums' kernel finishes the maximum too, where there is one
+  const bool pairs = g_use_pairs && fp8k::gemm_pair_epilogue_eligible(fp8k::kScaleTensor, p.M, p.N, d->sms);
+  const int64_t tops = fp8k::gemm_grad_ctas(pairs, p.M, p.N, d->sms) * fp8k::kEpWarps;
+  if (ep.part != nullptr && ep.q_amax != nullptr && tops <= kGradTops)
+    ep.tops = ep.part + (p.M + 31) / 32 * p.N;
+  else if ((rc = clear_amax(ep, st)) != FP8_OK)
+    return rc;
   GemmArgs args = tensor_args(p);
   rc = run_gemm(fp8k::kScaleTensor, p.a, p.b, args, st, &ep, true);
   if (rc != FP8_OK || e.dbias == nullptr) return rc;
   return to_status(fp8k::launch_column_sum(ep.part, (p.M + 31) / 32, p.N, e.accumulate_dbias,
-                                           e.dbias, st));
+                                           e.dbias, ep.tops, (int)tops,
+                                           ep.tops != nullptr ? ep.q_amax : nullptr, st));
 }
 
 int fp8_rmsnorm_quantize(const fp8_rmsnorm_t *norm, fp8_stream_t stream) {
@@ -1003,7 +1013,7 @@ int fp8_rmsnorm_quantize(const fp8_rmsnorm_t *norm, fp8_stream_t stream) {
 
 int64_t fp8_rmsnorm_backward_workspace(int64_t M, int64_t K) {
   if (M < 1 || K < 1 || K % 16 != 0 || K > fp8k::kNormMaxK) return 0;
-  return fp8k::rmsnorm_grad_blocks(M, K, kNormSms) * K * 4;
+  return fp8k::rmsnorm_grad_blocks(M, K, kNormSms) * (K + 1) * 4;  // sums, then maxima
 }
 
 int fp8_rmsnorm_backward(const fp8_rmsnorm_grad_t *grad, fp8_stream_t stream) {
@@ -1039,11 +1049,13 @@ int fp8_rmsnorm_backward(const fp8_rmsnorm_grad_t *grad, fp8_stream_t stream) {
   a.dy = n.dy; a.r = n.r; a.w = n.w; a.dres = n.d_residual; a.inv_rms = n.inv_rms; a.dx = n.dx;
   a.parts = n.dw != nullptr ? static_cast<float *>(n.workspace) : nullptr;
   a.q = n.q; a.scale = n.scale; a.amax = reinterpret_cast<uint32_t *>(n.amax_out);
+  const int sms = d->sms < kNormSms ? d->sms : kNormSms;
+  if (a.parts != nullptr && a.amax != nullptr)
+    a.tops = reinterpret_cast<uint32_t *>(a.parts + fp8k::rmsnorm_grad_blocks(n.M, n.K, sms) * n.K);
   a.M = n.M; a.K = n.K; a.ld_dy = n.ld_dy; a.ld_r = n.ld_r; a.ld_dres = n.ld_dres; a.ld_dx = n.ld_dx;
   a.inv_k = (float)(1.0 / (double)n.K);
   a.fmt = n.fmt; a.w_dt = n.w_dt;
-  return to_status(fp8k::launch_rmsnorm_grad(a, n.dt, n.dy_dt, n.dw, n.accumulate_dw,
-                                             d->sms < kNormSms ? d->sms : kNormSms,
+  return to_status(fp8k::launch_rmsnorm_grad(a, n.dt, n.dy_dt, n.dw, n.accumulate_dw, sms,
                                              (cudaStream_t)stream));
 }
 

@@ -258,7 +258,7 @@ __global__ void __launch_bounds__(Cfg<MODE, BN, STAGES, LIN>::kThreads, 1)
   float amax = 0.0f;
   auto ep_scale = [&]() {
     if constexpr (LIN != 0)
-      return CodeScale(epp.e);
+      return code_scale(epp.e);
     else
       return 0;
   };
@@ -758,7 +758,7 @@ __global__ void __launch_bounds__(Cfg<MODE, BN, STAGES, LIN>::kThreads, 1)
                            (int)threadIdx.x, C::kThreads, put);
       };
       if constexpr (LIN != 0)
-        reduce(LinearPut{args, epp.e, CodeScale(epp.e), amax});
+        reduce(LinearPut{args, epp.e, code_scale(epp.e), amax});
       else
         reduce(StorePut{args});
     }
@@ -766,7 +766,12 @@ __global__ void __launch_bounds__(Cfg<MODE, BN, STAGES, LIN>::kThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if constexpr (LIN != 0) flush_amax(epp.e, amax);
+  if constexpr (LIN != 0) {
+    // (slots for the epilogue warps; with split K every warp has values, and
+    // they go to the call's maximum)
+    if (warp >= 2 || epp.e.tops == nullptr)
+      flush_amax(epp.e, amax, (int64_t)blockIdx.x * kEpWarps + warp - 2);
+  }
   // a multicast pair leaves together: no CTA exits while the other may still
   // write into its shared memory
   if constexpr (MC == 2) cluster_sync();

@@ -275,6 +275,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<BN, STAGES, 
   cluster_sync();  // barrier inits visible to the peer before any remote use
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  if constexpr (LINEAR != 0) {  // launched with programmatic stream serialization
+    launch_dependents();
+    grid_dependency_wait();
+  }
 
   // pair p takes global tiles p, p + npairs, ...; within problem i, local
   // tile t covers rows (t / tiles_n) * 256 (this CTA: + rank * 128) and
@@ -409,7 +413,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<BN, STAGES, 
     const LinearEp &e = epp.e;
     uint8_t *stage = out_stage + (warp - 2) * kEpStageBytes;
     const float alpha = *static_cast<const float *>(a.sa) * *static_cast<const float *>(a.sb);
-    const CodeScale d(e);
+    const CodeScale d = code_scale(e);
     float amax = 0.0f;
     uint32_t j = 0;
     for (int64_t gt = pair; gt < num_tiles; gt += npairs, ++j) {
@@ -453,7 +457,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<BN, STAGES, 
       }
     }
     __syncwarp();
-    flush_amax(e, amax);
+    flush_amax(e, amax, (int64_t)blockIdx.x * EW + (warp - 2));
   } else {
     // ------------------------------------------------------ epilogue (both)
     const uint32_t q = warp & 3u;
@@ -657,6 +661,15 @@ bool gemm_pair_epilogue_eligible(int mode, int64_t M, int64_t N, int sms) {
   return gemm_pair_tiles(M, N) * 2 >= sms / 2;
 }
 
+int64_t gemm_grad_ctas(bool pairs, int64_t M, int64_t N, int sms) {
+  if (pairs) {
+    const int64_t tiles = gemm_pair_tiles(M, N);
+    return 2 * (tiles < sms / 2 ? tiles : sms / 2);
+  }
+  const int64_t tiles = (M + 127) / 128 * ((N + 127) / 128);
+  return tiles < sms ? tiles : sms;
+}
+
 // Tiles of one problem: gated problems cover BN / 2 output columns per tile.
 int64_t gemm_pair_tiles_of(const GemmArgs &a) {
   const int64_t tn = a.gated ? kPairBN / 2 : kPairBN;
@@ -721,8 +734,17 @@ static cudaError_t run_pair_epilogue(const PairGroup &g, const LinearEp &ep, int
   }
   const int64_t tiles = g.tile_begin[g.count];
   const int64_t pairs = tiles < sms / 2 ? tiles : sms / 2;
-  kern<<<(unsigned)(2 * pairs), C::kThreads, C::kSmem, st>>>(g, EpParam<true>{ep});
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3((unsigned)(2 * pairs));
+  cfg.blockDim = dim3(C::kThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, g, EpParam<true>{ep});
 }
 
 cudaError_t launch_gemm_pair_epilogue(const CUtensorMap &tma, const CUtensorMap &tmb,

@@ -167,6 +167,8 @@ struct GemmArgs {
 };
 constexpr int kMaxExperts = 256;
 
+constexpr int kEpWarps = 8;  // epilogue warps of the kernels that take it
+
 // The linear layer's epilogue (linear_epilogue.cuh), beside GemmArgs::bias
 // and GemmArgs::c (nullable with codes).
 struct LinearEp {
@@ -179,6 +181,7 @@ struct LinearEp {
   const float *q_scale;
   uint32_t *q_amax;         // nullable (cleared by the caller)
   float *part;              // nullable, gradient only: [ceil(M / 32)][N] column sums
+  float *tops;              // nullable, with part: [CTAs][kEpWarps] max |y| of each warp
   int64_t ld_res, ld_pre;
   // 1: base and pitch are multiples of 32 bytes (q_vec: 2, or 1 for 16 bytes)
   int c_vec, res_vec, pre_vec, q_vec;
@@ -225,6 +228,8 @@ cudaError_t launch_gemm_experts(int mode, int bn, const CUtensorMap &tma, const 
 // staged half per CTA (the B tensor map box has gemm_pair_b_rows() rows).
 bool gemm_pair_eligible(int mode, int64_t M, int64_t N, int sms);
 bool gemm_pair_epilogue_eligible(int mode, int64_t M, int64_t N, int sms);
+// CTAs of the gradient epilogue's launch, on CTA pairs or not.
+int64_t gemm_grad_ctas(bool pairs, int64_t M, int64_t N, int sms);
 constexpr int kMaxGroup = 4;  // problems per grouped launch
 // One launch over `count` independent per-tensor problems (longest K first).
 // tmc[i]: the output tensor map of problem i (read when args[i].tma_store).

@@ -15,17 +15,13 @@
 // the warp touches one row's 32 neighbouring elements at a time: with a lane
 // per row, each scalar access would touch 32 rows (1000 x 2053 x 2064 with an
 // fp32 residual: 42.5 us that way).
-//
-// The codes take y times the correctly rounded reciprocal of the scale: y
-// already carries the accumulation's rounding, which the quotient's last bit
-// does not sharpen, and the exact quotient costs seven more instructions per
-// element (57 us of 757 on the 16384 x 14336 x 4096 product with codes).
 #pragma once
 
 #include "activation.cuh"
 #include "common.cuh"
 #include "gemm_common.cuh"
 #include "kernels.h"
+#include "pairs.cuh"
 #include "quant_common.cuh"
 
 namespace fp8k {
@@ -39,23 +35,11 @@ struct EpParam<true> {
   LinearEp e;
 };
 
-constexpr uint32_t kEpStageBytes = 32 * 128;  // per epilogue warp, 16-byte aligned
+__device__ __forceinline__ CodeScale code_scale(const LinearEp &e) {
+  return CodeScale(e.q != nullptr ? *e.q_scale : 1.0f);
+}
 
-// The codes' scale: multiply by inv where 1 / s is a normal number, divide
-// otherwise.
-struct CodeScale {
-  float s, inv;
-  bool fast;
-  __device__ __forceinline__ explicit CodeScale(const LinearEp &e) {
-    s = e.q != nullptr ? *e.q_scale : 1.0f;
-    inv = __frcp_rn(s);
-    fast = s >= 0x1p-120f && s <= 0x1p120f;
-  }
-  __device__ __forceinline__ F2 quotient(F2 y) const {
-    if (fast) return y * F2(inv);
-    return each(y, [this](float x) { return __fdiv_rn(x, s); });
-  }
-};
+constexpr uint32_t kEpStageBytes = 32 * 128;  // per epilogue warp, 16-byte aligned
 
 // 32 bf16 operand values of one row, as pairs.
 struct RowIn {
@@ -105,20 +89,33 @@ __device__ __forceinline__ bool direct(const GemmArgs &a, int64_t col0, int vec)
 // path's and cost 2% of the 16384 x 14336 x 4096 products.  rows, cols: the
 // chunk's valid part.
 
-// A 32 x 32 chunk of bf16 (size 2) or fp32 values into the stage, as fp32,
-// row by row along the lanes.
-__device__ __forceinline__ void gather_stage(const void *src, int64_t ld, int size, int rows,
-                                                 int cols, uint8_t *stage) {
+// A 32 x 32 chunk of bf16 values into the stage, as fp32, row by row along the
+// lanes.
+__device__ __forceinline__ void gather_stage(const __nv_bfloat16 *src, int64_t ld, int rows,
+                                             int cols, uint8_t *stage) {
   const int lane = (int)lane_id();
   __syncwarp();
 #pragma unroll 8
   for (int r = 0; r < 32; ++r) {
-    float t = 0.0f;
-    if (lane < cols && r < rows)
-      t = size == 2 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(src)[r * ld + lane])
-                    : static_cast<const float *>(src)[r * ld + lane];
+    const float t = lane < cols && r < rows ? __bfloat162float(src[r * ld + lane]) : 0.0f;
     *reinterpret_cast<float *>(stage + stage_at(r, lane)) = t;
   }
+  __syncwarp();
+}
+// The same of fp32 values: asynchronous copies, all 32 rows in flight (a
+// missing element is filled with zero).
+__device__ __forceinline__ void gather_stage(const float *src, int64_t ld, int rows, int cols,
+                                             uint8_t *stage) {
+  const int lane = (int)lane_id();
+  __syncwarp();
+  for (int r = 0; r < 32; ++r) {
+    const bool in = lane < cols && r < rows;
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(
+                     smem_u32(stage + stage_at(r, lane))),
+                 "l"(in ? src + r * ld + lane : src), "r"(in ? 4 : 0)
+                 : "memory");
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
   __syncwarp();
 }
 
@@ -169,17 +166,13 @@ __device__ __forceinline__ void fetch_chunk(const GemmArgs &a, const LinearEp &e
     ld_sector(src + row * ld + col0 + 16, in.w + 8);
     return;
   }
-  gather_stage(src + row0 * ld + col0, ld, 2, left32(a.M - row0), left32(a.N - col0), stage);
+  gather_stage(src + row0 * ld + col0, ld, left32(a.M - row0), left32(a.N - col0), stage);
 #pragma unroll
   for (int u = 0; u < 8; ++u) {
     const float4 f = stage_row4(stage, u);
     in.w[2 * u] = __byte_perm(__float_as_uint(f.x), __float_as_uint(f.y), 0x7632);
     in.w[2 * u + 1] = __byte_perm(__float_as_uint(f.z), __float_as_uint(f.w), 0x7632);
   }
-}
-
-__device__ __forceinline__ F2 bf16_pair(uint32_t w) {
-  return F2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
 }
 
 // One 32 x 32 chunk to a row-major matrix of T.
@@ -230,8 +223,7 @@ __device__ __forceinline__ void put_result(const GemmArgs &a, const LinearEp &e,
   if (e.q_amax != nullptr && row_in) {
     if (col0 + 32 <= a.N) {
 #pragma unroll
-      for (int i = 0; i < 32; i += 2)
-        asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(amax) : "f"(amax), "f"(fabsf(v[i])), "f"(fabsf(v[i + 1])));
+      for (int i = 0; i < 32; i += 2) amax = max_abs2(amax, F2(v[i], v[i + 1]));
     } else {
 #pragma unroll
       for (int i = 0; i < 32; ++i)
@@ -318,8 +310,8 @@ __device__ __forceinline__ void linear_chunk(const GemmArgs &a, const LinearEp &
         }
       }
     } else {
-      gather_stage(src + row0 * e.ld_res + col0, e.ld_res, 4, left32(a.M - row0),
-                   left32(a.N - col0), stage);
+      gather_stage(src + row0 * e.ld_res + col0, e.ld_res, left32(a.M - row0), left32(a.N - col0),
+                   stage);
 #pragma unroll
       for (int u = 0; u < 8; ++u) {
         const float4 f = stage_row4(stage, u);
@@ -564,11 +556,17 @@ struct LinearPut {
   }
 };
 
-// The warp's running max |y| into the call's (every lane calls).
-__device__ __forceinline__ void flush_amax(const LinearEp &e, float amax) {
+// The warp's running max |y| into the call's, or into its slot where the
+// column sums' kernel finishes it (every lane calls; slot: the warp's index
+// in the grid).
+__device__ __forceinline__ void flush_amax(const LinearEp &e, float amax, int64_t slot) {
   if (e.q == nullptr || e.q_amax == nullptr) return;
   const uint32_t key = warp_max_u32(__float_as_uint(amax));
-  if (lane_id() == 0 && key != 0u) atomicMax(e.q_amax, key);
+  if (lane_id() != 0) return;
+  if (e.tops != nullptr)
+    e.tops[slot] = __uint_as_float(key);
+  else if (key != 0u)
+    atomicMax(e.q_amax, key);
 }
 
 }  // namespace fp8k

@@ -19,6 +19,7 @@
 #include "common.cuh"
 #include "kernels.h"
 #include "norm.h"
+#include "pairs.cuh"
 #include "quant_common.cuh"
 
 namespace fp8k {
@@ -41,26 +42,56 @@ __device__ __forceinline__ float block_sum(float v, float *red) {
   return warp_sum(lane_id() < nw ? red[lane_id()] : 0.0f);
 }
 
-// Round eight values to T, in place, and pack them as stored.
+// The four pairs of a raw vector.
 template <typename T>
-__device__ __forceinline__ Raw8<T> round_pack(float (&v)[8]) {
+__device__ __forceinline__ F2 pair_of(const Raw8<T> &r, int i) {
+  if constexpr (sizeof(T) == 2) {
+    const uint32_t w[4] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w};
+    return bf16_pair(w[i]);
+  } else {
+    const uint4 &u = r.w[i >> 1];
+    return i & 1 ? F2(__uint_as_float(u.z), __uint_as_float(u.w))
+                 : F2(__uint_as_float(u.x), __uint_as_float(u.y));
+  }
+}
+
+// Four pairs rounded to T, as stored.
+template <typename T>
+__device__ __forceinline__ Raw8<T> pack(const F2 (&v)[4]) {
   Raw8<T> r;
   if constexpr (sizeof(T) == 2) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-      w[i] = *reinterpret_cast<const uint32_t *>(&h);
-    }
-    r.w[0] = make_uint4(w[0], w[1], w[2], w[3]);
-    r.decode(v);
+    r.w[0] = make_uint4(to_bf16_pair(v[0]), to_bf16_pair(v[1]), to_bf16_pair(v[2]), to_bf16_pair(v[3]));
   } else {
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-      r.w[i] = make_uint4(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]),
-                          __float_as_uint(v[4 * i + 2]), __float_as_uint(v[4 * i + 3]));
+    for (int i = 0; i < 2; ++i) {
+      float a, b, c, d;
+      v[2 * i].get(a, b);
+      v[2 * i + 1].get(c, d);
+      r.w[i] = make_uint4(__float_as_uint(a), __float_as_uint(b), __float_as_uint(c), __float_as_uint(d));
+    }
   }
   return r;
+}
+
+// x + y, each sum rounded once to T (bf16: packed bf16 additions, exact up to
+// that rounding).
+template <typename T>
+__device__ __forceinline__ Raw8<T> add(const Raw8<T> &x, const Raw8<T> &y) {
+  if constexpr (sizeof(T) == 2) {
+    auto sum = [](uint32_t a, uint32_t b) {
+      const __nv_bfloat162 h = __hadd2_rn(*reinterpret_cast<const __nv_bfloat162 *>(&a),
+                                          *reinterpret_cast<const __nv_bfloat162 *>(&b));
+      return *reinterpret_cast<const uint32_t *>(&h);
+    };
+    Raw8<T> r;
+    r.w[0] = make_uint4(sum(x.w[0].x, y.w[0].x), sum(x.w[0].y, y.w[0].y),
+                        sum(x.w[0].z, y.w[0].z), sum(x.w[0].w, y.w[0].w));
+    return r;
+  } else {
+    const F2 v[4] = {pair_of(x, 0) + pair_of(y, 0), pair_of(x, 1) + pair_of(y, 1),
+                     pair_of(x, 2) + pair_of(y, 2), pair_of(x, 3) + pair_of(y, 3)};
+    return pack<T>(v);
+  }
 }
 
 template <typename T>
@@ -69,38 +100,35 @@ __device__ __forceinline__ void store_raw8(T *p, const Raw8<T> &r) {
   for (int i = 0; i < Raw8<T>::kWords; ++i) reinterpret_cast<uint4 *>(p)[i] = r.w[i];
 }
 
-// Eight gains (w null: ones).  They are re-read per row: K values that stay
-// in L1.
-__device__ __forceinline__ void load_gain8(const void *w, int w_dt, int64_t c, float (&g)[8]) {
+// Eight gains as pairs (w null: ones).  They are re-read per row: K values
+// that stay in L1.
+__device__ __forceinline__ void load_gain8(const void *w, int w_dt, int64_t c, F2 (&g)[4]) {
   if (w == nullptr) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) g[j] = 1.0f;
+    for (int j = 0; j < 4; ++j) g[j] = F2(1.0f);
   } else if (w_dt == 0) {
-    Vec8<__nv_bfloat16>::load(static_cast<const __nv_bfloat16 *>(w) + c, g);
+    const uint4 u = __ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(w) + c));
+    g[0] = bf16_pair(u.x); g[1] = bf16_pair(u.y); g[2] = bf16_pair(u.z); g[3] = bf16_pair(u.w);
   } else {
-    Vec8<float>::load(static_cast<const float *>(w) + c, g);
+    const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(w) + c);
+    const float4 a = __ldg(p), b = __ldg(p + 1);
+    g[0] = F2(a.x, a.y); g[1] = F2(a.z, a.w); g[2] = F2(b.x, b.y); g[3] = F2(b.z, b.w);
   }
 }
 
-__device__ __forceinline__ uint32_t max_key8(const float (&y)[8]) {
-  uint32_t k = abs_key(y[0]);
-#pragma unroll
-  for (int j = 1; j < 8; ++j) k = max(k, abs_key(y[j]));
-  return k;
-}
-
-__device__ __forceinline__ uint2 codes8(const float (&y)[8], const ScaleDiv &d, int fmt) {
+__device__ __forceinline__ uint2 codes8(const F2 (&y)[4], const CodeScale &d, int fmt) {
   float z[8];
-  div8(d, y, z);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) d.quotient(y[j]).get(z[2 * j], z[2 * j + 1]);
   return pack8(fmt, z);
 }
 
 // Codes of eight values under the power of two 2^e.
-__device__ __forceinline__ uint2 codes8_pow2(const float (&y)[8], int e, int fmt) {
-  const float inv = exp2_int(-e);
+__device__ __forceinline__ uint2 codes8_pow2(const F2 (&y)[4], int e, int fmt) {
+  const F2 inv(exp2_int(-e));
   float z[8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) z[j] = __fmul_rn(y[j], inv);
+  for (int j = 0; j < 4; ++j) (y[j] * inv).get(z[2 * j], z[2 * j + 1]);
   return pack8(fmt, z);
 }
 
@@ -110,17 +138,33 @@ __device__ __forceinline__ int ue8m0_exp(float amax, float mx) {
   return amax > 0.0f ? min(max(ceil_log2_pos(__fdiv_rn(amax, mx)), -127), 127) : 0;
 }
 
+// The CTA's max |x|: whole into *slot where one is given, else into *dst,
+// cleared before the launch.
+__device__ __forceinline__ void put_amax(float amax, uint32_t *dst, uint32_t *slot) {
+  if (slot != nullptr) {
+    __shared__ uint32_t top;
+    if (threadIdx.x == 0) top = 0u;
+    __syncthreads();
+    const uint32_t k = warp_max_u32(__float_as_uint(amax));
+    if (lane_id() == 0) atomicMax(&top, k);
+    __syncthreads();
+    if (threadIdx.x == 0) *slot = top;
+  } else {
+    block_max_to(__float_as_uint(amax), dst);
+  }
+}
+
 // ---------------------------------------------------------------- forward --
 template <typename T, int MODE, int V>
-__global__ void __launch_bounds__(V == 4 ? 512 : 1024) rmsnorm_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(1024) rmsnorm_kernel(const NormArgs a) {
   __shared__ float red[2][32];
   launch_dependents();
   grid_dependency_wait();
   const T *x = static_cast<const T *>(a.x), *res = static_cast<const T *>(a.res);
   T *sum = static_cast<T *>(a.sum);
   const float mx = fmt_max(a.fmt);
-  const ScaleDiv dt(MODE == kNormTensor ? *a.scale : 1.0f);
-  uint32_t key = 0;
+  const CodeScale dt(MODE == kNormTensor ? *a.scale : 1.0f);
+  float top = 0.0f;  // kNormTensor: running max |y|
   // the block-scaled layout also holds words for the rows that pad M to 128
   const int64_t rows = MODE == kNormMx ? (a.M + 127) / 128 * 128 : a.M;
 
@@ -148,61 +192,54 @@ __global__ void __launch_bounds__(V == 4 ? 512 : 1024) rmsnorm_kernel(const Norm
         words[g * rows + (row & ~127) + 4 * (row % 32) + (row % 128) / 32] = 0x7F7F7F7Fu;
       continue;
     }
-    float r[V][8];
-    float ss = 0.0f;
+    Raw8<T> r[V];
+    F2 ss(0.0f);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      xr[i].decode(r[i]);
-      if (res != nullptr) {
-        float b[8];
-        rr[i].decode(b);
+      r[i] = res != nullptr ? add(xr[i], rr[i]) : xr[i];
+      if (sum != nullptr && col[i] < a.K) store_raw8(sum + row * a.ld_sum + col[i], r[i]);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) r[i][j] += b[j];
-        const Raw8<T> packed = round_pack<T>(r[i]);
-        if (sum != nullptr && col[i] < a.K) store_raw8(sum + row * a.ld_sum + col[i], packed);
-      } else if (sum != nullptr && col[i] < a.K) {
-        store_raw8(sum + row * a.ld_sum + col[i], xr[i]);
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) ss = fmaf(r[i][j], r[i][j], ss);
+      for (int j = 0; j < 4; ++j) ss = fma2(pair_of(r[i], j), pair_of(r[i], j), ss);
     }
     if (row + gridDim.x < a.M) fetch(row + gridDim.x);
-    const float inv = rsqrtf(fmaf(block_sum(ss, red[phase]), a.inv_k, a.eps));
+    float s0, s1;
+    ss.get(s0, s1);
+    const float inv = rsqrtf(fmaf(block_sum(s0 + s1, red[phase]), a.inv_k, a.eps));
     if (a.inv_rms != nullptr && threadIdx.x == 0) a.inv_rms[row] = inv;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       // (every lane of a warp takes part in the group reductions; a lane past
       // the row's end holds zeros)
-      if constexpr (MODE == kNormTensor) {
-        if (col[i] >= a.K) continue;
-      }
-      float y[8];
-      if (col[i] < a.K) {
+      const bool in = col[i] < a.K;
+      if (MODE == kNormTensor && !in) continue;
+      F2 y[4];
+      if (in) {
         load_gain8(a.w, a.w_dt, col[i], y);
-      } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) y[j] = 0.0f;
+        for (int j = 0; j < 4; ++j) y[j] = (pair_of(r[i], j) * F2(inv)) * y[j];
       }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) y[j] = __fmul_rn(__fmul_rn(r[i][j], inv), y[j]);
-      uint32_t k8 = max_key8(y);
       uint2 c;
       if constexpr (MODE == kNormTensor) {
-        key = max(key, k8);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) top = max_abs2(top, y[j]);
         c = codes8(y, dt, a.fmt);
       } else {
+        float m8 = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) m8 = max_abs2(m8, y[j]);
+        uint32_t k8 = __float_as_uint(m8);
         constexpr int kLanes = MODE == kNormGroup ? 16 : 4;
 #pragma unroll
         for (int o = kLanes / 2; o > 0; o >>= 1)
           k8 = max(k8, __shfl_xor_sync(0xffffffffu, k8, o));
         const float amax = __uint_as_float(k8);
         if constexpr (MODE == kNormGroup) {
-          const bool owner = (threadIdx.x & 15u) == 0 && col[i] < a.K;
+          const bool owner = (threadIdx.x & 15u) == 0 && in;
           const int64_t at = (col[i] >> 7) * a.M + row;
           if (a.sfmt == 0) {
             const float s = scale_from_amax(amax, mx);
             if (owner) static_cast<float *>(a.scales)[at] = s;
-            c = codes8(y, ScaleDiv(s), a.fmt);
+            c = codes8(y, CodeScale(s), a.fmt);
           } else {
             const int e = ue8m0_exp(amax, mx);
             if (owner) static_cast<uint8_t *>(a.scales)[at] = (uint8_t)(e + 127);
@@ -213,21 +250,20 @@ __global__ void __launch_bounds__(V == 4 ? 512 : 1024) rmsnorm_kernel(const Norm
           uint32_t word = (uint32_t)(e + 127) << (8 * ((threadIdx.x >> 2) & 3u));
           word |= __shfl_xor_sync(0xffffffffu, word, 4);
           word |= __shfl_xor_sync(0xffffffffu, word, 8);
-          if ((threadIdx.x & 15u) == 0 && col[i] < a.K)
+          if ((threadIdx.x & 15u) == 0 && in)
             static_cast<uint32_t *>(a.scales)[(col[i] >> 7) * rows + (row & ~127) +
                                               4 * (row % 32) + (row % 128) / 32] = word;
           c = codes8_pow2(y, e, a.fmt);
         }
-        if (col[i] >= a.K) continue;
+        if (!in) continue;
       }
       *reinterpret_cast<uint2 *>(a.q + row * a.K + col[i]) = c;
-      if (a.y != nullptr) {
-        const Raw8<__nv_bfloat16> p = round_pack<__nv_bfloat16>(y);
-        store_raw8(static_cast<__nv_bfloat16 *>(a.y) + row * a.ld_y + col[i], p);
-      }
+      if (a.y != nullptr)
+        store_raw8(static_cast<__nv_bfloat16 *>(a.y) + row * a.ld_y + col[i], pack<__nv_bfloat16>(y));
     }
   }
-  if (MODE == kNormTensor && a.amax != nullptr) block_max_to(key, a.amax);
+  if (MODE == kNormTensor && a.amax != nullptr)
+    put_amax(top, a.amax, gridDim.x == 1 ? a.amax : nullptr);
 }
 
 // --------------------------------------------------------------- backward --
@@ -238,23 +274,19 @@ __global__ void __launch_bounds__(V == 4 ? 512 : 1024) rmsnorm_kernel(const Norm
 template <typename T, typename DY, int V>
 __global__ void __launch_bounds__(512, 1) rmsnorm_grad_kernel(const NormGradArgs a) {
   // next row in flight while this one is reduced, where the registers allow
-  constexpr bool kPrefetch = V * (2 * sizeof(T) + sizeof(DY)) <= 16;
+  constexpr bool kPrefetch = V * (2 * sizeof(T) + sizeof(DY)) <= 24;
   __shared__ float red[2][32];
   launch_dependents();
   grid_dependency_wait();
   const T *r = static_cast<const T *>(a.r), *dres = static_cast<const T *>(a.dres);
   const DY *dy = static_cast<const DY *>(a.dy);
   T *dx = static_cast<T *>(a.dx);
-  const ScaleDiv d(a.q != nullptr ? *a.scale : 1.0f);
-  uint32_t key = 0;
+  const CodeScale d(a.q != nullptr ? *a.scale : 1.0f);
+  float top = 0.0f;  // running max |dx|
   int64_t col[V];
-  float dw[V][8];
+  F2 dw[V][4];
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    col[i] = 8 * ((int64_t)i * blockDim.x + threadIdx.x);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) dw[i][j] = 0.0f;
-  }
+  for (int i = 0; i < V; ++i) col[i] = 8 * ((int64_t)i * blockDim.x + threadIdx.x);
   Raw8<DY> yr[V];
   Raw8<T> rr[V], er[V];
   float inv = 0.0f;
@@ -276,78 +308,101 @@ __global__ void __launch_bounds__(512, 1) rmsnorm_grad_kernel(const NormGradArgs
   if (kPrefetch && row < a.M) fetch(row);
   for (int phase = 0; row < a.M; row += gridDim.x, phase ^= 1) {
     if (!kPrefetch) fetch(row);
-    float g[V][8], xh[V][8];
-    Raw8<T> er0[V];
+    // the row stays in registers as loaded (half the size of its products)
+    Raw8<DY> y0[V];
+    Raw8<T> r0[V], e0[V];
     const float inv0 = inv;
-    float dot = 0.0f;
+    F2 dot(0.0f);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      float t[8];
-      yr[i].decode(t);
-      rr[i].decode(xh[i]);
-      er0[i] = er[i];
-      if (col[i] < a.K) {
-        load_gain8(a.w, a.w_dt, col[i], g[i]);
-      } else {
+      y0[i] = yr[i];
+      r0[i] = rr[i];
+      e0[i] = er[i];
+      if (col[i] >= a.K) continue;
+      F2 g[4];
+      load_gain8(a.w, a.w_dt, col[i], g);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) g[i][j] = 0.0f;
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        xh[i][j] *= inv0;
-        dw[i][j] = fmaf(t[j], xh[i][j], dw[i][j]);
-        g[i][j] *= t[j];
-        dot = fmaf(g[i][j], xh[i][j], dot);
+      for (int j = 0; j < 4; ++j) {
+        const F2 t = pair_of(y0[i], j) * (pair_of(r0[i], j) * F2(inv0));  // dy xhat
+        dw[i][j] = dw[i][j] + t;
+        dot = fma2(t, g[j], dot);
       }
     }
     if (kPrefetch && row + gridDim.x < a.M) fetch(row + gridDim.x);
-    const float c = block_sum(dot, red[phase]) * a.inv_k;
+    float d0, d1;
+    dot.get(d0, d1);
+    const float c = block_sum(d0 + d1, red[phase]) * a.inv_k;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       if (col[i] >= a.K) continue;
-      float e[8];
-      er0[i].decode(e);
+      F2 g[4];
+      load_gain8(a.w, a.w_dt, col[i], g);
+      const F2 mc(-c), i2(inv0);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) e[j] = fmaf(inv0, fmaf(-xh[i][j], c, g[i][j]), e[j]);
+      for (int j = 0; j < 4; ++j)
+        g[j] = fma2(i2, fma2(pair_of(r0[i], j) * i2, mc, pair_of(y0[i], j) * g[j]), pair_of(e0[i], j));
       if (a.q != nullptr) {
-        key = max(key, max_key8(e));
-        *reinterpret_cast<uint2 *>(a.q + row * a.K + col[i]) = codes8(e, d, a.fmt);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) top = max_abs2(top, g[j]);
+        *reinterpret_cast<uint2 *>(a.q + row * a.K + col[i]) = codes8(g, d, a.fmt);
       }
-      store_raw8(dx + row * a.ld_dx + col[i], round_pack<T>(e));
+      store_raw8(dx + row * a.ld_dx + col[i], pack<T>(g));
     }
   }
   if (a.parts != nullptr) {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       if (col[i] >= a.K) continue;
-      float4 *p = reinterpret_cast<float4 *>(a.parts + (int64_t)blockIdx.x * a.K + col[i]);
-      p[0] = make_float4(dw[i][0], dw[i][1], dw[i][2], dw[i][3]);
-      p[1] = make_float4(dw[i][4], dw[i][5], dw[i][6], dw[i][7]);
+      store_raw8(a.parts + (int64_t)blockIdx.x * a.K + col[i], pack<float>(dw[i]));
     }
   }
-  if (a.q != nullptr && a.amax != nullptr) block_max_to(key, a.amax);
+  if (a.q != nullptr && a.amax != nullptr)
+    put_amax(top, a.amax, a.tops != nullptr ? a.tops + blockIdx.x : nullptr);
 }
 
 // out[n] (+)= sum over p < P of parts[p][n], in a fixed order: 32 columns per
 // CTA, warp w adds rows w, w + 32, ..., then the 32 warps' sums are added.
+// The first CTA also finishes a maximum: *top_out = max of tops[0 .. ntops)
+// (keys of non-negative floats; nullable).
 __global__ void __launch_bounds__(1024) column_sum_kernel(const float *__restrict__ parts,
                                                           int64_t P, int64_t N, int accumulate,
-                                                          float *__restrict__ out) {
+                                                          float *__restrict__ out,
+                                                          const uint32_t *__restrict__ tops,
+                                                          int ntops, uint32_t *top_out) {
   __shared__ float s[32][33];
+  __shared__ uint32_t top;
+  if (threadIdx.x == 0) top = 0u;
   launch_dependents();
   grid_dependency_wait();
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int64_t n = (int64_t)blockIdx.x * 32 + lane;
   float acc = 0.0f;
   if (n < N) {
-#pragma unroll 4
+#pragma unroll 8
     for (int64_t p = w; p < P; p += 32) acc += __ldcg(parts + p * N + n);
   }
   s[w][lane] = acc;
   __syncthreads();
+  if (blockIdx.x == 0 && top_out != nullptr) {
+    uint32_t k = 0u;
+    for (int i = threadIdx.x; i < ntops; i += 1024) k = max(k, __ldcg(tops + i));
+    k = warp_max_u32(k);
+    if (lane == 0) atomicMax(&top, k);
+    __syncthreads();
+    if (threadIdx.x == 0) *top_out = top;
+  }
   acc = warp_sum(s[lane][w]);  // column w of this CTA
   const int64_t m = (int64_t)blockIdx.x * 32 + w;
   if (lane == 0 && m < N) out[m] = accumulate ? out[m] + acc : acc;
+}
+
+// *p = 0 between two kernels that are launched with programmatic stream
+// serialization (a memset node would end that chain: 3 us of a call against
+// 1.5).
+__global__ void clear_word_kernel(uint32_t *p) {
+  launch_dependents();
+  grid_dependency_wait();
+  if (threadIdx.x == 0) *p = 0u;
 }
 
 // A launch with programmatic stream serialization (the kernels wait for the
@@ -370,8 +425,13 @@ static cudaError_t launch_serial(void (*kern)(KArgs...), int64_t blocks, int thr
 static int round32(int64_t n) { return (int)((n + 31) / 32 * 32); }
 
 cudaError_t launch_column_sum(const float *parts, int64_t P, int64_t N, int accumulate, float *out,
-                              cudaStream_t st) {
-  return launch_serial(column_sum_kernel, (N + 31) / 32, 1024, st, parts, P, N, accumulate, out);
+                              const float *tops, int ntops, uint32_t *top_out, cudaStream_t st) {
+  return launch_serial(column_sum_kernel, (N + 31) / 32, 1024, st, parts, P, N, accumulate, out,
+                       reinterpret_cast<const uint32_t *>(tops), ntops, top_out);
+}
+
+cudaError_t launch_clear_word(uint32_t *p, cudaStream_t st) {
+  return launch_serial(clear_word_kernel, 1, 32, st, p);
 }
 
 // Vectors per thread of a K-element row: with a row per SM or fewer the row
@@ -380,9 +440,8 @@ cudaError_t launch_column_sum(const float *parts, int64_t P, int64_t N, int accu
 // barrier.
 static int forward_vectors(int64_t M, int64_t K, int sms) {
   const int64_t vecs = K / 8;
-  if (M <= sms) return vecs <= 1024 ? 1 : 2;
-  if (vecs < 64) return 1;
-  return vecs <= 1024 ? 2 : 4;
+  if (vecs > 1024) return 2;
+  return M <= sms || vecs < 64 ? 1 : 2;
 }
 
 template <typename T, int MODE>
@@ -390,19 +449,16 @@ static cudaError_t run_norm(const NormArgs &a, int sms, cudaStream_t st) {
   const int v = forward_vectors(a.M, a.K, sms);
   const int threads = round32((a.K / 8 + v - 1) / v);
   const int64_t rows = MODE == kNormMx ? (a.M + 127) / 128 * 128 : a.M;
-  // resident at once: 1024 threads of 64 registers (V 1, 2), 512 of 128 (V 4)
-  int64_t blocks = (int64_t)sms * max(1, (v == 4 ? 512 : 1024) / threads);
+  // resident at once: 1024 threads of 64 registers
+  int64_t blocks = (int64_t)sms * (1024 / threads);
   if (blocks > rows) blocks = rows;
-  switch (v) {
-    case 1: return launch_serial(rmsnorm_kernel<T, MODE, 1>, blocks, threads, st, a);
-    case 2: return launch_serial(rmsnorm_kernel<T, MODE, 2>, blocks, threads, st, a);
-    default: return launch_serial(rmsnorm_kernel<T, MODE, 4>, blocks, threads, st, a);
-  }
+  return v == 1 ? launch_serial(rmsnorm_kernel<T, MODE, 1>, blocks, threads, st, a)
+                : launch_serial(rmsnorm_kernel<T, MODE, 2>, blocks, threads, st, a);
 }
 
 cudaError_t launch_rmsnorm(const NormArgs &a, int dt, int mode, int sms, cudaStream_t st) {
-  if (a.amax != nullptr) {
-    const cudaError_t e = cudaMemsetAsync(a.amax, 0, sizeof(uint32_t), st);
+  if (a.amax != nullptr && a.M != 1) {  // one row is one CTA, which writes it whole
+    const cudaError_t e = launch_clear_word(a.amax, st);
     if (e != cudaSuccess) return e;
   }
   if (a.M == 0) return cudaSuccess;
@@ -418,7 +474,7 @@ cudaError_t launch_rmsnorm(const NormArgs &a, int dt, int mode, int sms, cudaStr
 
 static int grad_vectors(int64_t K) {
   const int64_t vecs = K / 8;
-  return vecs <= 256 ? 1 : vecs <= 1024 ? 2 : 4;
+  return vecs <= 64 ? 1 : vecs <= 1024 ? 2 : 4;
 }
 
 // CTAs (and rows of dw partials) of the backward pass on `sms` SMs: 512
@@ -443,8 +499,9 @@ static cudaError_t run_norm_grad(const NormGradArgs &a, int64_t blocks, cudaStre
 cudaError_t launch_rmsnorm_grad(const NormGradArgs &a, int dt, int dy_dt, float *dw,
                                 int accumulate, int sms, cudaStream_t st) {
   cudaError_t e = cudaSuccess;
-  if (a.q != nullptr && a.amax != nullptr &&
-      (e = cudaMemsetAsync(a.amax, 0, sizeof(uint32_t), st)) != cudaSuccess)
+  // the maximum: finished by the column sums' kernel, or by atomics
+  if (a.q != nullptr && a.amax != nullptr && (a.M == 0 || a.tops == nullptr) &&
+      (e = launch_clear_word(a.amax, st)) != cudaSuccess)
     return e;
   if (a.M == 0) {
     if (dw != nullptr && !accumulate) return cudaMemsetAsync(dw, 0, (size_t)a.K * 4, st);
@@ -458,7 +515,9 @@ cudaError_t launch_rmsnorm_grad(const NormGradArgs &a, int dt, int dy_dt, float 
     e = dy_dt == 0 ? run_norm_grad<float, __nv_bfloat16>(a, blocks, st)
                    : run_norm_grad<float, float>(a, blocks, st);
   if (e != cudaSuccess || dw == nullptr) return e;
-  return launch_column_sum(a.parts, blocks, a.K, accumulate, dw, st);
+  return launch_column_sum(a.parts, blocks, a.K, accumulate, dw,
+                           reinterpret_cast<const float *>(a.tops), (int)blocks,
+                           a.tops != nullptr ? a.amax : nullptr, st);
 }
 
 }  // namespace fp8k

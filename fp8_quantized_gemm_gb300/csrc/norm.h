@@ -9,7 +9,7 @@ namespace fp8k {
 
 enum NormMode : int { kNormTensor = 0, kNormGroup = 1, kNormMx = 2 };
 
-constexpr int64_t kNormMaxK = 16384;  // four vectors of 8 for each of 512 threads
+constexpr int64_t kNormMaxK = 16384;  // two vectors of 8 for each of 1024 threads
 
 struct NormArgs {
   const void *x, *res, *w;  // res, w nullable
@@ -30,6 +30,7 @@ struct NormGradArgs {
   const float *inv_rms;
   void *dx;
   float *parts;                   // nullable: dw partials [blocks][K]
+  uint32_t *tops;                 // nullable, with parts and amax: max |dx| of each CTA
   uint8_t *q;                     // nullable
   const float *scale;
   uint32_t *amax;                 // nullable
@@ -43,8 +44,10 @@ int64_t rmsnorm_grad_blocks(int64_t M, int64_t K, int sms);
 cudaError_t launch_rmsnorm_grad(const NormGradArgs &a, int dt, int dy_dt, float *dw,
                                 int accumulate, int sms, cudaStream_t st);
 
-// out[n] (+)= sum over p < P of parts[p][n]
+// out[n] (+)= sum over p < P of parts[p][n]; *top_out (nullable) = max of tops
 cudaError_t launch_column_sum(const float *parts, int64_t P, int64_t N, int accumulate, float *out,
-                              cudaStream_t st);
+                              const float *tops, int ntops, uint32_t *top_out, cudaStream_t st);
+// *p = 0, in the programmatic launch chain
+cudaError_t launch_clear_word(uint32_t *p, cudaStream_t st);
 
 }  // namespace fp8k

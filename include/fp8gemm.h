@@ -599,8 +599,9 @@ FP8_API int fp8_gemm_tensor_act_backward(const fp8_gemm_problem_t *problem,
  *   r = x + residual, rounded to the stream's type dt;  sum_out <- r
  *   inv = 1 / sqrt(mean(r^2) + eps);                    inv_rms[m] <- inv
  *   y = (r * inv) * w, in fp32;                         y_out <- bf16(y)
- *   q <- the codes and scales that the quantize call of `mode` gives for the
- *        fp32 tensor y:
+ *   q <- the codes of y and their scales, as the quantize call of `mode` forms
+ *        them for the fp32 tensor y, with y times the rounded reciprocal of a
+ *        scale in the place of the exact quotient:
  *     FP8_NORM_TENSOR  fp8_quantize_tensor with `scale`; amax_out (nullable,
  *                      cleared by the call, not `scale` itself) <- max |y|
  *     FP8_NORM_GROUP   fp8_quantize_token_group: scales [ceil(K/128), M] of

@@ -45,7 +45,7 @@ def test_norm(kw, status):
 def grad(**kw):
     d = dict(dy=P, r=P, w=P, d_residual=P, inv_rms=P, dy_dt=1, dt=0, w_dt=1, M=40, K=256, ld_dy=256,
              ld_r=256, ld_dres=256, ld_dx=256, dx=P, dw=P, accumulate_dw=0, q=P, fmt=1, scale=P,
-             amax_out=P + 16, workspace=P, workspace_bytes=40 * 256 * 4)
+             amax_out=P + 16, workspace=P, workspace_bytes=F.fp8_rmsnorm_backward_workspace(40, 256))
     d.update(kw)
     return call("fp8_rmsnorm_backward", F.RmsNormGrad(**d))
 
@@ -55,7 +55,7 @@ def grad(**kw):
     (dict(dx=None), INVALID), (dict(dy_dt=3), INVALID), (dict(accumulate_dw=2), INVALID),
     (dict(scale=None), INVALID), (dict(amax_out=P), INVALID), (dict(fmt=4), INVALID),
     (dict(q=None), UNSUPPORTED),                       # an amax without codes
-    (dict(workspace=None), INVALID), (dict(workspace_bytes=40 * 256 * 4 - 1), INVALID),
+    (dict(workspace=None), INVALID), (dict(workspace_bytes=F.fp8_rmsnorm_backward_workspace(40, 256) - 1), INVALID),
     (dict(workspace=P + 8), MISALIGNED), (dict(K=250), MISALIGNED), (dict(K=32768), UNSUPPORTED),
     (dict(ld_dx=248), INVALID), (dict(ld_dy=257), MISALIGNED), (dict(dw=P + 1), MISALIGNED)])
 def test_norm_grad(kw, status):
@@ -105,14 +105,14 @@ def test_output_may_be_missing_only_with_codes():
 
 def act_grad(p=None, **kw):
     d = dict(act=4, pre=P, ld_pre=64, q=P, q_fmt=1, q_scale=P, q_amax=P + 16, dbias=P,
-             accumulate_dbias=0, workspace=P, workspace_bytes=2 * 64 * 4)
+             accumulate_dbias=0, workspace=P, workspace_bytes=F.fp8_act_backward_workspace(64, 64))
     d.update(kw)
     return call("fp8_gemm_tensor_act_backward", problem(**dict(bias=None, **(p or {}))),
                 F.ActGradEpilogue(**d))
 
 
 @pytest.mark.parametrize("kw,status", CODES + [
-    (dict(pre=None), INVALID), (dict(workspace=None), INVALID), (dict(workspace_bytes=511), INVALID),
+    (dict(pre=None), INVALID), (dict(workspace=None), INVALID), (dict(workspace_bytes=F.fp8_act_backward_workspace(64, 64) - 1), INVALID),
     (dict(workspace=P + 4), MISALIGNED), (dict(accumulate_dbias=3), INVALID), (dict(dbias=P + 2), MISALIGNED)])
 def test_act_grad(kw, status):
     assert act_grad(**kw) == status
@@ -155,11 +155,12 @@ def test_well_formed_calls_reach_the_device():
 
 
 def test_workspace_sizes():
-    assert F.fp8_act_backward_workspace(1, 16) == 64
-    assert F.fp8_act_backward_workspace(33, 100) == 2 * 100 * 4
+    """At least the partial sums, nothing for an empty or refused shape."""
+    assert F.fp8_act_backward_workspace(33, 100) >= 2 * 100 * 4
     assert F.fp8_act_backward_workspace(0, 16) == 0
-    assert F.fp8_rmsnorm_backward_workspace(3, 256) == 3 * 256 * 4
+    assert F.fp8_rmsnorm_backward_workspace(3, 256) >= 3 * 256 * 4
     assert F.fp8_rmsnorm_backward_workspace(0, 256) == 0
+    assert F.fp8_rmsnorm_backward_workspace(8, 100) == 0
     assert F.fp8_rmsnorm_backward_workspace(1 << 20, 4096) >= 152 * 4096 * 4
 
 
