@@ -267,7 +267,7 @@ int run_gemm(int mode, const uint8_t *a, const uint8_t *b, GemmArgs &args, cudaS
   const int bn = ep != nullptr ? fp8k::gemm_epilogue_tile_n(mode, args.M, args.N, d->sms)
                                : fp8k::gemm_tile_n(mode, args.M, args.N, d->sms);
   args.multicast = g_use_multicast && mode != fp8k::kScaleTensor &&
-                           mode != fp8k::kScaleGroupF32x32 && bn == 128 &&
+                           mode != fp8k::kScaleGroupF32x32 && bn <= 192 &&
                            args.ksplit == 1 && !args.b_mn && args.experts == 0 && args.M > 128
                        ? 1
                        : 0;

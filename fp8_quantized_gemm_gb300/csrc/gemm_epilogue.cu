@@ -9,8 +9,10 @@ namespace fp8k {
 // warp half the epilogue).  Block-scale words: where the plain kernel takes
 // 256-wide tiles (one TMEM accumulator beside the scale factors: the epilogue
 // of a tile and the MMAs of the next take turns), 192-wide ones, two of which
-// fit: 4096 x 7168 x 2048 with bias and silu ran in 73.4 us against 87.8 (78.1
-// with B multicast over two CTAs, which couples their epilogues).
+// fit: 4096 x 7168 x 2048 with bias and silu runs in 57.7 us, B multicast to
+// the two CTAs of a cluster (59.4 without), against 72.1 on 256-wide tiles.
+// With few columns and a deep K (4096 x 2048 x 7168) the two are near: 62.5
+// against 59.9.
 int gemm_epilogue_tile_n(int mode, int64_t M, int64_t N, int sms) {
   const int bn = gemm_tile_n(mode, M, N, sms);
   if (mode == kScaleTensor) return 128;
@@ -30,7 +32,7 @@ cudaError_t launch_gemm_epilogue(int mode, const CUtensorMap &tma, const CUtenso
                   : run<kScaleTensor, 128, 5, false, 1, 1>(tma, tmb, args, sms, st, p);
     case kScaleMx:
       if (gemm_epilogue_tile_n(mode, args.M, args.N, sms) == 192)
-        return mc ? cudaErrorInvalidValue
+        return mc ? run<kScaleMx, 192, 4, false, 2, 1>(tma, tmb, args, sms, st, p)
                   : run<kScaleMx, 192, 4, false, 1, 1>(tma, tmb, args, sms, st, p);
       return mc ? run<kScaleMx, 128, 5, false, 2, 1>(tma, tmb, args, sms, st, p)
                 : run<kScaleMx, 128, 5, false, 1, 1>(tma, tmb, args, sms, st, p);

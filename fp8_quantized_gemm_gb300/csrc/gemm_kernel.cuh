@@ -216,14 +216,27 @@ __global__ void __launch_bounds__(Cfg<MODE, BN, STAGES, LIN>::kThreads, 1)
       // a few A row blocks and B column blocks and both stay in L2 (a plain
       // row-major order streams all of B once per wave of row blocks).
       const int64_t rows = MC == 2 ? (row_tiles + 1) / 2 : row_tiles;
-      const int64_t band = t / (kBandRows * tiles_n);
-      const int64_t band_rows =
-          rows - band * kBandRows < kBandRows ? rows - band * kBandRows : kBandRows;
-      const int64_t local = t - band * kBandRows * tiles_n;
-      const int64_t mt = band * kBandRows + local % band_rows;
+      int64_t mt, col;
+      if (LIN != 0 && num_tiles <= (int64_t)0x7FFFFFFF &&
+          kBandRows * tiles_n <= (int64_t)0x7FFFFFFF) {
+        // 32-bit divisions: every epilogue warp forms its tiles' origins
+        const uint32_t per_band = (uint32_t)(kBandRows * tiles_n), b = (uint32_t)t / per_band;
+        const uint32_t left = (uint32_t)rows - b * (uint32_t)kBandRows;
+        const uint32_t h = left < (uint32_t)kBandRows ? left : (uint32_t)kBandRows;
+        const uint32_t local = (uint32_t)t - b * per_band, c = local / h;
+        mt = b * (uint32_t)kBandRows + local - c * h;
+        col = c;
+      } else {
+        const int64_t band = t / (kBandRows * tiles_n);
+        const int64_t band_rows =
+            rows - band * kBandRows < kBandRows ? rows - band * kBandRows : kBandRows;
+        const int64_t local = t - band * kBandRows * tiles_n;
+        mt = band * kBandRows + local % band_rows;
+        col = local / band_rows;
+      }
       // (MC == 2: mt indexes row-tile pairs; this CTA takes row tile 2 mt + rank)
       ti.m0 = (mt * MC + mc_rank) * C::BM;
-      ti.n0 = (local / band_rows) * BN;
+      ti.n0 = col * BN;
       ti.row_end = args.M;
       ti.brow = ti.n0;
       ti.sbo = 0;
@@ -237,9 +250,13 @@ __global__ void __launch_bounds__(Cfg<MODE, BN, STAGES, LIN>::kThreads, 1)
   const int64_t u_first = csplit ? (int64_t)cluster_ctarank() * num_tiles + blockIdx.x / ks
                                  : (int64_t)(blockIdx.x / MC);
   const int64_t u_step = csplit ? num_units : (int64_t)(gridDim.x / MC);
-  auto unit_tile = [&](int64_t u) { return u % num_tiles; };
-  auto kb_begin = [&](int64_t u) { return (int)((u / num_tiles) * KB / ks); };
-  auto kb_end = [&](int64_t u) { return (int)((u / num_tiles + 1) * KB / ks); };
+  auto unit_tile = [&](int64_t u) { return LIN != 0 && ks == 1 ? u : u % num_tiles; };
+  auto kb_begin = [&](int64_t u) {
+    return LIN != 0 && ks == 1 ? 0 : (int)((u / num_tiles) * KB / ks);
+  };
+  auto kb_end = [&](int64_t u) {
+    return LIN != 0 && ks == 1 ? KB : (int)((u / num_tiles + 1) * KB / ks);
+  };
 
   if constexpr (!EXPERTS) {
     // the first unit's weight boxes into L2 while the previous kernel may
@@ -569,7 +586,7 @@ __global__ void __launch_bounds__(Cfg<MODE, BN, STAGES, LIN>::kThreads, 1)
       const int c0 = C::kEpiWarps == 8 ? (int)((warp - 2) >> 2) * C::kEpiCols : 0;
       for (int64_t u = u_first; u < num_units; u += u_step, ++j) {
         const int64_t t = unit_tile(u);
-        const int split = (int)(u / num_tiles);
+        const int split = LIN != 0 && ks == 1 ? 0 : (int)(u / num_tiles);
         const TileInfo ti = tile_info(t);
         const int64_t m0 = ti.m0, n0 = ti.n0;
         // rows past the tile's expert belong to the next expert: not stored

@@ -290,8 +290,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<BN, STAGES, 
     int64_t m0, n0;
     int kb_count;
   };
+  // (linear epilogues: one problem, its tile counts formed once and divided in
+  // 32 bits where they fit; the 64-bit divisions below are several hundred
+  // instructions per tile in each of the epilogue warps)
+  const int64_t lin_tiles_n = (grp.args[0].N + BN - 1) / BN;
+  const int64_t lin_rows = (grp.args[0].M + 255) / 256;
+  const bool narrow = LINEAR != 0 && num_tiles + npairs <= (int64_t)0x7FFFFFFF &&
+                      grp.band_rows * lin_tiles_n <= (int64_t)0x7FFFFFFF;
   auto tile_ref = [&](int64_t gt) {
     TileRef r;
+    if (narrow) {
+      const uint32_t t = (uint32_t)gt, bandh = (uint32_t)grp.band_rows;
+      const uint32_t per_band = bandh * (uint32_t)lin_tiles_n, band = t / per_band;
+      const uint32_t left = (uint32_t)lin_rows - band * bandh, h = left < bandh ? left : bandh;
+      const uint32_t local = t - band * per_band, col = local / h;
+      r.i = 0;
+      r.m0 = (int64_t)(band * bandh + local - col * h) * 256;
+      r.n0 = (int64_t)col * BN;
+      r.kb_count = (int)((grp.args[0].K + C::BK - 1) / C::BK);
+      return r;
+    }
     r.i = group_of(grp, gt);
     const GemmArgs &a = grp.args[r.i];
     const int64_t t = gt - grp.tile_begin[r.i];
