@@ -617,6 +617,7 @@ FP8_API int fp8_gemm_tensor_act_backward(const fp8_gemm_problem_t *problem,
  * and multiples of 8; K % 16 == 0, K <= 16384 (FP8_ERR_UNSUPPORTED beyond).
  * M == 0 writes only amax_out (0).  A row of zeros gives zero codes and unit
  * scales while eps > 0.  A non-finite value reaches its row's codes as a NaN.
+ * Squares are summed in fp32: |r| stays below 1e19 / sqrt(K).
  * Launched with programmatic stream serialization, as the per-group calls.
  */
 typedef enum { FP8_NORM_TENSOR = 0, FP8_NORM_GROUP = 1, FP8_NORM_MX = 2 } fp8_norm_mode_t;

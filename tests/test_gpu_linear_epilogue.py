@@ -304,3 +304,82 @@ def test_other_stream_and_graph():
     db2.zero_()
     g.replay()
     assert torch.equal(ref, got) and torch.equal(db, db2)
+
+
+def run_plain_epilogue(m, n, k, grad):
+    """One call with bf16 output; returns (output, exact, tolerance)."""
+    F = lib()
+    a, sa = codes(randn(m, k, seed=1), 0)
+    b, sb = codes(randn(n, k, seed=2, std=1 / math.sqrt(k)), 0)
+    pre = randn(m, n, seed=3).bfloat16()
+    out = torch.empty((m, n), dtype=torch.bfloat16, device="cuda")
+    if grad:
+        F.fp8_gemm_tensor_act_backward(a, 0, b, 0, sa, sb, pre, F.ACT_RELU, out=out)
+    else:
+        F.fp8_gemm_tensor_epilogue(a, 0, b, 0, sa, sb, out, act=F.ACT_RELU, residual=pre)
+    A, B, al = value(a, 0), value(b, 0), sa.double() * sb.double()
+    z = A @ B.t() * al
+    want = z * (pre.double() > 0) if grad else z.clamp_min(0) + pre.double()
+    tol = (k + 8) * 2.0 ** -23 * (A.abs() @ B.abs().t() * al) + 2.0 ** -8 * want.abs() + 1e-6
+    return out, want, tol
+
+
+@pytest.mark.parametrize("m,n,k,grad", [(2048, 2560, 16384, False), (128, 256, 65536, False),
+                                        (2048, 2560, 16384, True), (128, 256, 65536, True)])
+def test_expired_wait_is_reported_and_the_context_stays_usable(m, n, k, grad):
+    """With the wait bound at zero a wait of the kernel runs out: the call ends,
+    the status says so, and the next call is right (CTA pairs; one CTA per
+    tile, with K split over a cluster in the forward epilogue)."""
+    F = lib()
+    assert F.fp8_get_last_device_error()[0] == 0
+    F.fp8_set_option(F.OPT_WAIT_LIMIT_US, 0)
+    try:
+        run_plain_epilogue(m, n, k, grad)
+        torch.cuda.synchronize()
+    finally:
+        F.fp8_set_option(F.OPT_WAIT_LIMIT_US, 2_000_000)
+    assert F.fp8_get_last_device_error()[0] == F.FP8_ERR_TIMEOUT
+    close(*run_plain_epilogue(m, n, k, grad))
+    assert F.fp8_get_last_device_error() == (0, 0)
+
+
+@pytest.mark.parametrize("m,n,k", [(1029, 1283, 272), (2048, 2560, 160)])
+@pytest.mark.parametrize("grad", [False, True])
+def test_without_cta_pairs(m, n, k, grad):
+    """The same shapes on one CTA per tile."""
+    F = lib()
+    F.fp8_set_option(F.OPT_GEMM_CTA_PAIRS, 0)
+    try:
+        close(*run_plain_epilogue(m, n, k, grad))
+    finally:
+        F.fp8_set_option(F.OPT_GEMM_CTA_PAIRS, 1)
+
+
+def test_group_without_multicast():
+    F = lib()
+    a, sa, b, sb, A, B = group_operands(2200, 2600, 384, 1)
+    outs = []
+    for on in (0, 1):
+        F.fp8_set_option(F.OPT_GEMM_MULTICAST, on)
+        outs.append(torch.empty((2200, 2600), dtype=torch.bfloat16, device="cuda"))
+        F.fp8_gemm_group_epilogue(a, sa, b, sb, 1, outs[-1], act=F.ACT_SILU)
+    assert torch.equal(*outs)
+
+
+def test_repeatable():
+    """Maxima, column sums and codes have the same bits on every run."""
+    F = lib()
+    m, n, k = 1500, 2576, 528
+    a, sa = codes(randn(m, k), 1)
+    b, sb = codes(randn(k, n, seed=1), 0)
+    pre = randn(m, n, seed=2).bfloat16()
+    got = []
+    for _ in range(3):
+        q = torch.empty((m, n), dtype=torch.uint8, device="cuda")
+        am, db = torch.empty(1, device="cuda"), torch.empty(n, device="cuda")
+        F.fp8_gemm_tensor_act_backward(a, 1, b, 0, sa, sb, pre, F.ACT_SILU, q=q,
+                                       q_scale=torch.full((1,), 0.01, device="cuda"), q_amax=am,
+                                       dbias=db, b_layout=F.MN_MAJOR)
+        got.append((q, am, db))
+    for g in got[1:]:
+        assert all(torch.equal(x, y) for x, y in zip(got[0], g))
