@@ -86,7 +86,7 @@ struct Cfg {
   static constexpr uint32_t kSfColsPerStage = kBlockScaled ? 4 + kSfbRows / 32 : 0;
   static constexpr uint32_t kTmemCols = pow2_cols(kAccCols + STAGES * kSfColsPerStage);
   static constexpr int kNumBars = 2 * STAGES + 2 * kAccBufs + 1;  // + drain
-  static constexpr uint32_t kEpBytes = LIN != 0 && !kPromote ? kEpiWarps * kEpStageBytes : 0;  // linear_epilogue.cuh
+  static constexpr uint32_t kEpBytes = LIN != 0 ? kEpiWarps * kEpStageBytes : 0;  // linear_epilogue.cuh
   static constexpr uint32_t kSmem = 1024 + kTileBytes + kSfBytes + kEpBytes + 8 * kNumBars + 16;
   static_assert(kTmemCols <= 512, "TMEM budget");
   static_assert(kSmem <= 227 * 1024, "shared-memory budget");
@@ -574,7 +574,7 @@ __global__ void __launch_bounds__(Cfg<MODE, BN, STAGES, LIN>::kThreads, 1)
       float v[32];
       if constexpr (LIN == 1) scale_bias(args, c, r, alpha, v);
       next();
-      if constexpr (LIN == 1) linear_chunk(args, epp.e, r0, c, v, cur, qd, stage, amax);
+      if constexpr (LIN == 1) linear_chunk<true>(args, epp.e, r0, c, v, cur, qd, stage, amax);
       if constexpr (LIN == 2) grad_chunk(args, epp.e, r0, c, r, alpha, cur, qd, stage, amax);
     };
     if constexpr (!C::kPromote) {
@@ -734,9 +734,8 @@ __global__ void __launch_bounds__(Cfg<MODE, BN, STAGES, LIN>::kThreads, 1)
         if (ks > 1 && epi_any<C::kEpiWarps * 32>(!ok)) break;
         auto promoted = [&](int64_t c, float (&x)[32]) {
           if constexpr (LIN != 0) {
-#pragma unroll
-            for (int i = 0; i < 32; i += 16)
-              linear_part16(args, epp.e, row, c + i, *reinterpret_cast<float(*)[16]>(x + i));
+            add_bias(args, c, x);
+            linear_chunk<false>(args, epp.e, m0 + 32 * q, c, x, RowIn{}, qd, stage, amax);
           }
         };
         float v[32];

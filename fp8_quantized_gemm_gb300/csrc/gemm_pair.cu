@@ -465,7 +465,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<BN, STAGES, 
         if constexpr (kGrad)
           grad_chunk(a, e, row0, n0 + c, r, alpha, cur, d, stage, amax);
         else
-          linear_chunk(a, e, row0, n0 + c, v, cur, d, stage, amax);
+          linear_chunk<true>(a, e, row0, n0 + c, v, cur, d, stage, amax);
         if (!last) {
           // (the slopes leave no registers for a second chunk of accumulators)
           if constexpr (kGrad) FP8K_TMEM_LD_X32(lane_base + buf * BN + (uint32_t)c + 32u, r);

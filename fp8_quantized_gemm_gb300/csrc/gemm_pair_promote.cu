@@ -37,7 +37,7 @@ namespace fp8k {
 // 256-row tiles per band of the grouped tile order.
 constexpr int64_t kPromoteBandRows = 8;
 
-template <int BN_, int STAGES, int EPI>
+template <int BN_, int STAGES, int EPI, bool LINEAR = false>
 struct PromoteCfg {
   // per CTA: 128 rows x BN columns; pair: 256 x BN
   static constexpr int BM = 128, BN = BN_, BK = 128;
@@ -54,7 +54,8 @@ struct PromoteCfg {
   // the allocation: a power of two columns
   static constexpr uint32_t kTmemCols = kAccBufs * BN <= 256 ? 256u : 512u;
   static constexpr int kNumBars = 2 * STAGES + 2 * kAccBufs + 1;
-  static constexpr uint32_t kSmem = 1024 + kTileBytes + 8 * kNumBars + 16;
+  static constexpr uint32_t kEpBytes = LINEAR ? EPI * kEpStageBytes : 0;  // linear_epilogue.cuh
+  static constexpr uint32_t kSmem = 1024 + kTileBytes + kEpBytes + 8 * kNumBars + 16;
   static_assert(kStageBytes % 1024 == 0, "stages keep the 1024-byte swizzle alignment");
   static_assert(kTmemCols <= 512, "TMEM budget");
   static_assert(kSmem <= 227 * 1024, "shared-memory budget");
@@ -70,11 +71,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PromoteCfg<BN, STAGE
     gemm_pair_promote_kernel(const __grid_constant__ CUtensorMap tma,
                              const __grid_constant__ CUtensorMap tmb, const GemmArgs args,
                              const EpParam<LINEAR> epp) {
-  using C = PromoteCfg<BN, STAGES, EPI>;
+  using C = PromoteCfg<BN, STAGES, EPI, LINEAR>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::kTileBytes);
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::kTileBytes + C::kEpBytes);
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + C::kNumBars);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
@@ -323,10 +324,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PromoteCfg<BN, STAGE
         for (int i = 0; i < 32; ++i) v[i] = acc[32 * c + i];
         // (store_row32 itself skips rows past M; expert rows end earlier)
         if constexpr (LINEAR) {
-#pragma unroll
-          for (int h = 0; h < 32; h += 16)
-            linear_part16(args, epp.e, orow, to.n0 + col0 + 32 * c + h,
-                          *reinterpret_cast<float(*)[16]>(v + h));
+          const int64_t orow0 = to.m0 + rank * C::BM + 32 * q, ocol = to.n0 + col0 + 32 * c;
+          float amax = 0.0f;  // no codes here
+          add_bias(args, ocol, v);
+          linear_chunk<false>(args, epp.e, orow0, ocol, v, RowIn{}, CodeScale(1.0f),
+                              smem + C::kTileBytes + (warp - 2) * kEpStageBytes, amax);
         } else {
           if (!EXPERTS || orow < to.row_end) store_row32(args, orow, to.n0 + col0 + 32 * c, v);
         }
@@ -378,7 +380,7 @@ template <bool EXPERTS, bool LINEAR>
 static cudaError_t run_pair_promote(const CUtensorMap &tma, const CUtensorMap &tmb,
                                     const GemmArgs &args, const EpParam<LINEAR> &epp, int sms,
                                     cudaStream_t st) {
-  using C = PromoteC;
+  using C = PromoteCfg<kPromoteBN, kPromoteStages, kPromoteEpiWarps, LINEAR>;
   auto kern = gemm_pair_promote_kernel<kPromoteBN, kPromoteStages, kPromoteEpiWarps, EXPERTS, LINEAR>;
   static bool attr_done[64] = {};
   int dev = 0;

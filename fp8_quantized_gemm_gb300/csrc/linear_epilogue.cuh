@@ -95,10 +95,18 @@ __device__ __forceinline__ void gather_stage(const __nv_bfloat16 *src, int64_t l
                                              int cols, uint8_t *stage) {
   const int lane = (int)lane_id();
   __syncwarp();
-#pragma unroll 8
-  for (int r = 0; r < 32; ++r) {
-    const float t = lane < cols && r < rows ? __bfloat162float(src[r * ld + lane]) : 0.0f;
-    *reinterpret_cast<float *>(stage + stage_at(r, lane)) = t;
+#pragma unroll 1
+  for (int r0 = 0; r0 < 32; r0 += 8) {
+    // (the loads of a batch before its stores: the compiler cannot know that
+    // the stage is not the source, and ran them one by one, 319 us against 147
+    // at 13019 x 2273 x 256)
+    __nv_bfloat16 t[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      t[i] = lane < cols && r0 + i < rows ? src[(r0 + i) * ld + lane] : __nv_bfloat16(0.0f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      *reinterpret_cast<float *>(stage + stage_at(r0 + i, lane)) = __bfloat162float(t[i]);
   }
   __syncwarp();
 }
@@ -275,14 +283,57 @@ __device__ __forceinline__ void scale_bias(const GemmArgs &a, int64_t col0, cons
       fma2(acc(4 * i + 2), al, F2(b.z, b.w)).get(v[4 * i + 2], v[4 * i + 3]);
     }
   } else {
+    // one value per lane, handed around
+    const int64_t n = col0 + lane_id();
+    const float b = n < a.N ? __ldg(a.bias + n) : 0.0f;
 #pragma unroll
     for (int i = 0; i < 32; ++i)
-      v[i] = fmaf(__uint_as_float(r[i]), alpha, col0 + i < a.N ? __ldg(a.bias + col0 + i) : 0.0f);
+      v[i] = fmaf(__uint_as_float(r[i]), alpha, __shfl_sync(0xffffffffu, b, i));
   }
 }
 
-// Forward epilogue of one chunk (v: z of this lane's row; in: the residual of
-// fetch_chunk).  Every lane of the warp calls it.
+// The residual added to a chunk as it is loaded, 16 columns of registers at a
+// time (or through the stage).
+template <typename T>
+__device__ __forceinline__ void add_rows(const GemmArgs &a, const T *src, int64_t ld, int vec,
+                                         int64_t row0, int64_t col0, float (&v)[32],
+                                         uint8_t *stage) {
+  if (direct(a, col0, vec)) {
+    const int64_t row = row0 + lane_id();
+    if (row >= a.M) return;
+    constexpr int kPer = 32 / sizeof(T);  // values of a sector
+#pragma unroll
+    for (int h = 0; h < 32; h += 16) {
+      uint32_t w[16 * sizeof(T) / 4];
+      const T *p = src + row * ld + col0 + h;
+#pragma unroll
+      for (int i = 0; i < 16 / kPer; ++i) ld_sector(p + i * kPer, w + 8 * i);
+#pragma unroll
+      for (int i = 0; i < 16; i += 2) {
+        F2 x;
+        if constexpr (sizeof(T) == 2)
+          x = bf16_pair(w[i / 2]);
+        else
+          x = F2(__uint_as_float(w[i]), __uint_as_float(w[i + 1]));
+        (F2(v[h + i], v[h + i + 1]) + x).get(v[h + i], v[h + i + 1]);
+      }
+    }
+  } else {
+    gather_stage(src + row0 * ld + col0, ld, left32(a.M - row0), left32(a.N - col0), stage);
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const float4 f = stage_row4(stage, u);
+      v[4 * u] += f.x; v[4 * u + 1] += f.y; v[4 * u + 2] += f.z; v[4 * u + 3] += f.w;
+    }
+  }
+}
+
+// Forward epilogue of one chunk (v: z of this lane's row).  AHEAD: `in` holds a
+// bf16 residual of fetch_chunk; an fp32 one has too many registers for that,
+// and so has any in the kernels that keep a tile's accumulators in registers
+// (FP32 group scales: 4096 x 7168 x 2048 with bias and silu 110 -> 92 us over
+// a pass of its own per 16 columns).  Every lane of the warp calls it.
+template <bool AHEAD>
 __device__ __forceinline__ void linear_chunk(const GemmArgs &a, const LinearEp &e, int64_t row0,
                                              int64_t col0, float (&v)[32], const RowIn &in,
                                              const CodeScale &d, uint8_t *stage, float &amax) {
@@ -294,36 +345,37 @@ __device__ __forceinline__ void linear_chunk(const GemmArgs &a, const LinearEp &
     for (int i = 0; i < 32; i += 2)
       act_value2<decltype(act)::value>(F2(v[i], v[i + 1])).get(v[i], v[i + 1]);
   });
-  if (e.res != nullptr && e.res_dt == 0) {
-    // fp32: too many registers to hold a chunk ahead
-    const float *src = static_cast<const float *>(e.res);
-    if (direct(a, col0, e.res_vec)) {
-      if (row0 + lane_id() < a.M) {
+  if (e.res != nullptr) {
+    if (e.res_dt == 0) {
+      add_rows(a, static_cast<const float *>(e.res), e.ld_res, e.res_vec, row0, col0, v, stage);
+    } else if constexpr (AHEAD) {
 #pragma unroll
-        for (int h = 0; h < 32; h += 16) {
-          uint32_t w[16];
-          const float *p = src + (row0 + lane_id()) * e.ld_res + col0 + h;
-          ld_sector(p, w);
-          ld_sector(p + 8, w + 8);
-#pragma unroll
-          for (int i = 0; i < 16; ++i) v[h + i] += __uint_as_float(w[i]);
-        }
-      }
+      for (int i = 0; i < 32; i += 2)
+        (F2(v[i], v[i + 1]) + bf16_pair(in.w[i / 2])).get(v[i], v[i + 1]);
     } else {
-      gather_stage(src + row0 * e.ld_res + col0, e.ld_res, left32(a.M - row0), left32(a.N - col0),
-                   stage);
-#pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        const float4 f = stage_row4(stage, u);
-        v[4 * u] += f.x; v[4 * u + 1] += f.y; v[4 * u + 2] += f.z; v[4 * u + 3] += f.w;
-      }
+      add_rows(a, static_cast<const __nv_bfloat16 *>(e.res), e.ld_res, e.res_vec, row0, col0, v,
+               stage);
     }
-  } else if (e.res != nullptr) {
-#pragma unroll
-    for (int i = 0; i < 32; i += 2)
-      (F2(v[i], v[i + 1]) + bf16_pair(in.w[i / 2])).get(v[i], v[i + 1]);
   }
   put_result(a, e, row0, col0, v, d, stage, amax);
+}
+
+// The bias added to a chunk in place.
+__device__ __forceinline__ void add_bias(const GemmArgs &a, int64_t col0, float (&v)[32]) {
+  if (a.bias == nullptr || col0 >= a.N) return;
+  if (col0 + 32 <= a.N && (reinterpret_cast<uintptr_t>(a.bias + col0) & 15u) == 0) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float4 b = __ldg(reinterpret_cast<const float4 *>(a.bias + col0) + i);
+      v[4 * i] += b.x; v[4 * i + 1] += b.y; v[4 * i + 2] += b.z; v[4 * i + 3] += b.w;
+    }
+  } else {
+    // one value per lane, handed around
+    const int64_t n = col0 + lane_id();
+    const float b = n < a.N ? __ldg(a.bias + n) : 0.0f;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] += __shfl_sync(0xffffffffu, b, i);
+  }
 }
 
 // Gradient epilogue of one chunk (r: the accumulators of this lane's row; in:
@@ -368,75 +420,6 @@ __device__ __forceinline__ void grad_chunk(const GemmArgs &a, const LinearEp &e,
   s1 += __shfl_xor_sync(0xffffffffu, s1, 16);
   const int64_t col = col0 + 2 * (lane & 15) + (lane >> 4);  // each half writes one of the pair
   if (col < a.N) e.part[(row0 >> 5) * a.N + col] = lane < 16 ? s0 : s1;
-}
-
-// Forward epilogue of 16 columns of this lane's row, bf16 c and no codes: for
-// the kernels that keep a tile's accumulators in registers (FP32 group
-// scales), which leave no room for a 32-column chunk and its operands.
-// Unaligned rows take scalar accesses.
-__device__ __forceinline__ void linear_part16(const GemmArgs &a, const LinearEp &e, int64_t row,
-                                              int64_t col0, float (&v)[16]) {
-  if (row >= a.M || col0 >= a.N) return;
-  const bool whole = col0 + 16 <= a.N;
-  const int n = whole ? 16 : (int)(a.N - col0);
-  const __nv_bfloat16 *rb = static_cast<const __nv_bfloat16 *>(e.res) + row * e.ld_res + col0;
-  const float *rf = static_cast<const float *>(e.res) + row * e.ld_res + col0;
-  const bool res_b = e.res != nullptr && e.res_dt == 1;
-  uint32_t w[8];
-  if (res_b) {
-    if (whole && e.res_vec) {
-      ld_sector(rb, w);
-    } else {
-      const uint16_t *p = reinterpret_cast<const uint16_t *>(rb);
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        w[i] = (2 * i < n ? p[2 * i] : 0u) | (2 * i + 1 < n ? (uint32_t)p[2 * i + 1] << 16 : 0u);
-    }
-  }
-  if (a.bias != nullptr) {
-    if (whole && (reinterpret_cast<uintptr_t>(a.bias + col0) & 15u) == 0) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float4 b = __ldg(reinterpret_cast<const float4 *>(a.bias + col0) + i);
-        v[4 * i] += b.x; v[4 * i + 1] += b.y; v[4 * i + 2] += b.z; v[4 * i + 3] += b.w;
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 16; ++i)
-        if (i < n) v[i] += __ldg(a.bias + col0 + i);
-    }
-  }
-  auto put = [&](void *base, int64_t ld, int vec) {
-    __nv_bfloat16 *p = static_cast<__nv_bfloat16 *>(base) + row * ld + col0;
-    if (whole && vec) {
-      uint32_t o[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-        o[i] = *reinterpret_cast<const uint32_t *>(&h);
-      }
-      st_sector(p, o);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 16; ++i)
-        if (i < n) p[i] = __float2bfloat16_rn(v[i]);
-    }
-  };
-  if (e.pre != nullptr) put(e.pre, e.ld_pre, e.pre_vec);
-  with_act(e.act, [&](auto act) {
-#pragma unroll
-    for (int i = 0; i < 16; i += 2)
-      act_value2<decltype(act)::value>(F2(v[i], v[i + 1])).get(v[i], v[i + 1]);
-  });
-  if (res_b) {
-#pragma unroll
-    for (int i = 0; i < 16; i += 2) (F2(v[i], v[i + 1]) + bf16_pair(w[i / 2])).get(v[i], v[i + 1]);
-  } else if (e.res != nullptr) {
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (i < n) v[i] += rf[i];
-  }
-  put(a.c, a.ldc, e.c_vec);
 }
 
 // pre, activation and residual of one value z = result + bias: returns y.
