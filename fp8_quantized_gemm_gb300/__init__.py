@@ -14,6 +14,7 @@ from __future__ import annotations
 import ctypes
 import os
 import struct
+import threading
 
 import torch
 
@@ -510,6 +511,7 @@ _c_norm, _c_norm_grad = _lib.fp8_rmsnorm_quantize, _lib.fp8_rmsnorm_backward
 _c_tensor_epilogue = _lib.fp8_gemm_tensor_epilogue
 _c_group_epilogue = _lib.fp8_gemm_group_epilogue
 _c_act_backward = _lib.fp8_gemm_tensor_act_backward
+_c_norm_grad_ws, _c_act_ws = _lib.fp8_rmsnorm_backward_workspace, _lib.fp8_act_backward_workspace
 _raw_stream, _get_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 _BF16, _F32 = torch.bfloat16, torch.float32
 
@@ -573,12 +575,33 @@ def _check(name, rc):
         raise Fp8Error(name, rc)
 
 
-def _scratch(nbytes, device, stream):
-    """Scratch of one call: torch hands the memory on in the current stream's
-    order, so a call on another stream brings its own."""
+# Scratch of calls that bring none.  Up to _KEPT bytes come from a buffer kept
+# per thread, device and stream (calls that share it follow one another on that
+# stream; allocating it anew costs 3 of a small call's 8 us); larger ones, and
+# calls recorded into a graph, whose memory must live as long as the graph, come
+# from torch's allocator in the current stream's order.
+_KEPT = 8 << 20
+_kept = threading.local()
+_capturing = torch._C._cuda_isCurrentStreamCapturing
+
+
+def _scratch(nbytes, workspace, device, stream):
+    """(pointer, bytes, owner) of a call's scratch; the owner lives through it."""
+    if workspace is not None:
+        return _flat(workspace), workspace.nbytes, None
     if stream is not None:
         raise ValueError("a call on an explicit stream needs an explicit workspace")
-    return torch.empty(max(16, nbytes), dtype=torch.uint8, device=device)
+    if nbytes > _KEPT or _capturing():
+        t = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        return t.data_ptr(), nbytes, t
+    dev = _get_device()
+    try:
+        return _kept.buffers[dev, _raw_stream(dev)]
+    except (AttributeError, KeyError):
+        if not hasattr(_kept, "buffers"):
+            _kept.buffers = {}
+        t = torch.empty(_KEPT, dtype=torch.uint8, device=device)
+        return _kept.buffers.setdefault((dev, _raw_stream(dev)), (t.data_ptr(), _KEPT, t))
 
 
 def fp8_rmsnorm_quantize(x, w, eps, fmt, q, *, residual=None, sum_out=None, scale=None,
@@ -619,11 +642,11 @@ def fp8_rmsnorm_backward(dy, r, inv_rms, w, dx, *, d_residual=None, dw=None, acc
     """dx = gradient of x and of residual, through the norm and (d_residual)
     past it; dw: fp32 [K]; q: the codes of dx under `scale`, amax_out its
     max |dx|.  r, inv_rms: as fp8_rmsnorm_quantize wrote them.  workspace
-    (with dw): device scratch, allocated on the current stream when None."""
+    (with dw): device scratch; None: the binding's own."""
     shape, t = r.shape, r.dtype
     m, k = shape
-    if dw is not None and workspace is None:
-        workspace = _scratch(fp8_rmsnorm_backward_workspace(m, k), r.device, stream)
+    pws, ws_bytes, keep = (0, 0, None) if dw is None else _scratch(
+        _c_norm_grad_ws(m, k), workspace, r.device, stream)
     py, ldy = _rows(dy, shape, dy.dtype, "dy")
     pr, ldr = _rows(r, shape, t, "r")
     pe, lde = _rows(d_residual, shape, t, "d_residual")
@@ -633,7 +656,7 @@ def fp8_rmsnorm_backward(dy, r, inv_rms, w, dx, *, d_residual=None, dw=None, acc
                         m, k, ldy, ldr, lde, ldx, px, _vector(dw, k, "dw"),
                         int(bool(accumulate_dw)), _codes(q, m * k, "q"), fmt,
                         _vector(scale, 1, "scale"), _vector(amax_out, 1, "amax_out"),
-                        _flat(workspace), 0 if workspace is None else workspace.nbytes)
+                        pws, ws_bytes)
     _check("fp8_rmsnorm_backward", _c_norm_grad(d, _on(stream)))
 
 
@@ -698,17 +721,16 @@ def fp8_gemm_tensor_act_backward(a, fa, b, fb, sa, sb, pre, act, *, out=None, q=
                                  workspace=None, a_layout=K_MAJOR, b_layout=K_MAJOR, stream=None):
     """dz = (sa sb A B^T) * act'(pre) in the GEMM's epilogue: out (bf16 or
     fp32) and/or q <- codes of dz under q_scale (q_amax: max |dz|); dbias:
-    fp32 [N] column sums.  workspace (with dbias): device scratch, allocated
-    on the current stream when None."""
+    fp32 [N] column sums.  workspace (with dbias): device scratch; None: the
+    binding's own."""
     shape, p = _epilogue_problem(a, fa, b, fb, sa, sb, out, a_layout, b_layout, None)
     m, n = shape
-    if dbias is not None and workspace is None:
-        workspace = _scratch(fp8_act_backward_workspace(m, n), pre.device, stream)
+    pws, ws_bytes, keep = (0, 0, None) if dbias is None else _scratch(
+        _c_act_ws(m, n), workspace, pre.device, stream)
     pp, ldp = _rows(pre, shape, _BF16, "pre")
     e = _pack_act_grad(act, pp, ldp, _codes(q, m * n, "q"), q_fmt, _vector(q_scale, 1, "q_scale"),
                        _vector(q_amax, 1, "q_amax"), _vector(dbias, n, "dbias"),
-                       int(bool(accumulate_dbias)), _flat(workspace),
-                       0 if workspace is None else workspace.nbytes)
+                       int(bool(accumulate_dbias)), pws, ws_bytes)
     _check("fp8_gemm_tensor_act_backward", _c_act_backward(p, e, _on(stream)))
 
 

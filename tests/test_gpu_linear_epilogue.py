@@ -383,3 +383,33 @@ def test_repeatable():
         got.append((q, am, db))
     for g in got[1:]:
         assert all(torch.equal(x, y) for x, y in zip(got[0], g))
+
+
+def test_own_scratch_on_two_streams():
+    """Calls without a workspace on two streams at once: neither sees the
+    other's partial sums."""
+    F = lib()
+    m, n, k = 300, 1040, 528
+    a, sa = codes(randn(m, k), 0)
+    pre = randn(m, n, seed=2).bfloat16()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    bs, dbs = [], []
+    for i in range(2):
+        b, sb = codes(randn(n, k, seed=10 + i), 0)
+        bs.append((b, sb))
+        dbs.append([torch.empty(n, device="cuda") for _ in range(20)])
+    for st in streams:
+        st.wait_stream(torch.cuda.current_stream())
+    for j in range(20):
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                F.fp8_gemm_tensor_act_backward(a, 0, bs[i][0], 0, sa, bs[i][1], pre, F.ACT_GELU,
+                                               q=torch.empty((m, n), dtype=torch.uint8, device="cuda"),
+                                               q_scale=sa, dbias=dbs[i][j])
+    torch.cuda.synchronize()
+    for i in range(2):
+        want = torch.empty(n, device="cuda")
+        ws = torch.empty(F.fp8_act_backward_workspace(m, n), dtype=torch.uint8, device="cuda")
+        F.fp8_gemm_tensor_act_backward(a, 0, bs[i][0], 0, sa, bs[i][1], pre, F.ACT_GELU,
+                                       out=torch.empty((m, n), device="cuda"), dbias=want, workspace=ws)
+        assert all(torch.equal(d, want) for d in dbs[i])
