@@ -278,14 +278,14 @@ __device__ __forceinline__ void scale_bias(const GemmArgs &a, int64_t col0, cons
     const float4 *b4 = reinterpret_cast<const float4 *>(a.bias + col0);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float4 b = __ldg(b4 + i);
+      const float4 b = b4[i];
       fma2(acc(4 * i), al, F2(b.x, b.y)).get(v[4 * i], v[4 * i + 1]);
       fma2(acc(4 * i + 2), al, F2(b.z, b.w)).get(v[4 * i + 2], v[4 * i + 3]);
     }
   } else {
     // one value per lane, handed around
     const int64_t n = col0 + lane_id();
-    const float b = n < a.N ? __ldg(a.bias + n) : 0.0f;
+    const float b = n < a.N ? a.bias[n] : 0.0f;
 #pragma unroll
     for (int i = 0; i < 32; ++i)
       v[i] = fmaf(__uint_as_float(r[i]), alpha, __shfl_sync(0xffffffffu, b, i));
@@ -366,13 +366,13 @@ __device__ __forceinline__ void add_bias(const GemmArgs &a, int64_t col0, float 
   if (col0 + 32 <= a.N && (reinterpret_cast<uintptr_t>(a.bias + col0) & 15u) == 0) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float4 b = __ldg(reinterpret_cast<const float4 *>(a.bias + col0) + i);
+      const float4 b = reinterpret_cast<const float4 *>(a.bias + col0)[i];
       v[4 * i] += b.x; v[4 * i + 1] += b.y; v[4 * i + 2] += b.z; v[4 * i + 3] += b.w;
     }
   } else {
     // one value per lane, handed around
     const int64_t n = col0 + lane_id();
-    const float b = n < a.N ? __ldg(a.bias + n) : 0.0f;
+    const float b = n < a.N ? a.bias[n] : 0.0f;
 #pragma unroll
     for (int i = 0; i < 32; ++i) v[i] += __shfl_sync(0xffffffffu, b, i);
   }
@@ -494,7 +494,7 @@ struct LinearPut {
     if (a.bias != nullptr) {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        if (i < n) v[i] += __ldg(a.bias + col + i);
+        if (i < n) v[i] += a.bias[col + i];
     }
     if (e.pre != nullptr)
       put_bf16(static_cast<__nv_bfloat16 *>(e.pre) + row * e.ld_pre + col, n, v);

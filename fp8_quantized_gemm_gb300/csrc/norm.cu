@@ -106,17 +106,19 @@ __device__ __forceinline__ void store_raw8(T *p, const Raw8<T> &r) {
 }
 
 // Eight gains as pairs (w null: ones).  They are re-read per row: K values
-// that stay in L1.
+// that stay in L1.  (Plain loads here and of inv: the previous kernel, still
+// running when this one starts, may write them, and what
+// grid_dependency_wait() makes visible does not cover the read-only path.)
 __device__ __forceinline__ void load_gain8(const void *w, int w_dt, int64_t c, F2 (&g)[4]) {
   if (w == nullptr) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) g[j] = F2(1.0f);
   } else if (w_dt == 0) {
-    const uint4 u = __ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(w) + c));
+    const uint4 u = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(w) + c);
     g[0] = bf16_pair(u.x); g[1] = bf16_pair(u.y); g[2] = bf16_pair(u.z); g[3] = bf16_pair(u.w);
   } else {
     const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(w) + c);
-    const float4 a = __ldg(p), b = __ldg(p + 1);
+    const float4 a = p[0], b = p[1];
     g[0] = F2(a.x, a.y); g[1] = F2(a.z, a.w); g[2] = F2(b.x, b.y); g[3] = F2(b.z, b.w);
   }
 }
@@ -303,7 +305,7 @@ __global__ void __launch_bounds__(512, 1) rmsnorm_grad_kernel(const NormGradArgs
   Raw8<T> rr[V], er[V];
   float inv = 0.0f;
   auto fetch = [&](int64_t row) {
-    inv = __ldg(a.inv_rms + row);
+    inv = a.inv_rms[row];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       yr[i].zero();

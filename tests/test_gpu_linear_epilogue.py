@@ -413,3 +413,54 @@ def test_own_scratch_on_two_streams():
         F.fp8_gemm_tensor_act_backward(a, 0, bs[i][0], 0, sa, bs[i][1], pre, F.ACT_GELU,
                                        out=torch.empty((m, n), device="cuda"), dbias=want, workspace=ws)
         assert all(torch.equal(d, want) for d in dbs[i])
+
+
+@pytest.mark.parametrize("kind", ["tensor", "mx", "f32", "grad"])
+def test_long_output_offsets(kind):
+    """Outputs, residual, pre and codes whose element offsets pass 2^31: the
+    last rows, the only ones with operands other than zero."""
+    F = lib()
+    m, n, k, t = 66049, 32784, 128, 200
+    x = torch.zeros((m, k), device="cuda")
+    x[-t:] = randn(t, k)
+    if kind in ("mx", "f32"):
+        a, sa, b, sb, A, B = group_operands(m, n, k, int(kind == "mx"))
+        A, al, rows = A[-t:], 1.0, slice(m - t, m)
+    else:
+        a, sa = codes(x, 0)
+        b, sb = codes(randn(n, k, seed=1), 0)
+        A, B, al, rows = value(a, 0)[-t:], value(b, 0), sa.double() * sb.double(), slice(m - t, m)
+    other = torch.zeros((m, n), dtype=torch.bfloat16, device="cuda")  # residual, or pre
+    other[rows] = randn(t, n, seed=2).bfloat16()
+    o = other[rows].double()
+    z = A @ B.t() * al
+    tz = (k + 8) * 2.0 ** -23 * (A.abs() @ B.abs().t() * al)
+    c = torch.empty((m, n), dtype=torch.bfloat16, device="cuda")
+    q = torch.empty((m, n), dtype=torch.uint8, device="cuda")
+    qs, am = torch.full((1,), 0.1, device="cuda"), torch.empty(1, device="cuda")
+    if kind == "grad":
+        db = torch.empty(n, device="cuda")
+        F.fp8_gemm_tensor_act_backward(a, 0, b, 0, sa, sb, other, F.ACT_SILU, out=c, q=q,
+                                       q_fmt=F.E4M3, q_scale=qs, q_amax=am, dbias=db)
+        s = act64(o, "silu")[1]
+        y, ty = z * s, tz * s.abs() + 2.0 ** -18 * z.abs() * (1 + s.abs()) + 1e-30
+        close(c[rows], y, ty + 2.0 ** -8 * (y.abs() + ty))
+        sq = qs.double()
+        v = (y / sq).clamp(-448, 448)
+        err = (value(q[rows], 0) - v).abs()
+        assert (err <= half_step(v.abs() + ty / sq, 0) * (1 + 1e-6) + 2 * ty / sq).all()
+        close(db, y.sum(0), ty.sum(0) + (m // 32 + 32) * 2.0 ** -24 * y.abs().sum(0))
+    else:
+        p = torch.empty((m, n), dtype=torch.bfloat16, device="cuda")
+        if kind == "tensor":
+            F.fp8_gemm_tensor_epilogue(a, 0, b, 0, sa, sb, c, act=F.ACT_RELU, residual=other,
+                                       pre_out=p, q=q, q_scale=qs, q_amax=am)
+        else:
+            F.fp8_gemm_group_epilogue(a, sa, b, sb, int(kind == "mx"), c, act=F.ACT_RELU,
+                                      residual=other, pre_out=p)
+        y = z.clamp_min(0) + o
+        check_epilogue(None, y, tz + 2.0 ** -23 * o.abs(), z, "relu", c[rows], p[rows],
+                       q[rows] if kind == "tensor" else None, qs, am, 0)
+        if kind == "tensor":
+            assert (q[:-t] == 0).all() and (c[:-t] == 0).all()
+    assert F.fp8_get_last_device_error() == (0, 0)
