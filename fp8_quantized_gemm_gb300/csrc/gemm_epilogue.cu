@@ -9,10 +9,10 @@ namespace fp8k {
 // warp half the epilogue).  Block-scale words: where the plain kernel takes
 // 256-wide tiles (one TMEM accumulator beside the scale factors: the epilogue
 // of a tile and the MMAs of the next take turns), 192-wide ones, two of which
-// fit: 4096 x 7168 x 2048 with bias and silu runs in 57.7 us, B multicast to
-// the two CTAs of a cluster (59.4 without), against 72.1 on 256-wide tiles.
-// With few columns and a deep K (4096 x 2048 x 7168) the two are near: 62.5
-// against 59.9.
+// fit: 4096 x 7168 x 2048 with bias and silu runs in 54.2 us, B multicast to
+// the two CTAs of a cluster (2-3 us more without), against 72.1 on 256-wide
+// tiles.  With few columns and a deep K (4096 x 2048 x 7168) the two are near:
+// 57.2 against 59.9.
 int gemm_epilogue_tile_n(int mode, int64_t M, int64_t N, int sms) {
   const int bn = gemm_tile_n(mode, M, N, sms);
   if (mode == kScaleTensor) return 128;

@@ -34,6 +34,9 @@
 //                                  MMA in its own buffer: a promotion per
 //                                  32-deep K step, with the scales of each
 //                                  32-column weight block.
+//
+// LIN variants end in the linear layer's epilogue (linear_epilogue.cuh) instead
+// of the plain store; gemm_epilogue.cu instantiates and chooses among them.
 #pragma once
 
 #include "common.cuh"

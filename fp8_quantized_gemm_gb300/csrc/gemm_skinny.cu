@@ -49,6 +49,11 @@
 //            slice into one of four TMEM buffers (MP columns each).
 //   warps 2+ promotion (4 warps, 8 from MP = 32 on: two column halves),
 //            then the stores or the exchange.
+//
+// EPI: the values end in the linear layer's epilogue (pre-activation,
+// activation, residual) instead of the plain store, each on its own: with few
+// rows the epilogue's operands are small beside the weights.  1 x 2048 x 7168 with
+// FP32 scales, bias and a bf16 residual: 6.1 us (2.2 for the weights' bytes).
 #include "common.cuh"
 #include "gemm_common.cuh"
 #include "kernels.h"

@@ -16,8 +16,8 @@
 // and a 1x128 group is 16 neighbouring lanes, a 1x32 block four), reduces it
 // with one barrier (the partial sums alternate between two buffers), and has
 // the loads of its next row in flight meanwhile.  Measured (HBM's copy rate
-// 6690 GB/s): forward 16384 x 4096 with residual and per-tensor codes 75.6 us,
-// 93% of it; backward with codes and dw 103.5 us, 87%.  For the backward pass
+// 6690 GB/s): forward 16384 x 4096 with residual and per-tensor codes 75.4 us,
+// 93% of it; backward with codes and dw 102-103 us, 88%.  For the backward pass
 // a ring of rows in shared memory filled by bulk copies measured 101-104 us
 // at 4096 columns and 135 at 2048 (a row's chain of reduction, barrier and
 // second pass bounds it, not the bytes in flight).
