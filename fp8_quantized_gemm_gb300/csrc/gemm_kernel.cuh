@@ -578,7 +578,10 @@ __global__ void __launch_bounds__(Cfg<MODE, BN, STAGES, LIN>::kThreads, 1)
       if constexpr (LIN == 1) scale_bias(args, c, r, alpha, v);
       next();
       if constexpr (LIN == 1) linear_chunk<true>(args, epp.e, r0, c, v, cur, qd, stage, amax);
-      if constexpr (LIN == 2) grad_chunk(args, epp.e, r0, c, r, alpha, cur, qd, stage, amax);
+      // (the gradient's next accumulators are read after the chunk: read inside
+      // it, 333 x 1040 x 528 took 10.6 us against 10.4)
+      if constexpr (LIN == 2)
+        grad_chunk(args, epp.e, r0, c, r, alpha, cur, qd, stage, amax, [] {});
     };
     if constexpr (!C::kPromote) {
       float alpha = 1.0f;

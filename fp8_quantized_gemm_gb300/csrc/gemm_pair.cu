@@ -46,14 +46,14 @@
 // Two more, for single problems, are the linear layer's epilogues, forward and
 // gradient (linear_epilogue.cuh), in kernels of their own (LINEAR) with eight
 // epilogue warps: a warp takes 128 of the tile's 256 columns as four 32 x 32
-// chunks and fetches the next chunk's bf16 operand, and in the forward form its
-// accumulators, while it works on one.  Launched back to back the large shapes
+// chunks and fetches the next chunk's bf16 operand and accumulators while it
+// works on one.  Launched back to back the large shapes
 // run at the board's power limit (1310-1420 MHz), where each instruction of the
 // epilogue costs clock.  16384 x 14336 x 4096 with bias, GELU, stored
 // pre-activation and codes: 545-565 us in a short run, 645 in a long one (the
 // product without an epilogue 600-620; 497 at the dense FP8 peak); 16384 x 4096
 // x 14336 with bias and residual 605 / 630; the activation gradient of the first
-// 660 / 695.  Four epilogue warps: equal for light epilogues, 779 against 656
+// 660 / 682.  Four epilogue warps: equal for light epilogues, 779 against 656
 // us for the GELU product.
 #include "common.cuh"
 #include "elementwise.cuh"
@@ -456,7 +456,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<BN, STAGES, 
       if (!mbar_wait_warp(accf_bar(buf), use & 1u, abort_flag, err, 3)) break;
       tc_fence_after();
       // the operands of a chunk are fetched while the previous one is worked
-      // on, and (forward) its accumulators read
+      // on, and its accumulators read as soon as that one's are used
       uint32_t r[32];
       FP8K_TMEM_LD_X32(lane_base + buf * BN, r);
       tmem_ld_wait();
@@ -476,12 +476,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<BN, STAGES, 
           if constexpr (!kGrad) FP8K_TMEM_LD_X32(lane_base + buf * BN + (uint32_t)c + 32u, r);
         }
         if constexpr (kGrad)
-          grad_chunk(a, e, row0, n0 + c, r, alpha, cur, d, stage, amax);
+          grad_chunk(a, e, row0, n0 + c, r, alpha, cur, d, stage, amax, [&]() {
+            if (!last) FP8K_TMEM_LD_X32(lane_base + buf * BN + (uint32_t)c + 32u, r);
+          });
         else
           linear_chunk<true>(a, e, row0, n0 + c, v, cur, d, stage, amax);
         if (!last) {
-          // (the slopes leave no registers for a second chunk of accumulators)
-          if constexpr (kGrad) FP8K_TMEM_LD_X32(lane_base + buf * BN + (uint32_t)c + 32u, r);
           tmem_ld_wait();
           FP8K_REG_FENCE32(r);
         }

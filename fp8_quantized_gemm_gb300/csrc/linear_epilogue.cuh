@@ -382,11 +382,16 @@ __device__ __forceinline__ void add_bias(const GemmArgs &a, int64_t col0, float 
 // pre); its 32 rows' column sums go to
 // part[row0 / 32][col0 ...], through the stage: lane l adds 16 rows of the
 // columns 2 (l % 16) and the next, then the two halves of the warp add up.
+// next(): the accumulators have been used (the whole warp calls it).
+template <typename Next>
 __device__ __forceinline__ void grad_chunk(const GemmArgs &a, const LinearEp &e, int64_t row0,
                                            int64_t col0, const uint32_t (&r)[32], float alpha,
                                            const RowIn &in, const CodeScale &d, uint8_t *stage,
-                                           float &amax) {
-  if (row0 >= a.M || col0 >= a.N) return;
+                                           float &amax, Next &&next) {
+  if (row0 >= a.M || col0 >= a.N) {
+    next();
+    return;
+  }
   const int lane = (int)lane_id();
   const F2 al(alpha);
   float v[32];
@@ -404,6 +409,7 @@ __device__ __forceinline__ void grad_chunk(const GemmArgs &a, const LinearEp &e,
     for (int i = 0; i < 32; ++i) v[i] = 0.0f;
   }
   __syncwarp();
+  next();
   put_result(a, e, row0, col0, v, d, stage, amax);
   if (e.part == nullptr) return;
   stage_put(stage, v);
