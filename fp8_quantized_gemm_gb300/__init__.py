@@ -557,6 +557,13 @@ def _codes(t, n, what):
     return t.data_ptr()
 
 
+def _scales(t, n, size, what):
+    """Device pointer of n scales (or words) of `size` bytes, at least."""
+    if t.element_size() != size or t.numel() < n or not t.is_cuda or not t.is_contiguous():
+        raise ValueError("%s must hold %d contiguous %d-byte CUDA scales" % (what, n, size))
+    return t.data_ptr()
+
+
 def _gain(w, k):
     """(device pointer, type) of the norm's gains (None: ones)."""
     if w is None:
@@ -623,9 +630,10 @@ def fp8_rmsnorm_quantize(x, w, eps, fmt, q, *, residual=None, sum_out=None, scal
     if scale is not None:
         mode, psc = NORM_TENSOR, 0
     elif scales is not None:
-        mode, psc = NORM_GROUP, _flat(scales)
+        mode = NORM_GROUP
+        psc = _scales(scales, (k + 127) // 128 * m, 4 if sfmt == SCALE_F32 else 1, "scales")
     else:
-        mode, psc = NORM_MX, _flat(local)
+        mode, psc = NORM_MX, _scales(local, k // 128 * ((m + 127) // 128 * 128), 4, "local")
     d = _pack_norm(px, pr, pw, _in_dt(x), wdt, m, k, ldx, ldr, eps, mode, fmt, sfmt,
                    _vector(scale, 1, "scale"), _codes(q, m * k, "q"), psc, ps, lds, py, ldy,
                    _vector(inv_rms, m, "inv_rms"), _vector(amax_out, 1, "amax_out"))
@@ -706,9 +714,11 @@ def fp8_gemm_group_epilogue(a, sa, b, sb, sfmt, out, *, bias=None, act=ACT_NONE,
     shape = (m, n)
     e = _linear_epilogue(shape, act, residual, pre_out)
     c, ldc = _rows(out, shape, _BF16, "out")
+    g, size = k // 128, 4 if sfmt == SCALE_F32 else 1
     _check("fp8_gemm_group_epilogue",
-           _c_group_epilogue(_codes(a, m * k, "a"), _flat(sa), _codes(b, n * k, "b"), _flat(sb), sfmt,
-                             m, n, k, _vector(bias, n, "bias"), e, c, ldc, _on(stream)))
+           _c_group_epilogue(_codes(a, m * k, "a"), _scales(sa, g * m, size, "sa"),
+                             _codes(b, n * k, "b"), _scales(sb, (n + 127) // 128 * g, size, "sb"),
+                             sfmt, m, n, k, _vector(bias, n, "bias"), e, c, ldc, _on(stream)))
 
 
 def fp8_act_backward_workspace(m, n):

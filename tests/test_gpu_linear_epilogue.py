@@ -464,3 +464,22 @@ def test_long_output_offsets(kind):
         if kind == "tensor":
             assert (q[:-t] == 0).all() and (c[:-t] == 0).all()
     assert F.fp8_get_last_device_error() == (0, 0)
+
+
+def test_short_scales_are_refused():
+    """Scale tensors of too few elements or of the other format's size."""
+    F = lib()
+    m, n, k = 40, 200, 384
+    a, sa, b, sb, _, _ = group_operands(m, n, k, 0)
+    c = torch.empty((m, n), dtype=torch.bfloat16, device="cuda")
+    byte = torch.zeros(sa.numel(), dtype=torch.uint8, device="cuda")
+    for s, t in ((sa.flatten()[:-1], sb), (sa, sb.flatten()[:-1]), (byte, sb), (sa.double(), sb)):
+        with pytest.raises(ValueError):
+            F.fp8_gemm_group_epilogue(a, s, b, t, F.SCALE_F32, c)
+    with pytest.raises(ValueError):
+        F.fp8_gemm_group_epilogue(a, sa, b, sb, F.SCALE_UE8M0, c)
+    x, q = randn(m, k).bfloat16(), torch.empty((m, k), dtype=torch.uint8, device="cuda")
+    for kw in (dict(scales=sa.flatten()[:-1]), dict(scales=byte), dict(scales=sa, sfmt=F.SCALE_UE8M0),
+               dict(local=torch.zeros(k // 128 * 128 - 1, dtype=torch.int32, device="cuda"))):
+        with pytest.raises(ValueError):
+            F.fp8_rmsnorm_quantize(x, None, 1e-5, F.E4M3, q, **kw)
