@@ -332,12 +332,12 @@ __global__ void __launch_bounds__(Cfg<MODE, BN, STAGES, LIN>::kThreads, 1)
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           const int64_t m = m0 + 32 * c + lane;
-          fa[c] = m < args.M ? (uint32_t)__ldg(sa8 + (int64_t)kb * args.M + m) : 127u;
+          fa[c] = m < args.M ? (uint32_t)sa8[(int64_t)kb * args.M + m] : 127u;
         }
 #pragma unroll
         for (int c = 0; c < BN / 32; ++c) {
           const int64_t n = n0 + 32 * c + lane;
-          fb[c] = n < args.N ? (uint32_t)__ldg(sb8 + (n >> 7) * G + kb) : 127u;
+          fb[c] = n < args.N ? (uint32_t)sb8[(n >> 7) * G + kb] : 127u;
         }
       }
     };
@@ -697,9 +697,9 @@ __global__ void __launch_bounds__(Cfg<MODE, BN, STAGES, LIN>::kThreads, 1)
         constexpr int kQ = 4;
         float sa_q[kQ], sb_q[kQ], sb2_q[kQ];
         auto load_s = [&](int k, float &fa, float &fb, float &fb2) {
-          fa = row < args.M ? __ldg(sa + (int64_t)k * args.M + row) : 0.0f;
-          fb = __ldg(sb_row0 + k);
-          fb2 = C::kSub == 1 ? fb : __ldg(sb_row1 + k);
+          fa = row < args.M ? sa[(int64_t)k * args.M + row] : 0.0f;
+          fb = sb_row0[k];
+          fb2 = C::kSub == 1 ? fb : sb_row1[k];
         };
 #pragma unroll
         for (int d = 0; d < kQ; ++d)

@@ -602,7 +602,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<BN, STAGES, 
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
               float v = __uint_as_float(r[i]) * alpha;
-              if (a.bias != nullptr && col0 + i < a.N) v += __ldg(a.bias + col0 + i);
+              if (a.bias != nullptr && col0 + i < a.N) v += a.bias[col0 + i];
               packed[i] = __float_as_uint(v);
             }
           } else {
@@ -610,8 +610,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<BN, STAGES, 
             for (int i = 0; i < 32; ++i) {
               float v0 = __uint_as_float(r[2 * i]) * alpha, v1 = __uint_as_float(r[2 * i + 1]) * alpha;
               if (a.bias != nullptr) {
-                if (col0 + 2 * i < a.N) v0 += __ldg(a.bias + col0 + 2 * i);
-                if (col0 + 2 * i + 1 < a.N) v1 += __ldg(a.bias + col0 + 2 * i + 1);
+                if (col0 + 2 * i < a.N) v0 += a.bias[col0 + 2 * i];
+                if (col0 + 2 * i + 1 < a.N) v1 += a.bias[col0 + 2 * i + 1];
               }
               const __nv_bfloat162 h = __floats2bfloat162_rn(v0, v1);
               packed[i] = *reinterpret_cast<const uint32_t *>(&h);

@@ -92,13 +92,15 @@ struct SkinnyCfg {
 // One group scale as loaded (fp32 bits, or a UE8M0 byte) and as a
 // multiplier (2^(b - 127) for a byte).  The loads land in a queue of
 // registers and are converted only when used, so no thread waits on a load
-// it issued for a later slice.
+// it issued for a later slice.  They are plain loads, as every read of this
+// kernel of what the previous one, still running when this one starts, may
+// write (the read-only path wants data constant for the kernel's lifetime).
 template <int SFMT>
 __device__ __forceinline__ uint32_t skinny_scale_raw(const void *s, int64_t i) {
   if constexpr (SFMT == 0)
-    return __float_as_uint(__ldg(static_cast<const float *>(s) + i));
+    return __float_as_uint(static_cast<const float *>(s)[i]);
   else
-    return (uint32_t)__ldg(static_cast<const uint8_t *>(s) + i);
+    return (uint32_t)static_cast<const uint8_t *>(s)[i];
 }
 template <int SFMT>
 __device__ __forceinline__ float skinny_scale_value(uint32_t raw) {
@@ -305,7 +307,7 @@ __global__ void __launch_bounds__(SkinnyCfg<MP>::kThreads, 1)
     if (ks == 1) {
       const int64_t n = n0 + nl;
       if (ok && n < args.N) {
-        const float bn = args.bias != nullptr ? __ldg(args.bias + n) : 0.0f;
+        const float bn = args.bias != nullptr ? args.bias[n] : 0.0f;
 #pragma unroll
         for (int c = 0; c < C::kCols; ++c) {
           const int64_t m = mcol0 + c;
@@ -344,7 +346,7 @@ __global__ void __launch_bounds__(SkinnyCfg<MP>::kThreads, 1)
           v.x += p.x; v.y += p.y; v.z += p.z; v.w += p.w;
         }
         if (n < args.N) {
-          const float bn = args.bias != nullptr ? __ldg(args.bias + n) : 0.0f;
+          const float bn = args.bias != nullptr ? args.bias[n] : 0.0f;
           const float r[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
           for (int i = 0; i < 4; ++i)

@@ -375,12 +375,13 @@ __global__ void __launch_bounds__(512, 1) rmsnorm_grad_kernel(const NormGradArgs
 // out[n] (+)= sum over p < P of parts[p][n], in a fixed order: 32 columns per
 // CTA, warp w adds rows w, w + 32, ..., then the 32 warps' sums are added.
 // The first CTA also finishes a maximum: *top_out = max of tops[0 .. ntops)
-// (keys of non-negative floats; nullable).
-__global__ void __launch_bounds__(1024) column_sum_kernel(const float *__restrict__ parts,
-                                                          int64_t P, int64_t N, int accumulate,
-                                                          float *__restrict__ out,
-                                                          const uint32_t *__restrict__ tops,
-                                                          int ntops, uint32_t *top_out) {
+// (keys of non-negative floats; nullable).  (parts and tops are not declared
+// __restrict__: the previous kernel may still be writing them when this one
+// starts, and const __restrict__ data may be read through the read-only path.)
+__global__ void __launch_bounds__(1024) column_sum_kernel(const float *parts, int64_t P, int64_t N,
+                                                          int accumulate, float *out,
+                                                          const uint32_t *tops, int ntops,
+                                                          uint32_t *top_out) {
   __shared__ float s[32][33];
   __shared__ uint32_t top;
   if (threadIdx.x == 0) top = 0u;

@@ -291,11 +291,11 @@ __global__ void __launch_bounds__(256, 2)
 // Launched with programmatic stream serialization: it lets the next kernel
 // start at once (a GEMM that reads these codes then brings its weights into
 // L2 meanwhile, and waits for this kernel before it reads anything this
-// kernel writes) and waits itself for the kernel before it.
+// kernel writes) and waits itself for the kernel before it (which may still
+// be writing x: not declared __restrict__, so never read-only data).
 template <typename T, int F, int GS>
 __global__ void __launch_bounds__(256, 3)
-    quant_group_kernel(const T *__restrict__ x, int64_t M, int64_t K, int sfmt,
-                       uint8_t *__restrict__ q, void *scales) {
+    quant_group_kernel(const T *x, int64_t M, int64_t K, int sfmt, uint8_t *q, void *scales) {
   constexpr int kU = sizeof(T) == 2 ? 2 : 1;
   constexpr int kShift = GS == 128 ? 7 : 5;  // log2 of the group size
   launch_dependents();
