@@ -7,7 +7,10 @@
 //   gelu  z Phi(z)        gelu, tanh form  z s(2 sqrt(2/pi) (z + 0.044715 z^3))
 //
 // with s(z) = 1 / (1 + e^-z); the tanh form uses (1 + tanh u) / 2 = s(2u), so
-// that its left tail keeps its relative accuracy.  A NaN stays a NaN.
+// that its left tail keeps its relative accuracy.  A NaN stays a NaN; at an
+// infinite z (finite values near the top of fp32 are infinite in a bf16
+// pre-activation) every function and slope takes its limit: a factor that has
+// vanished there never meets an infinite one.
 //
 // Two values at a time: the products and sums are packed f32x2 instructions
 // (each half rounded as the scalar instruction), which halves what the
@@ -35,8 +38,23 @@ __device__ __forceinline__ float rcp_ftz(float x) {
 
 __device__ __forceinline__ F2 exp2_2(F2 a) { return each(a, [](float x) { return ex2_approx_ftz(x); }); }
 __device__ __forceinline__ F2 rcp_2(F2 a) { return each(a, [](float x) { return rcp_ftz(x); }); }
-__device__ __forceinline__ F2 abs_2(F2 a) { return each(a, [](float x) { return fabsf(x); }); }
 __device__ __forceinline__ F2 relu_2(F2 a) { return each(a, [](float x) { return max_nan(x, 0.0f); }); }
+
+// Bounds beyond which the logistic function and the normal tail are 0 or 1 in
+// fp32 (from |z| = 150 on) while z and z^3 are far from overflow.
+constexpr float kFar = 1e4f, kFarCubed = 1e3f;
+// z within [-b, b], one instruction: min(|z|, b) with the sign of z (b > 0)
+__device__ __forceinline__ F2 within_2(F2 a, float b) {
+  return each(a, [b](float x) {
+    float r;
+    asm("min.NaN.xorsign.abs.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(b));
+    return r;
+  });
+}
+// z where its logistic factor is not zero yet
+__device__ __forceinline__ F2 left_capped(F2 a) {
+  return each(a, [](float x) { return max_nan(x, -kFar); });
+}
 
 // s(-t / log2 e) = 1 / (1 + 2^t)
 __device__ __forceinline__ F2 logistic2(F2 t) { return rcp_2(exp2_2(t) + F2(1.0f)); }
@@ -47,12 +65,13 @@ constexpr float kT1 = -2.3022081985175f, kT3 = -0.10294323959671f;
 // 2 sqrt(2/pi) and 3 x 0.044715 of it: d/dz of its argument
 constexpr float kD1 = 1.5957691216057308f, kD3 = 0.21406444881478f;
 
-// E = e^(-z^2/2), a = |z| and Phi(-a) / E = erfcx(a / sqrt 2) / 2, which is t
-// times a degree-8 polynomial in t = 1 / (1 + 0.4 a / sqrt 2) (least squares
-// on Chebyshev nodes with the weights driven to equal relative error: 1.3e-7
-// over t in (0, 1], that is for every z).
+// E = e^(-z^2/2), a = |z| (at most kFar, where E is 0) and
+// Phi(-a) / E = erfcx(a / sqrt 2) / 2, which is t times a degree-8 polynomial
+// in t = 1 / (1 + 0.4 a / sqrt 2) (least squares on Chebyshev nodes with the
+// weights driven to equal relative error: 1.6e-7 with the coefficients as
+// rounded here, over t in (0, 1], that is for every z).
 __device__ __forceinline__ F2 normal_tail(F2 z, F2 &a, F2 &E) {
-  a = abs_2(z);
+  a = each(z, [](float x) { return fminf(fabsf(x), kFar); });  // (E keeps a NaN)
   E = exp2_2(z * z * F2(-0.72134752044448170f));
   const F2 t = rcp_2(fma2(a, F2(0.28284271247461901f), F2(1.0f)));
   F2 p(0.025127250701189041f);
@@ -74,8 +93,9 @@ __device__ __forceinline__ F2 act_value2(F2 z) {
     const F2 p = relu_2(z);
     return p * p;
   }
-  if constexpr (A == kActSilu) return z * logistic2(z * F2(kNegLog2e));
-  if constexpr (A == kActGeluTanh) return z * logistic2(z * fma2(z * z, F2(kT3), F2(kT1)));
+  if constexpr (A == kActSilu) return left_capped(z) * logistic2(z * F2(kNegLog2e));
+  if constexpr (A == kActGeluTanh)
+    return left_capped(z) * logistic2(z * fma2(z * z, F2(kT3), F2(kT1)));
   if constexpr (A == kActGelu) {
     // z Phi(z) = max(z, 0) - |z| Phi(-|z|)
     F2 a(0.0f), E(0.0f);
@@ -85,9 +105,7 @@ __device__ __forceinline__ F2 act_value2(F2 z) {
   return z;
 }
 
-// The derivative.  At finite z no product of a vanished factor and an
-// overflowed one is formed: the factors that vanish do so long before the
-// others leave fp32 (the tanh form's z^2 is capped where its slope is 0 or 1).
+// The derivative (z bounded where the slope is 0 or 1: see above).
 template <int A>
 __device__ __forceinline__ F2 act_slope2(F2 z) {
   if constexpr (A == kActRelu)
@@ -97,13 +115,13 @@ __device__ __forceinline__ F2 act_slope2(F2 z) {
     return p + p;
   }
   if constexpr (A == kActSilu) {
-    const F2 s = logistic2(z * F2(kNegLog2e));
-    return s * fma2(z, fma2(s, F2(-1.0f), F2(1.0f)), F2(1.0f));
+    const F2 b = within_2(z, kFar), s = logistic2(b * F2(kNegLog2e));
+    return s * fma2(b, fma2(s, F2(-1.0f), F2(1.0f)), F2(1.0f));
   }
   if constexpr (A == kActGeluTanh) {
-    const F2 zz = each(z * z, [](float x) { return fminf(x, 1e6f); });
-    const F2 s = logistic2(z * fma2(zz, F2(kT3), F2(kT1)));
-    return fma2(z * s, fma2(s, F2(-1.0f), F2(1.0f)) * fma2(zz, F2(kD3), F2(kD1)), s);
+    const F2 b = within_2(z, kFarCubed), bb = b * b;
+    const F2 s = logistic2(b * fma2(bb, F2(kT3), F2(kT1)));
+    return fma2(b * s, fma2(s, F2(-1.0f), F2(1.0f)) * fma2(bb, F2(kD3), F2(kD1)), s);
   }
   if constexpr (A == kActGelu) {
     // Phi(z) + z phi(z) = u for z < 0 and 1 - u otherwise, with

@@ -512,6 +512,7 @@ FP8_API int fp8_gemm_mx(const uint8_t *a, const uint32_t *la, const float *ga, c
  *
  *   FP8_ACT_RELU max(z, 0); RELU2 max(z, 0)^2; SILU z / (1 + e^-z);
  *   GELU z Phi(z); GELU_TANH z (1 + tanh(sqrt(2/pi)(z + 0.044715 z^3))) / 2.
+ *   At z = +inf and -inf: the limits (+inf and 0; NONE: z itself).
  *
  * residual  nullable [M, ld_residual] of residual_dt (fp8_out_dtype_t); may
  *           be c itself (same type and pitch).
@@ -569,7 +570,8 @@ FP8_API int fp8_gemm_group_epilogue(const uint8_t *a, const void *sa, const uint
  *   c <- dz (nullable with q)   q, q_amax as above (E5M2 for gradients)
  *   dbias[n] (+)= sum_m dz[m,n] in fp32, in a fixed order (no atomics)
  *   act        as above; the derivative is taken at the stored bf16 pre
- *              (relu and relu2: slope 0 at z = 0).
+ *              (relu and relu2: slope 0 at z = 0; at an infinite pre the
+ *              limits 1 and 0, relu2 +inf and 0).
  *   dbias      nullable device fp32 [N]; accumulate_dbias 1 adds to it.
  *   workspace  device scratch for dbias, 16-byte aligned, of at least
  *              fp8_act_backward_workspace(M, N) bytes; calls that can run at
