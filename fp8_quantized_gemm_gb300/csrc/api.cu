@@ -212,7 +212,7 @@ int get_workspace(cudaStream_t st, size_t need, void **out, int slot) {
     size_t bytes = need > 2 * w.bytes ? need : 2 * w.bytes;
     bytes = (bytes + (1u << 20) - 1) & ~(size_t)((1u << 20) - 1);
     if (cudaMalloc(&w.ptr, bytes) != cudaSuccess) return FP8_ERR_CUDA;
-    if (cudaMemset(w.ptr, 0, bytes) != cudaSuccess) return FP8_ERR_CUDA;
+    // (not cleared: every word a call reads, it has written)
     w.bytes = bytes;
   }
   *out = w.ptr;
