@@ -8,8 +8,6 @@
 #include <cudaTypedefs.h>
 #include <nvtx3/nvToolsExt.h>
 
-#include <map>
-#include <tuple>
 #include <mutex>
 #include <utility>
 
@@ -17,6 +15,7 @@
 #include "kernels.h"
 #include "norm.h"
 #include "support.h"
+#include "workspace.h"
 
 namespace {
 
@@ -44,19 +43,6 @@ struct DeviceState {
 constexpr int kMaxDevices = 64;
 DeviceState g_dev[kMaxDevices];
 std::mutex g_mu;
-
-// Device workspace of the UE8M0 per-group GEMM beyond one row tile: the
-// E8M0 words the byte scales are expanded into (see fp8_gemm_group_bias),
-// one buffer per (device, stream, slot) so that calls on different streams
-// never share it.  Allocated on first need and grown by doubling; never
-// inside a stream capture.  (Split K needs no workspace: the splits of a
-// tile reduce inside a thread-block cluster.)
-struct Workspace {
-  void *ptr = nullptr;
-  size_t bytes = 0;
-};
-constexpr int kWsWords = 1;
-std::map<std::tuple<int, cudaStream_t, int>, Workspace> g_ws;
 
 // CTA-pair GEMM path switch (on by default; fp8_set_option turns it off).
 bool g_use_pairs = true;
@@ -192,31 +178,6 @@ int vector_store_ok(const void *c, int64_t ldc, int out_dt) {
 // otherwise: accumulation, or an unaligned base or pitch).
 bool use_tma_store(const void *c, int64_t ldc, int out_dt, int accumulate) {
   return g_use_tma_store && accumulate == 0 && vector_store_ok(c, ldc, out_dt);
-}
-
-int get_workspace(cudaStream_t st, size_t need, void **out, int slot) {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return FP8_ERR_CUDA;
-  std::lock_guard<std::mutex> lk(g_mu);
-  Workspace &w = g_ws[std::make_tuple(dev, st, slot)];
-  if (w.bytes < need) {
-    cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
-    if (cudaStreamIsCapturing(st, &cs) != cudaSuccess) return FP8_ERR_CUDA;
-    if (cs != cudaStreamCaptureStatusNone) return FP8_ERR_UNSUPPORTED;  // warm up before capture
-    if (w.ptr != nullptr) {
-      if (cudaStreamSynchronize(st) != cudaSuccess || cudaFree(w.ptr) != cudaSuccess)
-        return FP8_ERR_CUDA;
-      w.ptr = nullptr;
-      w.bytes = 0;
-    }
-    size_t bytes = need > 2 * w.bytes ? need : 2 * w.bytes;
-    bytes = (bytes + (1u << 20) - 1) & ~(size_t)((1u << 20) - 1);
-    if (cudaMalloc(&w.ptr, bytes) != cudaSuccess) return FP8_ERR_CUDA;
-    // (not cleared: every word a call reads, it has written)
-    w.bytes = bytes;
-  }
-  *out = w.ptr;
-  return FP8_OK;
 }
 
 // ep: the linear layer's epilogue (nullable).
@@ -480,10 +441,9 @@ int run_group(const uint8_t *a, const void *sa, const uint8_t *b, const void *sb
     if ((rc = device_state(&d)) != FP8_OK) return rc;
     const size_t G = (size_t)(K / 128);
     const size_t mpad = (size_t)(M + 127) / 128 * 128, npad = (size_t)(N + 127) / 128 * 128;
-    void *w = nullptr;
-    if ((rc = get_workspace((cudaStream_t)stream, G * (mpad + npad) * 4, &w, kWsWords)) != FP8_OK)
-      return rc;
-    uint32_t *la = static_cast<uint32_t *>(w), *lb = la + G * mpad;
+    fp8k::Workspace w;
+    if ((rc = to_status(w.get((cudaStream_t)stream, G * (mpad + npad) * 4))) != FP8_OK) return rc;
+    uint32_t *la = static_cast<uint32_t *>(w.ptr()), *lb = la + G * mpad;
     if ((rc = to_status(fp8k::launch_ue8m0_words(static_cast<const uint8_t *>(sa),
                                                  static_cast<const uint8_t *>(sb), M, N, K, la, lb,
                                                  d->sms, (cudaStream_t)stream))) != FP8_OK)
@@ -1102,10 +1062,9 @@ int fp8_gemm_group_experts(const uint8_t *a, const void *sa, const uint8_t *b, c
     // block-scaled kernel; the A words are stored per expert row tile
     const int64_t G = K / 128, tmax = (M + 127) / 128 + experts;
     const size_t a_words = (size_t)tmax * (size_t)G * 128, b_words = (size_t)G * experts * N;
-    void *w = nullptr;
-    if ((rc = get_workspace((cudaStream_t)stream, (a_words + b_words) * 4, &w, kWsWords)) != FP8_OK)
-      return rc;
-    uint32_t *la = static_cast<uint32_t *>(w), *lb = la + a_words;
+    fp8k::Workspace w;
+    if ((rc = to_status(w.get((cudaStream_t)stream, (a_words + b_words) * 4))) != FP8_OK) return rc;
+    uint32_t *la = static_cast<uint32_t *>(w.ptr()), *lb = la + a_words;
     if ((rc = to_status(fp8k::launch_ue8m0_words_experts(
              static_cast<const uint8_t *>(sa), static_cast<const uint8_t *>(sb), offsets, experts,
              M, N, K, tmax, la, lb, d->sms, (cudaStream_t)stream))) != FP8_OK)

@@ -401,6 +401,13 @@ FP8_API int fp8_gemm_tensor_grouped(const fp8_gemm_problem_t *problems, int coun
  *   previous kernel on `stream` ends, and then reads and writes nothing that
  *   kernel may write until it has completed.  Every per-group GEMM launch and
  *   fp8_quantize_token_group (/32) are launched that way.
+ *   UE8M0 scales beyond 128 rows (_experts: 256) use device scratch of the library, 4
+ *   bytes per row of a and of b and K group: one buffer per stream, allocated
+ *   or grown (which waits for the stream) by the first call that needs it.  A
+ *   call inside a stream capture needs no call before it: its scratch belongs
+ *   to the graph, so replays share it with no direct call and no other graph,
+ *   and it goes with the graph.  The same holds for fp8_gemm_group_bias,
+ *   _epilogue and _experts.
  */
 FP8_API int fp8_gemm_group(const uint8_t *a, const void *sa, const uint8_t *b, const void *sb,
                    int sfmt, int64_t M, int64_t N, int64_t K, void *c, int64_t ldc,
