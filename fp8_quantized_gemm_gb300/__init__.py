@@ -512,7 +512,13 @@ _c_tensor_epilogue = _lib.fp8_gemm_tensor_epilogue
 _c_group_epilogue = _lib.fp8_gemm_group_epilogue
 _c_act_backward = _lib.fp8_gemm_tensor_act_backward
 _c_norm_grad_ws, _c_act_ws = _lib.fp8_rmsnorm_backward_workspace, _lib.fp8_act_backward_workspace
-_raw_stream, _get_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+# (torch's raw accessors where this torch has them: its public functions build
+# objects around the same values)
+_get_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+_capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing", None) or (
+    torch.cuda.is_current_stream_capturing)
 _BF16, _F32 = torch.bfloat16, torch.float32
 
 
@@ -589,7 +595,6 @@ def _check(name, rc):
 # from torch's allocator in the current stream's order.
 _KEPT = 8 << 20
 _kept = threading.local()
-_capturing = torch._C._cuda_isCurrentStreamCapturing
 
 
 def _scratch(nbytes, workspace, device, stream):
