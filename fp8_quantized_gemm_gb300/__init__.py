@@ -517,6 +517,9 @@ _c_norm_grad_ws, _c_act_ws = _lib.fp8_rmsnorm_backward_workspace, _lib.fp8_act_b
 _get_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+_stream_of = getattr(torch._C, "_cuda_getCurrentStream", None)
+_stream_id = (lambda dev: _stream_of(dev)[0]) if _stream_of else (
+    lambda dev: torch.cuda.current_stream(dev).stream_id)
 _capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing", None) or (
     torch.cuda.is_current_stream_capturing)
 _BF16, _F32 = torch.bfloat16, torch.float32
@@ -589,31 +592,43 @@ def _check(name, rc):
 
 
 # Scratch of calls that bring none.  Up to _KEPT bytes come from a buffer kept
-# per thread, device and stream (calls that share it follow one another on that
-# stream; allocating it anew costs 3 of a small call's 8 us); larger ones, and
-# calls recorded into a graph, whose memory must live as long as the graph, come
-# from torch's allocator in the current stream's order.
+# per thread and stream (calls that share it follow one another on that stream;
+# allocating it anew costs 3 of a small call's 8 us), as large as the largest of
+# these calls needed.  torch's own streams live as long as the process, and their
+# ids are odd, or 0 for the default one; any other stream's id is its handle,
+# which may be issued again while the work of the stream that had it still runs,
+# so its calls keep nothing.  Those, larger ones, and calls recorded into a
+# graph, whose memory must live as long as the graph, take theirs from torch's
+# allocator in the current stream's order.
 _KEPT = 8 << 20
+_KEPT_STEP = 64 << 10
 _kept = threading.local()
 
 
-def _scratch(nbytes, workspace, device, stream):
-    """(pointer, bytes, owner) of a call's scratch; the owner lives through it."""
+def _scratch(nbytes, workspace, like, stream):
+    """(pointer, bytes, owner) of a call's scratch; the owner lives through it.
+    like: one of the call's operands, all checked before."""
     if workspace is not None:
         return _flat(workspace), workspace.nbytes, None
     if stream is not None:
         raise ValueError("a call on an explicit stream needs an explicit workspace")
-    if nbytes > _KEPT or _capturing():
-        t = torch.empty(nbytes, dtype=torch.uint8, device=device)
-        return t.data_ptr(), nbytes, t
     dev = _get_device()
-    try:
-        return _kept.buffers[dev, _raw_stream(dev)]
-    except (AttributeError, KeyError):
-        if not hasattr(_kept, "buffers"):
-            _kept.buffers = {}
-        t = torch.empty(_KEPT, dtype=torch.uint8, device=device)
-        return _kept.buffers.setdefault((dev, _raw_stream(dev)), (t.data_ptr(), _KEPT, t))
+    if like.device.index != dev:
+        raise ValueError("operands must be on the current device")
+    if nbytes <= _KEPT and not _capturing():
+        sid = _stream_id(dev)
+        if sid & 1 or sid == 0:
+            try:
+                kept = _kept.buffers.get((dev, sid))
+            except AttributeError:
+                _kept.buffers, kept = {}, None
+            if kept is None or kept[1] < nbytes:
+                size = max(_KEPT_STEP, 1 << (nbytes - 1).bit_length())
+                t = torch.empty(size, dtype=torch.uint8, device=like.device)
+                kept = _kept.buffers[dev, sid] = (t.data_ptr(), size, t)
+            return kept
+    t = torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+    return t.data_ptr(), nbytes, t
 
 
 def fp8_rmsnorm_quantize(x, w, eps, fmt, q, *, residual=None, sum_out=None, scale=None,
@@ -658,18 +673,17 @@ def fp8_rmsnorm_backward(dy, r, inv_rms, w, dx, *, d_residual=None, dw=None, acc
     (with dw): device scratch; None: the binding's own."""
     shape, t = r.shape, r.dtype
     m, k = shape
-    pws, ws_bytes, keep = (0, 0, None) if dw is None else _scratch(
-        _c_norm_grad_ws(m, k), workspace, r.device, stream)
     py, ldy = _rows(dy, shape, dy.dtype, "dy")
     pr, ldr = _rows(r, shape, t, "r")
     pe, lde = _rows(d_residual, shape, t, "d_residual")
     px, ldx = _rows(dx, shape, t, "dx")
     pw, wdt = _gain(w, k)
-    d = _pack_norm_grad(py, pr, pw, pe, _vector(inv_rms, m, "inv_rms"), _in_dt(dy), _in_dt(r), wdt,
-                        m, k, ldy, ldr, lde, ldx, px, _vector(dw, k, "dw"),
-                        int(bool(accumulate_dw)), _codes(q, m * k, "q"), fmt,
-                        _vector(scale, 1, "scale"), _vector(amax_out, 1, "amax_out"),
-                        pws, ws_bytes)
+    pi, pdw, pq = _vector(inv_rms, m, "inv_rms"), _vector(dw, k, "dw"), _codes(q, m * k, "q")
+    ps, pa = _vector(scale, 1, "scale"), _vector(amax_out, 1, "amax_out")
+    pws, ws_bytes, keep = (0, 0, None) if dw is None else _scratch(
+        _c_norm_grad_ws(m, k), workspace, r, stream)
+    d = _pack_norm_grad(py, pr, pw, pe, pi, _in_dt(dy), _in_dt(r), wdt, m, k, ldy, ldr, lde, ldx,
+                        px, pdw, int(bool(accumulate_dw)), pq, fmt, ps, pa, pws, ws_bytes)
     _check("fp8_rmsnorm_backward", _c_norm_grad(d, _on(stream)))
 
 
@@ -740,12 +754,13 @@ def fp8_gemm_tensor_act_backward(a, fa, b, fb, sa, sb, pre, act, *, out=None, q=
     binding's own."""
     shape, p = _epilogue_problem(a, fa, b, fb, sa, sb, out, a_layout, b_layout, None)
     m, n = shape
-    pws, ws_bytes, keep = (0, 0, None) if dbias is None else _scratch(
-        _c_act_ws(m, n), workspace, pre.device, stream)
     pp, ldp = _rows(pre, shape, _BF16, "pre")
-    e = _pack_act_grad(act, pp, ldp, _codes(q, m * n, "q"), q_fmt, _vector(q_scale, 1, "q_scale"),
-                       _vector(q_amax, 1, "q_amax"), _vector(dbias, n, "dbias"),
-                       int(bool(accumulate_dbias)), pws, ws_bytes)
+    pq, ps = _codes(q, m * n, "q"), _vector(q_scale, 1, "q_scale")
+    pa, pdb = _vector(q_amax, 1, "q_amax"), _vector(dbias, n, "dbias")
+    pws, ws_bytes, keep = (0, 0, None) if dbias is None else _scratch(
+        _c_act_ws(m, n), workspace, pre, stream)
+    e = _pack_act_grad(act, pp, ldp, pq, q_fmt, ps, pa, pdb, int(bool(accumulate_dbias)), pws,
+                       ws_bytes)
     _check("fp8_gemm_tensor_act_backward", _c_act_backward(p, e, _on(stream)))
 
 
