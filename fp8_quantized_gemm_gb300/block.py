@@ -23,6 +23,13 @@ operand reaches memory only as codes, written by the kernel that forms it:
   update    fp8_delayed_state_update_multi, fp8_adamw_multi (which also writes
             the next step's weight codes)
 
+Blocks are chained from the top one down: ``drq`` holds the codes of dr under
+``drq_scale``, the scale of their own step (``update`` replaces the live one), and
+the block below takes both with dr, before this block's next backward pass:
+
+  top.step(x1, dout, s1)
+  below.step(x0, top.dr, s0, doutq=top.drq, dout_scale=top.drq_scale)
+
 ``PreNormMLP`` is the forward pass alone with fine-grained scales (1x128 groups
 times 128x128 blocks), from one decoded token to a prefill chunk.
 
@@ -60,6 +67,7 @@ class PreNormMLPTrainer:
         self.hist = torch.zeros((7, history), device=dev)
         self.scale = torch.ones(7, device=dev)
         self.amax = torch.zeros(7, device=dev)
+        self.drq_scale = torch.ones(1, device=dev)
         T = tokens
         self.r, self.out, self.dr = (new(T, d, t=bf) for _ in range(3))
         self.inv, self.z, self.dy = new(T), new(T, ffn, t=bf), new(T, d, t=bf)
@@ -102,8 +110,11 @@ class PreNormMLPTrainer:
     def backward(self, dout: torch.Tensor, doutq=None, dout_scale=None):
         """dr [tokens, d] bf16, the gradient of x and of the stream.  doutq,
         dout_scale: E5M2 codes of dout where the block above has written them
-        (its ``drq`` and scale)."""
+        (its ``drq`` and ``drq_scale``)."""
+        if (doutq is None) != (dout_scale is None):
+            raise ValueError("doutq and dout_scale come together")
         E4, E5, MN = F.E4M3, F.E5M2, F.MN_MAJOR
+        self.drq_scale.copy_(self._s(DR))  # what drq is written under below
         if doutq is None:
             doutq, dout_scale = self.doutq, self._s(DOUT)
             F.fp8_quantize_tensor(dout, E5, doutq, scale=dout_scale, amax_out=self._a(DOUT))
@@ -130,9 +141,9 @@ class PreNormMLPTrainer:
                            F.E5M2 if i in (DZ, DOUT, DR) else F.E4M3) for i in range(7)])
         F.fp8_adamw_multi(self.items, self.step_dev, **self.hp)
 
-    def step(self, x, dout, stream=None):
+    def step(self, x, dout, stream=None, doutq=None, dout_scale=None):
         self.forward(x, stream)
-        self.backward(dout)
+        self.backward(dout, doutq, dout_scale)
         self.update()
 
 
