@@ -100,7 +100,13 @@ int device_state(DeviceState **out) {
   return FP8_OK;
 }
 
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned_to(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+bool aligned16(const void *p) { return aligned_to(p, 16); }
+// Group scales are read as the elements they are: fp32, or bytes.
+bool scales_aligned(const void *sa, const void *sb, int sfmt) {
+  const uintptr_t n = sfmt == FP8_SCALE_F32 ? 4 : 1;
+  return aligned_to(sa, n) && aligned_to(sb, n);
+}
 bool valid_fmt(int f) { return f == FP8_E4M3 || f == FP8_E5M2; }
 bool valid_in(int d) { return d == FP8_IN_BF16 || d == FP8_IN_F32; }
 constexpr int64_t kMaxDim = (int64_t)1 << 31;
@@ -263,6 +269,8 @@ int check_tensor_problem(const fp8_gemm_problem_t &p) {
   // multiple of 16 bytes for its tensor map
   const bool a_mn = p.a_layout == FP8_MN_MAJOR, b_mn = p.b_layout == FP8_MN_MAJOR;
   if (!aligned16(p.a) || !aligned16(p.b)) return FP8_ERR_MISALIGNED;
+  if (!aligned_to(p.sa, 4) || !aligned_to(p.sb, 4) || !aligned_to(p.bias, 4))
+    return FP8_ERR_MISALIGNED;
   if ((!a_mn || !b_mn) && p.K % 16 != 0) return FP8_ERR_MISALIGNED;
   if ((a_mn && p.M % 16 != 0) || (b_mn && p.N % 16 != 0)) return FP8_ERR_MISALIGNED;
   if (p.adamw != nullptr && p.swiglu != nullptr) return FP8_ERR_INVALID_ARG;
@@ -319,8 +327,6 @@ int run_tensor_problem(const fp8_gemm_problem_t &p, cudaStream_t st) {
 constexpr int kNormSms = 152;
 // Slots for the maxima of the activation gradient's epilogue warps.
 constexpr int64_t kGradTops = 160 * fp8k::kEpWarps;
-
-bool aligned_to(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
 // A nullable [rows, ld] operand read and written in 16-byte vectors of eight
 // elements (fp32: two).
@@ -400,6 +406,7 @@ int run_group(const uint8_t *a, const void *sa, const uint8_t *b, const void *sb
   if (rc != FP8_OK) return rc;
   if (sa == nullptr || sb == nullptr) return FP8_ERR_INVALID_ARG;
   if (sfmt != FP8_SCALE_F32 && sfmt != FP8_SCALE_UE8M0) return FP8_ERR_INVALID_ARG;
+  if (!scales_aligned(sa, sb, sfmt) || !aligned_to(bias, 4)) return FP8_ERR_MISALIGNED;
   if ((rc = check_output(c, N, ldc, FP8_OUT_BF16)) != FP8_OK) return rc;
   GemmArgs args{};
   args.M = M; args.N = N; args.K = K; args.fa = FP8_E4M3; args.fb = FP8_E4M3;
@@ -704,6 +711,7 @@ int fp8_gemm_group32(const uint8_t *a, const float *sa, const uint8_t *b, const 
   int rc = check_gemm_common(a, b, M, N, K, 128);
   if (rc != FP8_OK) return rc;
   if (sa == nullptr || sb == nullptr) return FP8_ERR_INVALID_ARG;
+  if (!scales_aligned(sa, sb, FP8_SCALE_F32)) return FP8_ERR_MISALIGNED;
   if ((rc = check_output(c, N, ldc, FP8_OUT_BF16)) != FP8_OK) return rc;
   GemmArgs args{};
   args.M = M; args.N = N; args.K = K; args.fa = FP8_E4M3; args.fb = FP8_E4M3;
@@ -1029,6 +1037,7 @@ int fp8_gemm_group_experts(const uint8_t *a, const void *sa, const uint8_t *b, c
   if (experts < 1 || experts > fp8k::kMaxExperts) return FP8_ERR_INVALID_ARG;
   if (experts * N >= kMaxDim) return FP8_ERR_INVALID_ARG;
   if (sfmt != FP8_SCALE_F32 && sfmt != FP8_SCALE_UE8M0) return FP8_ERR_INVALID_ARG;
+  if (!scales_aligned(sa, sb, sfmt) || !aligned_to(offsets, 4)) return FP8_ERR_MISALIGNED;
   if ((rc = check_output(c, N, ldc, FP8_OUT_BF16)) != FP8_OK) return rc;
   DeviceState *d = nullptr;
   if ((rc = device_state(&d)) != FP8_OK) return rc;
@@ -1085,7 +1094,8 @@ int fp8_gemm_mx(const uint8_t *a, const uint32_t *la, const float *ga, const uin
   int rc = check_gemm_common(a, b, M, N, K, 128);
   if (rc != FP8_OK) return rc;
   if (la == nullptr || lb == nullptr || ga == nullptr || gb == nullptr) return FP8_ERR_INVALID_ARG;
-  if (!aligned16(la) || !aligned16(lb)) return FP8_ERR_MISALIGNED;
+  if (!aligned16(la) || !aligned16(lb) || !aligned_to(ga, 4) || !aligned_to(gb, 4))
+    return FP8_ERR_MISALIGNED;
   if ((rc = check_output(c, N, ldc, out_dt)) != FP8_OK) return rc;
   GemmArgs args{};
   args.M = M; args.N = N; args.K = K; args.fa = FP8_E4M3; args.fb = FP8_E4M3;
@@ -1101,7 +1111,8 @@ int fp8_gemm_mx_rows(const uint8_t *a, const uint32_t *la, const float *ga, cons
   int rc = check_gemm_common(a, b, M, N, K, 128);
   if (rc != FP8_OK) return rc;
   if (la == nullptr || lb == nullptr || ga == nullptr || gb == nullptr) return FP8_ERR_INVALID_ARG;
-  if (!aligned16(la) || !aligned16(lb)) return FP8_ERR_MISALIGNED;
+  if (!aligned16(la) || !aligned16(lb) || !aligned_to(ga, 4) || !aligned_to(gb, 4))
+    return FP8_ERR_MISALIGNED;
   if ((rc = check_output(c, N, ldc, out_dt)) != FP8_OK) return rc;
   GemmArgs args{};
   args.M = M; args.N = N; args.K = K; args.fa = FP8_E4M3; args.fb = FP8_E4M3;

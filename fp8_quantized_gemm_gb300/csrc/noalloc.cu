@@ -69,6 +69,9 @@ int gemm_group_noalloc(const uint8_t *a, const void *sa, const uint8_t *b, const
     return FP8_ERR_INVALID_ARG;
   if (K % 128 != 0 || !aligned16(a) || !aligned16(b) || (reinterpret_cast<uintptr_t>(c) & 1u))
     return FP8_ERR_MISALIGNED;
+  if (sfmt == FP8_SCALE_F32 &&
+      ((reinterpret_cast<uintptr_t>(sa) | reinterpret_cast<uintptr_t>(sb)) & 3u) != 0)
+    return FP8_ERR_MISALIGNED;
 
   int sms = 0;
   uint32_t *err = nullptr;
