@@ -331,8 +331,9 @@ __device__ __forceinline__ void add_rows(const GemmArgs &a, const T *src, int64_
 // Forward epilogue of one chunk (v: z of this lane's row).  AHEAD: `in` holds a
 // bf16 residual of fetch_chunk; an fp32 one has too many registers for that,
 // and so has any in the kernels that keep a tile's accumulators in registers
-// (FP32 group scales: 4096 x 7168 x 2048 with bias and silu 110 -> 92 us over
-// a pass of its own per 16 columns).  Every lane of the warp calls it.
+// (FP32 group scales: 4096 x 7168 x 2048 with bias and silu 92 us on operands
+// that L2 still holds, 97-100 on others; a pass of its own per 16 columns took
+// 110; the same product without an epilogue takes 76).  Every lane of the warp calls it.
 template <bool AHEAD>
 __device__ __forceinline__ void linear_chunk(const GemmArgs &a, const LinearEp &e, int64_t row0,
                                              int64_t col0, float (&v)[32], const RowIn &in,

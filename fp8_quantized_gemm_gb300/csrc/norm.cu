@@ -17,7 +17,13 @@
 // with one barrier (the partial sums alternate between two buffers), and has
 // the loads of its next row in flight meanwhile.  Measured (HBM's copy rate
 // 6690 GB/s): forward 16384 x 4096 with residual and per-tensor codes 75.4 us,
-// 93% of it; backward with codes and dw 102-103 us, 88%.  For the backward pass
+// 93% of it; 1x128 groups 76-78 us, one-level MX 82 (their scales go out a few
+// bytes at a time, a row of the group-major layout each); an fp32 stream 143-151
+// (86-91%: two vectors of fp32 per thread spill a few registers of the 64).
+// Backward with codes and dw 102-103 us, 88%; an fp32 stream 180 (95%).  Rows of
+// more than 8192 elements take four vectors per thread, which leaves no
+// registers to prefetch the next row: 4096 x 14336 126-128 us (62%), fp32 235
+// (64%).  For the backward pass
 // a ring of rows in shared memory filled by bulk copies measured 101-104 us
 // at 4096 columns and 135 at 2048 (a row's chain of reduction, barrier and
 // second pass bounds it, not the bytes in flight).

@@ -561,9 +561,9 @@ FP8_API int fp8_gemm_tensor_epilogue(const fp8_gemm_problem_t *problem,
                                      const fp8_linear_epilogue_t *epilogue, fp8_stream_t stream);
 
 /* fp8_gemm_group_epilogue: fp8_gemm_group_bias with the epilogue; bf16 c
- * (required), no codes (q null, else FP8_ERR_UNSUPPORTED: the next product's
- * 1x128 scales depend on the whole group).  1-128 rows always run the few-row
- * kernel. */
+ * (required), no codes (q null, else FP8_ERR_UNSUPPORTED: codes of the result
+ * under 1x128 scales are fp8_quantize_token_group's).  1-128 rows always run
+ * the few-row kernel. */
 FP8_API int fp8_gemm_group_epilogue(const uint8_t *a, const void *sa, const uint8_t *b,
                                     const void *sb, int sfmt, int64_t M, int64_t N, int64_t K,
                                     const float *bias, const fp8_linear_epilogue_t *epilogue,
