@@ -399,11 +399,13 @@ FP8_API int fp8_gemm_tensor_grouped(const fp8_gemm_problem_t *problems, int coun
  *   With 1-128 rows the call runs the few-row kernel (FP8_OPT_GEMM_SKINNY),
  *   launched with programmatic stream serialization: it may start before the
  *   previous kernel on `stream` ends, and then reads and writes nothing that
- *   kernel may write until it has completed.  Every per-group GEMM launch and
- *   fp8_quantize_token_group (/32) are launched that way.
- *   UE8M0 scales beyond 128 rows (_experts: 256) use device scratch of the library, 4
- *   bytes per row of a and of b and K group: one buffer per stream, allocated
- *   or grown (which waits for the stream) by the first call that needs it.  A
+ *   kernel may write until it has completed.  Every per-group GEMM launch but
+ *   the CTA-pair one (FP32 scales, large M) and fp8_quantize_token_group (/32)
+ *   are launched that way.
+ *   UE8M0 scales beyond 128 rows (_experts: 256) use device scratch of the
+ *   library, 4 bytes per row of a and of b and K group: one buffer per stream,
+ *   allocated or grown (which waits for the stream) by the first call that
+ *   needs it; beyond 64 streams, allocated and freed in the stream's order.  A
  *   call inside a stream capture needs no call before it: its scratch belongs
  *   to the graph, so replays share it with no direct call and no other graph,
  *   and it goes with the graph.  The same holds for fp8_gemm_group_bias,
