@@ -52,11 +52,14 @@ State &state() {
   return *s;
 }
 
-void give_back(const Buffer &b) {
+void give_back(const Buffer &b) noexcept {
   if (b.ptr == nullptr) return;
-  State &s = state();
-  std::lock_guard<std::mutex> lk(s.free_mu);
-  s.free.push_back(b);
+  try {
+    State &s = state();
+    std::lock_guard<std::mutex> lk(s.free_mu);
+    s.free.push_back(b);
+  } catch (...) {  // no host memory for the list: the buffer stays unused
+  }
 }
 
 void release(void *p) {  // of a graph's reference
@@ -107,10 +110,13 @@ cudaError_t for_capture(int dev, cudaStream_t st, unsigned long long capture, cu
                         size_t need, void **out) {
   Recorded &r = state().recorded[{dev, st}];
   if (r.capture != capture || r.buf.bytes < need) {
-    Buffer b;
-    cudaError_t e = take(dev, need, &b);
-    if (e != cudaSuccess) return e;
-    Buffer *owned = new Buffer(b);
+    Buffer *owned = new Buffer;
+    cudaError_t e = take(dev, need, owned);
+    if (e != cudaSuccess) {
+      delete owned;
+      return e;
+    }
+    const Buffer b = *owned;
     cudaUserObject_t ref = nullptr;
     e = cudaUserObjectCreate(&ref, owned, release, 1, cudaUserObjectNoDestructorSync);
     if (e != cudaSuccess) {
@@ -148,6 +154,14 @@ cudaError_t for_stream(Buffer &w, int dev, cudaStream_t st, size_t need, void **
 }  // namespace
 
 cudaError_t Workspace::get(cudaStream_t st, size_t need) {
+  try {  // the callers are C functions
+    return find(st, need);
+  } catch (...) {
+    return cudaErrorMemoryAllocation;
+  }
+}
+
+cudaError_t Workspace::find(cudaStream_t st, size_t need) {
   int dev = 0;
   unsigned long long id = 0, capture = 0;
   cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;

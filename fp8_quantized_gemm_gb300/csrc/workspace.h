@@ -22,6 +22,8 @@ class Workspace {
   void *ptr() const { return ptr_; }
 
  private:
+  cudaError_t find(cudaStream_t st, size_t need);
+
   std::unique_lock<std::mutex> lock_;
   void *ptr_ = nullptr;
   cudaStream_t st_ = nullptr;
