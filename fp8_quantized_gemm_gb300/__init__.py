@@ -37,6 +37,7 @@ OUT_F32, OUT_BF16 = 0, 1
 K_MAJOR, MN_MAJOR = 0, 1
 ACT_NONE, ACT_RELU, ACT_RELU2, ACT_SILU, ACT_GELU_TANH, ACT_GELU = 0, 1, 2, 3, 4, 5
 NORM_TENSOR, NORM_GROUP, NORM_MX = 0, 1, 2
+IDS_I32, IDS_I64 = 0, 1
 
 _vp, _i64, _int, _d = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_double
 _SIGS = {
@@ -78,6 +79,12 @@ _SIGS = {
     "fp8_gemm_tensor_act_backward": [_vp, _vp, _vp],
     "fp8_gemm_group_epilogue": [_vp, _vp, _vp, _vp, _int, _i64, _i64, _i64, _vp, _vp, _vp, _i64,
                                 _vp],
+    "fp8_experts_sort": [_vp, _int, _i64, _i64, _int, _vp, _vp, _vp, _vp],
+    "fp8_experts_gather": [_vp, _vp],
+    "fp8_experts_combine": [_vp, _vp],
+    "fp8_experts_combine_backward": [_vp, _vp],
+    "fp8_act_checkpoint": [_vp, _vp],
+    "fp8_act_checkpoint_backward": [_vp, _vp],
     "fp8_get_last_device_error": [ctypes.POINTER(ctypes.c_int), _vp],
     "fp8_set_option": [_int, _int],
 }
@@ -762,6 +769,261 @@ def fp8_gemm_tensor_act_backward(a, fa, b, fb, sa, sb, pre, act, *, out=None, q=
     e = _pack_act_grad(act, pp, ldp, pq, q_fmt, ps, pa, pdb, int(bool(accumulate_dbias)), pws,
                        ws_bytes)
     _check("fp8_gemm_tensor_act_backward", _c_act_backward(p, e, _on(stream)))
+
+
+# ------------------- tokens to their experts and back, 8-bit checkpoints --
+
+class ExpertsGather(ctypes.Structure):
+    """fp8_experts_gather_t (include/fp8gemm.h)."""
+    _fields_ = [("x", _vp), ("dt", _int), ("ld_x", _i64), ("xq", _vp), ("x_scales", _vp),
+                ("rows", _vp), ("T", _i64), ("S", _i64), ("K", _i64), ("M", _i64), ("fmt", _int),
+                ("sfmt", _int), ("q", _vp), ("scales", _vp), ("out", _vp), ("ld_out", _i64)]
+
+
+class ExpertsCombine(ctypes.Structure):
+    """fp8_experts_combine_t (include/fp8gemm.h)."""
+    _fields_ = [("x", _vp), ("x_dt", _int), ("ld_x", _i64), ("rows", _vp), ("weights", _vp),
+                ("T", _i64), ("S", _i64), ("K", _i64), ("M", _i64), ("residual", _vp),
+                ("ld_residual", _i64), ("out", _vp), ("out_dt", _int), ("ld_out", _i64)]
+
+
+class ExpertsCombineGrad(ctypes.Structure):
+    """fp8_experts_combine_grad_t (include/fp8gemm.h)."""
+    _fields_ = [("dy", _vp), ("dy_dt", _int), ("ld_dy", _i64), ("x", _vp), ("x_dt", _int),
+                ("ld_x", _i64), ("rows", _vp), ("weights", _vp), ("T", _i64), ("S", _i64),
+                ("K", _i64), ("M", _i64), ("d_weights", _vp), ("q", _vp), ("scales", _vp),
+                ("fmt", _int), ("sfmt", _int), ("dx", _vp), ("dx_dt", _int), ("ld_dx", _i64)]
+
+
+class ActCheckpoint(ctypes.Structure):
+    """fp8_act_checkpoint_t (include/fp8gemm.h)."""
+    _fields_ = [("act", _int), ("h", _vp), ("ld_h", _i64), ("u", _vp), ("ld_u", _i64),
+                ("M", _i64), ("N", _i64), ("valid_rows", _vp), ("mode", _int), ("fmt", _int),
+                ("sfmt", _int), ("q", _vp), ("scale", _vp), ("scales", _vp), ("amax_out", _vp),
+                ("keep_sfmt", _int), ("h_q", _vp), ("h_scales", _vp), ("u_q", _vp),
+                ("u_scales", _vp), ("out", _vp), ("ld_out", _i64)]
+
+
+class ActCheckpointGrad(ctypes.Structure):
+    """fp8_act_checkpoint_grad_t (include/fp8gemm.h)."""
+    _fields_ = [("act", _int), ("da", _vp), ("ld_da", _i64), ("h_q", _vp), ("h_scales", _vp),
+                ("u_q", _vp), ("u_scales", _vp), ("keep_sfmt", _int), ("M", _i64), ("N", _i64),
+                ("valid_rows", _vp), ("mode", _int), ("fmt", _int), ("sfmt", _int), ("dh_q", _vp),
+                ("du_q", _vp), ("ld_q", _i64), ("scale_dh", _vp), ("scale_du", _vp),
+                ("dh_scales", _vp), ("du_scales", _vp), ("amax_dh", _vp), ("amax_du", _vp),
+                ("dh", _vp), ("du", _vp), ("ld_d", _i64)]
+
+
+_pack_gather, _pack_combine = _packer(ExpertsGather), _packer(ExpertsCombine)
+_pack_combine_grad = _packer(ExpertsCombineGrad)
+_pack_act, _pack_act_ckpt_grad = _packer(ActCheckpoint), _packer(ActCheckpointGrad)
+_c_sort, _c_gather = _lib.fp8_experts_sort, _lib.fp8_experts_gather
+_c_combine, _c_combine_grad = _lib.fp8_experts_combine, _lib.fp8_experts_combine_backward
+_c_act, _c_act_grad = _lib.fp8_act_checkpoint, _lib.fp8_act_checkpoint_backward
+_I32 = torch.int32
+
+
+def _here(*tensors):
+    """The tensors (None skipped) lie on the current device."""
+    dev = _get_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError("operands must be on the current device")
+
+
+def _ints(t, n, what):
+    """Device pointer of n contiguous int32 values (None -> 0)."""
+    if t is None:
+        return 0
+    if t.dtype != _I32 or t.numel() != n or not t.is_cuda or not t.is_contiguous():
+        raise ValueError("%s must be contiguous CUDA int32 [%d]" % (what, n))
+    return t.data_ptr()
+
+
+def _grouped_rows(t, k, what):
+    """Rows of the grouped side: M of a matrix [M, k]."""
+    if t.dim() != 2 or t.shape[1] != k:
+        raise ValueError("%s must be [M, %d]" % (what, k))
+    return t.shape[0]
+
+
+def _group_codes(q, scales, m, k, sfmt, what):
+    """(codes, scales) pointers of [m, k] in 1x128 groups; both or neither."""
+    if (q is None) != (scales is None):
+        raise ValueError("%s needs its scales, and they it" % what)
+    if q is None:
+        return 0, 0
+    return (_codes(q, m * k, what),
+            _scales(scales, (k + 127) // 128 * m, 4 if sfmt == SCALE_F32 else 1, what + "'s scales"))
+
+
+def fp8_experts_sort(ids, experts, offsets, rows, pairs=None, stream=None):
+    """Rows in expert order of the choices ids [T, S] (int32 or int64): offsets
+    int32 [experts + 1], rows int32 [T, S] (-1: dropped, an id outside
+    [0, experts)), pairs (optional) int32 [T * S], -1 behind the last row."""
+    t, s = ids.shape
+    if ids.dtype not in (_I32, torch.int64):
+        raise ValueError("ids must be int32 or int64")
+    _here(ids, offsets, rows, pairs)
+    _check("fp8_experts_sort",
+           _c_sort(_flat(ids), IDS_I32 if ids.dtype == _I32 else IDS_I64, t, s, experts,
+                   _ints(offsets, experts + 1, "offsets"), _ints(rows, t * s, "rows"),
+                   _ints(pairs, t * s, "pairs"), _on(stream)))
+
+
+def fp8_experts_gather(x, rows, *, q=None, scales=None, fmt=E4M3, sfmt=SCALE_F32, x_scales=None,
+                       out=None, stream=None):
+    """Row rows[t, s] <- x[t]: as 1x128-group codes (q [M, K] with scales
+    [ceil(K/128), M]) and / or as it is (out [M, K] of x's type).  x bf16 or
+    fp32, or codes with x_scales [ceil(K/128), T], which are moved."""
+    t, k = x.shape
+    s = rows.shape[1]
+    _here(x, rows, q, scales, x_scales, out)
+    if q is None and out is None:
+        raise ValueError("q or out takes the rows")
+    m = _grouped_rows(out if q is None else q, k, "q and out")
+    pq, ps = _group_codes(q, scales, m, k, sfmt, "q")
+    if x_scales is not None:
+        if out is not None:
+            raise ValueError("codes are moved into q")
+        px, dt, ldx, po, ldo = 0, 0, 0, 0, 0
+        pc, pcs = _group_codes(x, x_scales, t, k, sfmt, "x")
+    else:
+        (px, ldx), dt, pc, pcs = _rows(x, (t, k), x.dtype, "x"), _in_dt(x), 0, 0
+        po, ldo = _rows(out, (m, k), x.dtype, "out")
+    d = _pack_gather(px, dt, ldx, pc, pcs, _ints(rows, t * s, "rows"), t, s, k, m, fmt, sfmt, pq,
+                     ps, po, ldo)
+    _check("fp8_experts_gather", _c_gather(d, _on(stream)))
+
+
+def _weights(weights, rows):
+    if weights is not None and weights.shape != rows.shape:
+        raise ValueError("weights must have the shape of rows")
+    return _vector(weights, rows.numel(), "weights")
+
+
+def fp8_experts_combine(x, rows, weights, out, *, residual=None, stream=None):
+    """out[t] = residual[t] + sum_s weights[t, s] x[rows[t, s]] (weights None:
+    ones, the gradient of fp8_experts_gather).  x [M, K], out and residual
+    [T, K]: bf16 or fp32."""
+    t, s = rows.shape
+    m, k = x.shape
+    _here(x, rows, weights, out, residual)
+    px, ldx = _rows(x, (m, k), x.dtype, "x")
+    pr, ldr = _rows(residual, (t, k), out.dtype, "residual")
+    po, ldo = _rows(out, (t, k), out.dtype, "out")
+    d = _pack_combine(px, _in_dt(x), ldx, _ints(rows, t * s, "rows"), _weights(weights, rows), t,
+                      s, k, m, pr, ldr, po, _in_dt(out), ldo)
+    _check("fp8_experts_combine", _c_combine(d, _on(stream)))
+
+
+def fp8_experts_combine_backward(dy, rows, weights, *, x=None, d_weights=None, q=None, scales=None,
+                                 fmt=E4M3, sfmt=SCALE_F32, dx=None, stream=None):
+    """The gradient of fp8_experts_combine: row rows[t, s] of q (1x128-group
+    codes with scales) and / or dx (bf16 or fp32) <- weights[t, s] dy[t];
+    d_weights fp32 [T, S] <- <dy[t], x[rows[t, s]]> (x: what combine read)."""
+    t, s = rows.shape
+    k = dy.shape[1]
+    _here(dy, rows, weights, x, d_weights, q, scales, dx)
+    grouped = q if q is not None else dx if dx is not None else x
+    if grouped is None or (d_weights is not None and x is None):
+        raise ValueError("q, dx or d_weights (with x) takes the gradient")
+    m = _grouped_rows(grouped, k, "q, dx and x")
+    pdy, ldy = _rows(dy, (t, k), dy.dtype, "dy")
+    px, xdt, ldx = 0, IN_BF16, 0
+    if x is not None:
+        (px, ldx), xdt = _rows(x, (m, k), x.dtype, "x"), _in_dt(x)
+    pdx, dxdt, lddx = 0, IN_BF16, 0
+    if dx is not None:
+        (pdx, lddx), dxdt = _rows(dx, (m, k), dx.dtype, "dx"), _in_dt(dx)
+    pq, ps = _group_codes(q, scales, m, k, sfmt, "q")
+    d = _pack_combine_grad(pdy, _in_dt(dy), ldy, px, xdt, ldx, _ints(rows, t * s, "rows"),
+                           _weights(weights, rows), t, s, k, m,
+                           _vector(d_weights, t * s, "d_weights"), pq, ps, fmt, sfmt, pdx, dxdt,
+                           lddx)
+    _check("fp8_experts_combine_backward", _c_combine_grad(d, _on(stream)))
+
+
+def fp8_act_checkpoint(h, u, act, q, *, fmt=E4M3, scale=None, amax_out=None, scales=None,
+                       sfmt=SCALE_F32, h_q=None, h_scales=None, u_q=None, u_scales=None,
+                       keep_sfmt=SCALE_F32, out=None, valid_rows=None, stream=None):
+    """q <- codes of a = act(h) u (u None: act(h)), per tensor under `scale`
+    (amax_out: max |a|) or per 1x128 group (scales, sfmt); h_q, u_q (both or
+    neither) <- the checkpoints of h and u: E4M3 codes with 1x128-group scales
+    of keep_sfmt; out: a in bf16.  valid_rows: device int32, rows from it on
+    are left alone."""
+    shape = h.shape
+    m, n = shape
+    _here(h, u, q, scale, amax_out, scales, h_q, h_scales, u_q, u_scales, out, valid_rows)
+    if (scale is None) == (scales is None):
+        raise ValueError("one of scale and scales selects the quantization")
+    ph, ldh = _rows(h, shape, _BF16, "h")
+    pu, ldu = _rows(u, shape, _BF16, "u")
+    po, ldo = _rows(out, shape, _BF16, "out")
+    if scale is not None:
+        mode, pq, ps = NORM_TENSOR, _codes(q, m * n, "q"), 0
+    else:
+        mode = NORM_GROUP
+        pq, ps = _group_codes(q, scales, m, n, sfmt, "q")
+    phq, phs = _group_codes(h_q, h_scales, m, n, keep_sfmt, "h_q")
+    puq, pus = _group_codes(u_q, u_scales, m, n, keep_sfmt, "u_q")
+    d = _pack_act(act, ph, ldh, pu, ldu, m, n, _ints(valid_rows, 1, "valid_rows"), mode, fmt, sfmt,
+                  pq, _vector(scale, 1, "scale"), ps, _vector(amax_out, 1, "amax_out"), keep_sfmt,
+                  phq, phs, puq, pus, po, ldo)
+    _check("fp8_act_checkpoint", _c_act(d, _on(stream)))
+
+
+def _code_rows(t, shape, what):
+    """(device pointer, row pitch in bytes) of one-byte codes with contiguous
+    rows (None -> NULL)."""
+    if t is None:
+        return 0, 0
+    if t.element_size() != 1:
+        raise ValueError("%s must hold one-byte codes" % what)
+    return _rows(t, shape, t.dtype, what)
+
+
+def fp8_act_checkpoint_backward(da, act, h_q, h_scales, u_q=None, u_scales=None, *,
+                                keep_sfmt=SCALE_F32, dh_q=None, du_q=None, fmt=E5M2,
+                                scale_dh=None, scale_du=None, amax_dh=None, amax_du=None,
+                                dh_scales=None, du_scales=None, sfmt=SCALE_F32, dh=None, du=None,
+                                valid_rows=None, stream=None):
+    """dh = da u act'(h), du = da act(h) at the values of fp8_act_checkpoint's
+    checkpoints (u_q None: no gate): codes dh_q, du_q of one row pitch, per
+    tensor (scale_dh, scale_du, amaxes) or per 1x128 group (dh_scales,
+    du_scales, sfmt), and / or dh, du in bf16 (of one row pitch)."""
+    shape = da.shape
+    m, n = shape
+    _here(da, h_q, h_scales, u_q, u_scales, dh_q, du_q, scale_dh, scale_du, amax_dh, amax_du,
+          dh_scales, du_scales, dh, du, valid_rows)
+    group = dh_scales is not None or du_scales is not None
+    if group and (scale_dh is not None or scale_du is not None):
+        raise ValueError("scales per tensor or per group, not both")
+    pda, ldda = _rows(da, shape, _BF16, "da")
+    phq, phs = _group_codes(h_q, h_scales, m, n, keep_sfmt, "h_q")
+    puq, pus = _group_codes(u_q, u_scales, m, n, keep_sfmt, "u_q")
+    pqh, ldqh = _code_rows(dh_q, shape, "dh_q")
+    pqu, ldqu = _code_rows(du_q, shape, "du_q")
+    pdh, ldh = _rows(dh, shape, _BF16, "dh")
+    pdu, ldu = _rows(du, shape, _BF16, "du")
+    if (pqh and pqu and ldqh != ldqu) or (pdh and pdu and ldh != ldu):
+        raise ValueError("dh and du must have one row pitch")
+    psh = psu = 0
+    if group:
+        count, size = (n + 127) // 128 * m, 4 if sfmt == SCALE_F32 else 1
+        if (dh_q is None) != (dh_scales is None) or (du_q is None) != (du_scales is None):
+            raise ValueError("codes need their scales, and they them")
+        if dh_q is not None:
+            psh = _scales(dh_scales, count, size, "dh_scales")
+        if du_q is not None:
+            psu = _scales(du_scales, count, size, "du_scales")
+    d = _pack_act_ckpt_grad(act, pda, ldda, phq, phs, puq, pus, keep_sfmt, m, n,
+                            _ints(valid_rows, 1, "valid_rows"), NORM_GROUP if group else NORM_TENSOR,
+                            fmt, sfmt, pqh, pqu, ldqh or ldqu, _vector(scale_dh, 1, "scale_dh"),
+                            _vector(scale_du, 1, "scale_du"), psh, psu,
+                            _vector(amax_dh, 1, "amax_dh"), _vector(amax_du, 1, "amax_du"), pdh,
+                            pdu, ldh or ldu)
+    _check("fp8_act_checkpoint_backward", _c_act_grad(d, _on(stream)))
 
 
 def fp8_get_last_device_error(stream=None):

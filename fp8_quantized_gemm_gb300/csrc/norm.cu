@@ -29,6 +29,7 @@
 // second pass bounds it, not the bytes in flight).
 #include "common.cuh"
 #include "kernels.h"
+#include "launch.h"
 #include "norm.h"
 #include "pairs.cuh"
 #include "quant_common.cuh"
@@ -422,23 +423,6 @@ __global__ void clear_word_kernel(uint32_t *p) {
   launch_dependents();
   grid_dependency_wait();
   if (threadIdx.x == 0) *p = 0u;
-}
-
-// A launch with programmatic stream serialization (the kernels wait for the
-// previous one before they touch memory).
-template <typename... KArgs, typename... Args>
-static cudaError_t launch_serial(void (*kern)(KArgs...), int64_t blocks, int threads,
-                                 cudaStream_t st, Args... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)blocks);
-  cfg.blockDim = dim3((unsigned)threads);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
 static int round32(int64_t n) { return (int)((n + 31) / 32 * 32); }

@@ -54,6 +54,13 @@ the second step on the forward quantizes only x, and no call reads a bf16
 copy of the weights: the update writes none (`w_bf` then returns the bf16
 rounding of the fp32 masters, the values such a copy would hold).
 
+``checkpoint="fp8"`` keeps h and u for the backward pass in 8 bits (E4M3 codes
+with a scale per 1x128 group, 2.06 bytes an element for two bf16's 4): h and u
+are two plain products into buffers that live for the forward pass only, one
+call writes the codes of a and both checkpoints, and the SwiGLU backward reads
+the checkpoints.  The gradients are those at the values the checkpoints stand
+for.
+
 Buffers are allocated once (device memory through torch); `step` issues the
 calls on the current stream.
 """
@@ -74,7 +81,13 @@ class SwiGLUTrainer:
                  lr=1e-4, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.01,
                  history: int = HISTORY, weight_scaling: str = "delayed",
                  rescale_interval: int = 500, fuse_forward: bool = True,
-                 fuse_optimizer: bool = False, overlap_optimizer: bool = False):
+                 fuse_optimizer: bool = False, overlap_optimizer: bool = False,
+                 checkpoint: str = "bf16"):
+        if checkpoint not in ("bf16", "fp8"):
+            raise ValueError(checkpoint)
+        self.checkpoint = checkpoint
+        if checkpoint == "fp8":
+            fuse_forward = False  # (its epilogue keeps h and u in bf16)
         if weight_scaling not in ("delayed", "auto"):
             raise ValueError(weight_scaling)
         self.weight_scaling = weight_scaling
@@ -118,7 +131,13 @@ class SwiGLUTrainer:
         self.dyq = torch.empty((T, d), **u8)
         self.dhq, self.duq = torch.empty((T, ffn), **u8), torch.empty((T, ffn), **u8)
         # activations and gradients (a, dh and du exist only as codes)
-        self.h, self.u = (torch.empty((T, ffn), **bf) for _ in range(2))
+        self.h, self.u = ((torch.empty((T, ffn), **bf) for _ in range(2))
+                          if checkpoint == "bf16" else (None, None))
+        self.kept = {}  # the 8-bit checkpoints of h and u
+        if checkpoint == "fp8":
+            for name in ("h", "u"):
+                self.kept[name + "_q"] = torch.empty((T, ffn), **u8)
+                self.kept[name + "_scales"] = torch.empty(((ffn + 127) // 128, T), **f32)
         self.y = torch.empty((T, d), **bf)
         self.da = torch.empty((T, ffn), **bf)
         self.dx = torch.empty((T, d), **f32)
@@ -198,6 +217,14 @@ class SwiGLUTrainer:
         if self.fuse_forward:
             run([P(self.xq, E4, self.w1q, E4, sc(X1), sc(K1), self.h,       # h, u = x W1^T, x W3^T
                    swiglu=self.swiglu_ep)])                                 # a = silu(h) u
+        elif self.checkpoint == "fp8":
+            h, u = (torch.empty((self.T, self.ffn), dtype=torch.bfloat16, device=self.xq.device)
+                    for _ in range(2))
+            run([P(self.xq, E4, self.w1q, E4, sc(X1), sc(K1), h),           # h = x W1^T
+                 P(self.xq, E4, self.w3q, E4, sc(X1), sc(K3), u)])          # u = x W3^T
+            F.fp8_act_checkpoint(h, u, F.ACT_SILU, self.aq, scale=sc(A2),   # a = silu(h) u
+                                 amax_out=self._am(A2), **self.kept)
+            del h, u
         else:
             run([P(self.xq, E4, self.w1q, E4, sc(X1), sc(K1), self.h),      # h = x W1^T
                  P(self.xq, E4, self.w3q, E4, sc(X1), sc(K3), self.u)])     # u = x W3^T
@@ -214,8 +241,14 @@ class SwiGLUTrainer:
                a_layout=MN, b_layout=MN, adamw=ep[2])])
         if self.overlap:
             self._side_adamw([self.adamw_items[2]])                         # W2, beside the rest
-        F.fp8_swiglu_backward_quantize(self.da, self.h, self.u, E5, sc(G1), sc(G3),  # dh, du
-                                       self.dhq, self.duq, self._am(G1), self._am(G3))
+        if self.checkpoint == "fp8":                                        # dh, du
+            F.fp8_act_checkpoint_backward(self.da, F.ACT_SILU, **self.kept, dh_q=self.dhq,
+                                          du_q=self.duq, fmt=E5, scale_dh=sc(G1),
+                                          scale_du=sc(G3), amax_dh=self._am(G1),
+                                          amax_du=self._am(G3))
+        else:
+            F.fp8_swiglu_backward_quantize(self.da, self.h, self.u, E5, sc(G1), sc(G3),
+                                           self.dhq, self.duq, self._am(G1), self._am(G3))
         run([P(self.dhq, E5, self.w1q, E4, sc(G1), sc(K1), self.dx, b_layout=MN),   # dx = dh W1
              P(self.dhq, E5, self.xq, E4, sc(G1), sc(X1), self.dw[0],               # dW1 = dh^T x
                a_layout=MN, b_layout=MN, adamw=ep[0]),

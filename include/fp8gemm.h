@@ -481,10 +481,12 @@ FP8_API int fp8_gemm_mx_rows(const uint8_t *a, const uint32_t *la, const float *
  *   b        [E, N, K] E4M3 codes, expert-major: expert e's [N, K] block
  *            quantized as by fp8_quantize_block
  *   sb       [E, ceil(N/128), K/128] scales (fp32 or UE8M0 bytes per sfmt)
- *   offsets  DEVICE int32 [E + 1]: 0 = offsets[0] <= ... <= offsets[E] = M;
- *            segments of any size, empty experts allowed.  Read by the
- *            kernel: the host does not check them (a tile never spans two
- *            experts; rows outside [0, M) are never loaded or stored).
+ *   offsets  DEVICE int32 [E + 1]: 0 = offsets[0] <= ... <= offsets[E] <= M
+ *            (as fp8_experts_sort writes them); segments of any size, empty
+ *            experts allowed.  Read by the kernel: the host does not check
+ *            them (a tile never spans two experts; rows outside [0, M) are
+ *            never loaded or stored, and rows of c at and behind offsets[E]
+ *            are left as they were).
  *   experts  E, 1 <= E <= 256.  c [M, ldc] bf16.  K % 128 == 0.
  * One persistent launch over all experts' tiles (each expert's row range
  * split into 128-row tiles); no split K.
@@ -694,6 +696,217 @@ typedef struct {
 } fp8_rmsnorm_grad_t;
 FP8_API int64_t fp8_rmsnorm_backward_workspace(int64_t M, int64_t K);
 FP8_API int fp8_rmsnorm_backward(const fp8_rmsnorm_grad_t *grad, fp8_stream_t stream);
+
+/* ------------------------------------ tokens to their experts and back --
+ * What stands around the expert-grouped products of a mixture-of-experts layer
+ * ([HF] 6.4: FP8Experts; the pages leave the order of the rows open).  Each of T
+ * tokens has S choices of expert; pair p = t * S + s owns one row of the
+ * products' operands, rows [offsets[e], offsets[e+1]) being expert e's:
+ *
+ *   fp8_experts_sort              offsets, rows (and pairs) from the choices
+ *   fp8_experts_gather            row rows[t,s] <- x[t], as codes
+ *   fp8_gemm_group_experts ...    the products
+ *   fp8_experts_combine           out[t] = residual[t] + sum_s w[t,s] x[rows[t,s]]
+ *   fp8_experts_combine_backward  row rows[t,s] <- w[t,s] dy[t], as codes; dw
+ *
+ * The gradient of gather (its quantization passes the gradient through) is
+ * fp8_experts_combine of the rows' gradients with null weights.
+ *
+ *   rows   DEVICE int32 [T, S], each value at most once.  A value outside
+ *          [0, M) drops its pair: nothing is read or written for it, it adds
+ *          nothing and its dw is 0.  (Read by the kernels, not checked by the
+ *          host; as fp8_experts_sort writes them, or a user's own order.)
+ *   M      rows of the grouped side, e.g. T * S; rows that no pair owns are
+ *          left as they were.
+ * Matrices are bf16 or fp32 (fp8_in_dtype_t) with contiguous 16-byte aligned
+ * rows; pitches in elements, >= K and multiples of 8; K % 16 == 0.  Codes are
+ * [M, K] contiguous, 16-byte aligned; group scales [ceil(K/128), M] of sfmt.
+ * T == 0 or M == 0 is allowed; T * S < 2^31.  No call allocates or keeps
+ * scratch; all are launched with programmatic stream serialization, as the
+ * per-group calls, and give the same bits on every run.
+ *
+ * fp8_experts_sort: rows[t,s] = number of pairs with a smaller expert + number
+ * of earlier pairs of the same expert (a stable order).
+ *   ids     [T, S] int32 or int64 (id_dt), contiguous; an id outside
+ *           [0, experts) drops its pair (rows -1), as for the experts that
+ *           another device holds.  An expert may be chosen twice by a token.
+ *   experts 1 .. 256
+ *   offsets int32 [experts + 1]: offsets[experts] = number of kept pairs
+ *   pairs   nullable int32 [T * S]: the pair of each row; -1 from
+ *           offsets[experts] on
+ */
+typedef enum { FP8_IDS_I32 = 0, FP8_IDS_I64 = 1 } fp8_ids_dtype_t;
+FP8_API int fp8_experts_sort(const void *ids, int id_dt, int64_t T, int64_t S, int experts,
+                             int32_t *offsets, int32_t *rows, int32_t *pairs,
+                             fp8_stream_t stream);
+
+/* fp8_experts_gather: exactly one source: x [T, ld_x] of dt, or xq, codes
+ * [T, K] that exist already (fp8_rmsnorm_quantize with 1x128 groups,
+ * fp8_quantize_token_group) with x_scales [ceil(K/128), T].
+ *   q, scales  the codes of the rows: the bytes that fp8_quantize_token_group
+ *              (fmt, sfmt) gives for the reordered rows of x, or xq's own.
+ *              Nullable together with x when out is given.
+ *   out        nullable (x only): the rows themselves, [M, ld_out] of dt. */
+typedef struct {
+  const void *x;
+  int dt;
+  int64_t ld_x;
+  const uint8_t *xq;
+  const void *x_scales;
+  const int32_t *rows;
+  int64_t T, S, K, M;
+  int fmt, sfmt;
+  uint8_t *q;
+  void *scales;
+  void *out;
+  int64_t ld_out;
+} fp8_experts_gather_t;
+FP8_API int fp8_experts_gather(const fp8_experts_gather_t *gather, fp8_stream_t stream);
+
+/* fp8_experts_combine: sums in fp32 in the order of the choices, the residual
+ * last, rounded once.
+ *   x         [M, ld_x] of x_dt
+ *   weights   nullable fp32 [T, S]: ones
+ *   residual  nullable [T, ld_residual] of out_dt; may be out (same pitch)
+ *   out       [T, ld_out] of out_dt (both fp8_in_dtype_t); a token without a
+ *             kept pair gets its residual, or zeros. */
+typedef struct {
+  const void *x;
+  int x_dt;
+  int64_t ld_x;
+  const int32_t *rows;
+  const float *weights;
+  int64_t T, S, K, M;
+  const void *residual;
+  int64_t ld_residual;
+  void *out;
+  int out_dt;
+  int64_t ld_out;
+} fp8_experts_combine_t;
+FP8_API int fp8_experts_combine(const fp8_experts_combine_t *combine, fp8_stream_t stream);
+
+/* fp8_experts_combine_backward: with v = w[t,s] dy[t] in fp32 (weights null:
+ * dy[t]), for row r = rows[t,s]:
+ *   q, scales   nullable together: codes of v (fmt; E4M3 is what
+ *               fp8_gemm_group_experts reads) in 1x128 groups, with v times
+ *               the rounded reciprocal of a scale in the place of the exact
+ *               quotient
+ *   dx          nullable [M, ld_dx] of dx_dt: v, rounded once
+ *   d_weights   nullable fp32 [T, S] (x given): sum_k dy[t,k] x[r,k], in a
+ *               fixed order
+ *   dy [T, ld_dy] of dy_dt; x [M, ld_x] of x_dt, what combine read.  weights
+ *   are finite. */
+typedef struct {
+  const void *dy;
+  int dy_dt;
+  int64_t ld_dy;
+  const void *x;
+  int x_dt;
+  int64_t ld_x;
+  const int32_t *rows;
+  const float *weights;
+  int64_t T, S, K, M;
+  float *d_weights;
+  uint8_t *q;
+  void *scales;
+  int fmt, sfmt;
+  void *dx;
+  int dx_dt;
+  int64_t ld_dx;
+} fp8_experts_combine_grad_t;
+FP8_API int fp8_experts_combine_backward(const fp8_experts_combine_grad_t *grad,
+                                         fp8_stream_t stream);
+
+/* ---------------------------------- activation checkpoints in 8 bits --
+ * The activation between two FP8 products, a = act(h) u (u null: a = act(h)),
+ * as codes, with its arguments kept for the backward pass in 8 bits (support
+ * arithmetic around the pages' GEMMs):
+ *
+ *   fp8_act_checkpoint            q <- codes of a; h_q, u_q <- h, u as E4M3 codes
+ *                                 in 1x128 groups (fp8_quantize_token_group's
+ *                                 bytes), 2.06 bytes an element for two bf16
+ *   fp8_act_checkpoint_backward   dh = da u act'(h), du = da act(h) at the values
+ *                                 h and u that the checkpoints stand for
+ *
+ * act: fp8_act_t with its limits at infinite arguments (NONE: act(h) = h).
+ * Results are formed in fp32 and rounded once per stored copy.
+ *   mode   FP8_NORM_TENSOR: codes under scales fixed before the call (delayed
+ *          scaling), the maxima (nullable, cleared by the call, not a scale
+ *          itself) taken of the fp32 results; FP8_NORM_GROUP: 1x128 groups of
+ *          sfmt with scales [ceil(N/128), M].  Values times the rounded
+ *          reciprocal of a scale stand in the place of the exact quotient.
+ *   valid_rows  nullable DEVICE int32: rows at and behind valid_rows[0] are
+ *          neither read nor written and are in no maximum (offsets + experts of
+ *          fp8_experts_sort: the rows that hold no token).
+ * Matrices are bf16 with contiguous 16-byte aligned rows, pitches in elements,
+ * >= N and multiples of 8 (h and u may be halves of one [M, 2N] product); codes
+ * and checkpoints 16-byte aligned; N % 16 == 0.  M == 0 writes only the maxima
+ * (0).  A NaN argument is kept as one, and the rest of its group under a scale
+ * of 1; a group that holds an infinity is kept as NaN (UE8M0 scales: the
+ * infinity is kept, the rest of its group as zeros).
+ * Launched with programmatic stream serialization, as the per-group calls.
+ *
+ * fp8_act_checkpoint:
+ *   q       codes [M, N] of fmt (required);  scale / scales, amax_out  by mode
+ *   h_q, h_scales, u_q, u_scales  the checkpoints, [M, N] and
+ *           [ceil(N/128), M] of keep_sfmt; all null: none is kept (u_q and
+ *           u_scales null without u)
+ *   out     nullable bf16 [M, ld_out]: a
+ */
+typedef struct {
+  int act;
+  const void *h;
+  int64_t ld_h;
+  const void *u;
+  int64_t ld_u;
+  int64_t M, N;
+  const int32_t *valid_rows;
+  int mode, fmt, sfmt;
+  uint8_t *q;
+  const float *scale;
+  void *scales;
+  float *amax_out;
+  int keep_sfmt;
+  uint8_t *h_q;
+  void *h_scales;
+  uint8_t *u_q;
+  void *u_scales;
+  void *out;
+  int64_t ld_out;
+} fp8_act_checkpoint_t;
+FP8_API int fp8_act_checkpoint(const fp8_act_checkpoint_t *act, fp8_stream_t stream);
+
+/* fp8_act_checkpoint_backward:
+ *   da      bf16 [M, ld_da]
+ *   h_q, h_scales, u_q, u_scales (u's null together: no gate), keep_sfmt  as
+ *           the forward call left them
+ *   dh_q, du_q  nullable codes [M, ld_q] (bytes; a multiple of 16) of fmt, du_q
+ *           only with a gate: side by side in one [M, 2N] operand with ld_q = 2N.
+ *           scale_dh, scale_du, amax_dh, amax_du (nullable, distinct) per tensor;
+ *           dh_scales, du_scales per group
+ *   dh, du  nullable bf16 [M, ld_d]; may not overlap da. */
+typedef struct {
+  int act;
+  const void *da;
+  int64_t ld_da;
+  const uint8_t *h_q;
+  const void *h_scales;
+  const uint8_t *u_q;
+  const void *u_scales;
+  int keep_sfmt;
+  int64_t M, N;
+  const int32_t *valid_rows;
+  int mode, fmt, sfmt;
+  uint8_t *dh_q, *du_q;
+  int64_t ld_q;
+  const float *scale_dh, *scale_du;
+  void *dh_scales, *du_scales;
+  float *amax_dh, *amax_du;
+  void *dh, *du;
+  int64_t ld_d;
+} fp8_act_checkpoint_grad_t;
+FP8_API int fp8_act_checkpoint_backward(const fp8_act_checkpoint_grad_t *grad,
+                                        fp8_stream_t stream);
 
 /* -------------------------------------------------- delayed-state update --
  * fp8_delayed_state_update: one amax-history step of delayed scaling
