@@ -24,75 +24,67 @@
 
 namespace fp8k {
 
-// act(z) and act'(z) from one exponential (the forms and limits of
-// act_value2 / act_slope2).
+// act(z) and act'(z) from one exponential, the forms of act_value2 /
+// act_slope2 without their bounds: |z| is at most 2^49 here.
 template <int A>
 __device__ __forceinline__ void act_both2(F2 z, F2 &value, F2 &slope) {
   if constexpr (A == kActSilu) {
-    const F2 b = within_2(z, kFar), s = logistic2(b * F2(kNegLog2e));
-    value = left_capped(z) * s;
-    slope = s * fma2(b, fma2(s, F2(-1.0f), F2(1.0f)), F2(1.0f));
+    const F2 s = logistic2(z * F2(kNegLog2e));
+    value = z * s;
+    slope = fma2(value, fma2(s, F2(-1.0f), F2(1.0f)), s);
   } else if constexpr (A == kActGeluTanh) {
-    const F2 b = within_2(z, kFarCubed), bb = b * b;
-    const F2 s = logistic2(b * fma2(bb, F2(kT3), F2(kT1)));
-    value = left_capped(z) * s;
-    slope = fma2(b * s, fma2(s, F2(-1.0f), F2(1.0f)) * fma2(bb, F2(kD3), F2(kD1)), s);
+    const F2 zz = z * z, s = logistic2(z * fma2(zz, F2(kT3), F2(kT1)));
+    value = z * s;
+    slope = fma2(value, fma2(s, F2(-1.0f), F2(1.0f)) * fma2(zz, F2(kD3), F2(kD1)), s);
   } else {  // (the normal tail of gelu is common to both: the compiler keeps one)
     value = act_value2<A>(z);
     slope = act_slope2<A>(z);
   }
 }
-
-// Codes of 16 fp32 results.  Per tensor: under d, the maximum into `top`; per
-// group: under a scale of their own, stored by the group's first lane.
-template <int F>
-__device__ __forceinline__ uint4 code16(F2 (&y)[8], const CodeScale &d, float &top) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    top = max_abs2(top, y[i]);
-    y[i] = d.quotient(y[i]);
-  }
-  return pack16<F>(y);
+// The bounded forms, for values of any size; out of line.
+template <int A>
+__device__ __noinline__ uint64_t act_value_any(uint64_t z) {
+  return act_value2<A>(F2(z)).v;
 }
-template <int F>
-__device__ __forceinline__ uint4 code16_group(F2 (&y)[8], int sfmt, void *scales, int64_t at,
-                                              bool owner) {
-  float m = 0.0f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) m = max_abs2(m, y[i]);
-  const float amax = __uint_as_float(group8_max(__float_as_uint(m)));
-  if (sfmt == 0) {
-    const float s = scale_from_amax(amax, fmt_max(F));
-    if (owner) static_cast<float *>(scales)[at] = s;
-    const CodeScale d(s);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = d.quotient(y[i]);
-  } else {
-    const int e = ue8m0_exponent(amax, fmt_max(F));
-    if (owner) static_cast<uint8_t *>(scales)[at] = (uint8_t)(e + 127);
-    const F2 inv(exp2_int(-e));
-#pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = y[i] * inv;
-  }
-  return pack16<F>(y);
+template <int A>
+__device__ __noinline__ uint64_t act_slope_any(uint64_t z) {
+  return act_slope2<A>(F2(z)).v;
 }
 
-// The checkpoint of 16 bf16 values.
-__device__ __forceinline__ void keep16(const Vec16<__nv_bfloat16> &v, uint8_t *q, void *scales,
-                                       int64_t at, int sfmt, bool in, bool owner) {
-  const float amax = __uint_as_float(group8_max(v.max_key()));
-  uint4 c;
-  if (sfmt == 0) {
-    const float s = scale_from_amax(amax, kE4M3Max);
-    if (owner) static_cast<float *>(scales)[at] = s;
-    c = v.codes<0>(ScaleDiv(s));
+// Eight pairs of the activation's values from raw bf16 arguments.  silu and the
+// tanh form need their argument bounded on the left (-inf times a factor that has
+// vanished): two at a time on the bf16 pair.
+template <int A>
+__device__ __forceinline__ F2 act_of_word(uint32_t w) {
+  if constexpr (A == kActSilu || A == kActGeluTanh) {
+    uint32_t c;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(c) : "r"(w), "r"(0xC61CC61Cu));  // -9984
+    const F2 z = bf16_pair(c);
+    if constexpr (A == kActSilu) return z * logistic2(z * F2(kNegLog2e));
+    return z * logistic2(z * fma2(z * z, F2(kT3), F2(kT1)));
   } else {
-    const int e = ue8m0_exponent(amax, kE4M3Max);
-    if (owner) static_cast<uint8_t *>(scales)[at] = (uint8_t)(e + 127);
-    c = v.codes_pow2<0>(exp2_int(-e));
+    return act_value2<A>(bf16_pair(w));
   }
-  if (in) *reinterpret_cast<uint4 *>(q) = c;
 }
+
+// 16 bf16 values as two vectors of eight
+struct Words16 {
+  uint4 a, b;
+  __device__ __forceinline__ uint32_t word(int i) const {
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    return w[i];
+  }
+  __device__ __forceinline__ F2 pair(int i) const { return bf16_pair(word(i)); }
+  // max |x| (one instruction a pair; the sign that it leaves is dropped)
+  __device__ __forceinline__ float max_abs() const {
+    uint32_t m = 0u;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      asm("max.NaN.xorsign.abs.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(word(i)));
+    m &= 0x7FFF7FFFu;
+    return __uint_as_float(max(m << 16, m & 0xFFFF0000u));
+  }
+};
 
 // Two E4M3 codes -> two fp32 values (exact: through half precision, which
 // holds every E4M3 value).
@@ -116,122 +108,228 @@ __device__ __forceinline__ F2 kept_pair(const uint4 &c, int i, F2 s) {
 }
 
 // Rows that are dealt with.
-__device__ __forceinline__ int64_t live_rows(const int32_t *valid, int64_t M) {
-  return valid == nullptr ? M : max((int64_t)0, min((int64_t)*valid, M));
+__device__ __forceinline__ uint32_t live_rows(const int32_t *valid, int64_t M) {
+  return valid == nullptr ? (uint32_t)M : (uint32_t)max((int64_t)0, min((int64_t)*valid, M));
 }
 
-// This thread's place in a tile.
-struct TilePlace {
-  int64_t row, col, g;
-  bool in;     // its elements lie inside the matrix
-  bool owner;  // it stores its group's scale
+// A CTA's walk over the tiles blockIdx.x, blockIdx.x + gridDim.x, ... of 32 rows
+// by 128 columns, column first; this thread's row and first column.  (Rows,
+// columns and pitches are below 2^31: one wide multiplication an address.)
+struct TileWalk {
+  int64_t left;  // tiles from here to the end, this one included
+  uint32_t row, g, groups, step_rows, step_g;
+  __device__ __forceinline__ TileWalk(uint32_t rows, uint32_t N) {
+    groups = (N + 127) / 128;
+    const uint32_t rt = blockIdx.x / groups;
+    left = (int64_t)((rows + 31) / 32) * groups - blockIdx.x;
+    g = blockIdx.x - rt * groups;
+    row = rt * 32 + (threadIdx.x >> 3);
+    step_rows = gridDim.x / groups * 32;
+    step_g = gridDim.x % groups;
+  }
+  __device__ __forceinline__ void next() {
+    left -= gridDim.x;
+    row += step_rows;
+    g += step_g;
+    if (g >= groups) {
+      g -= groups;
+      row += 32;
+    }
+  }
+  __device__ __forceinline__ uint32_t col() const { return g * 128 + (threadIdx.x & 7u) * 16; }
+  __device__ __forceinline__ int64_t at(int64_t pitch) const {
+    return (int64_t)((uint64_t)row * (uint32_t)pitch + col());
+  }
+  __device__ __forceinline__ int64_t scale_at(int64_t M) const {
+    return (int64_t)((uint64_t)g * (uint32_t)M + row);
+  }
 };
-__device__ __forceinline__ TilePlace tile_place(int64_t tile, int64_t groups, bool narrow,
-                                                int64_t rows, int64_t N) {
-  TilePlace p;
-  int64_t rt;
-  split_task(tile, groups, narrow, rt, p.g);
-  p.row = rt * 32 + (threadIdx.x >> 3);
-  p.col = p.g * 128 + (threadIdx.x & 7u) * 16;
-  p.in = p.row < rows && p.col < N;
-  p.owner = p.row < rows && (threadIdx.x & 7u) == 0u;
-  return p;
+
+// Threads of a CTA, and CTAs that share an SM (64 registers a thread).
+constexpr int kTileThreads = 256, kForwardCtas = 4, kGradCtas = 4;
+
+// 16 values from p, or zeros
+__device__ __forceinline__ Words16 load16(const __nv_bfloat16 *p, bool in) {
+  Words16 v{make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
+  if (in) {
+    v.a = __ldcs(reinterpret_cast<const uint4 *>(p));
+    v.b = __ldcs(reinterpret_cast<const uint4 *>(p) + 1);
+  }
+  return v;
+}
+
+// Codes of 16 results under the scale of their group (group: 8 lanes), stored
+// with it.
+template <int F>
+__device__ __forceinline__ void put_group(const F2 (&y)[8], float amax, int sfmt, uint8_t *q,
+                                          void *scales, int64_t at, bool in, bool owner) {
+  const float top = __uint_as_float(group8_max(__float_as_uint(amax)));
+  GroupScale g = group_scale<F>(top, sfmt);
+  uint4 c;
+  if (__all_sync(0xffffffffu, g.fast)) {
+    c = codes16_times<F>(y, g.inv);
+  } else {
+    g = group_scale_any<F>(top, sfmt);
+    c = codes16_any<F>(y, g.s);
+  }
+  if (owner) store_scale(scales, at, g.stored, sfmt);
+  if (in) *reinterpret_cast<uint4 *>(q) = c;
+}
+// Under the tensor's scale d, the maximum into `top`.
+template <int F>
+__device__ __forceinline__ void put_tensor(const F2 (&y)[8], const CodeScale &d, float &top,
+                                           uint8_t *q, bool in) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) top = max_abs2(top, y[i]);
+  const uint4 c = d.fast ? codes16_times<F>(y, d.inv) : codes16_any<F>(y, d.s);
+  if (in) *reinterpret_cast<uint4 *>(q) = c;
+}
+__device__ __forceinline__ float max_abs16(const F2 (&y)[8]) {
+  float m = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max_abs2(m, y[i]);
+  return m;
+}
+
+// Two results of the same group at once: the first step of the reduction leaves
+// the maximum of y to even lanes and that of z to odd ones, so that each lane
+// forms one scale instead of two.
+template <int F>
+__device__ __forceinline__ void put_groups(const F2 (&y)[8], const F2 (&z)[8], int sfmt,
+                                           uint8_t *qy, uint8_t *qz, void *sy, void *sz, int64_t at,
+                                           bool in, bool live) {
+  const bool odd = threadIdx.x & 1u;
+  const uint32_t ky = __float_as_uint(max_abs16(y)), kz = __float_as_uint(max_abs16(z));
+  uint32_t key = odd ? kz : ky;
+  key = max(key, __shfl_xor_sync(0xffffffffu, odd ? ky : kz, 1));
+  key = max(key, __shfl_xor_sync(0xffffffffu, key, 2));
+  key = max(key, __shfl_xor_sync(0xffffffffu, key, 4));
+  const float top = __uint_as_float(key);
+  GroupScale g = group_scale<F>(top, sfmt);
+  const bool fast = __all_sync(0xffffffffu, g.fast);
+  if (!fast) g = group_scale_any<F>(top, sfmt);
+  const float mine = fast ? g.inv : g.s, other = __shfl_xor_sync(0xffffffffu, mine, 1);
+  const float fy = odd ? other : mine, fz = odd ? mine : other;
+  if (live && (threadIdx.x & 7u) < 2u) store_scale(odd ? sz : sy, at, g.stored, sfmt);
+  const uint4 cy = fast ? codes16_times<F>(y, fy) : codes16_any<F>(y, fy);
+  if (in) *reinterpret_cast<uint4 *>(qy) = cy;
+  const uint4 cz = fast ? codes16_times<F>(z, fz) : codes16_any<F>(z, fz);
+  if (in) *reinterpret_cast<uint4 *>(qz) = cz;
+}
+
+// The checkpoint of 16 bf16 values.
+__device__ __forceinline__ void keep16(const Words16 &v, uint8_t *q, void *scales, int64_t at,
+                                       int sfmt, bool in, bool owner) {
+  F2 x[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = v.pair(i);
+  put_group<0>(x, v.max_abs(), sfmt, q, scales, at, in, owner);
 }
 
 template <int A, bool GATE, int F>
-__global__ void __launch_bounds__(256) act_checkpoint_kernel(const ActArgs a) {
+__global__ void __launch_bounds__(kTileThreads, kForwardCtas)
+    act_checkpoint_kernel(const ActArgs a) {
   launch_dependents();
   grid_dependency_wait();
   const __nv_bfloat16 *h = static_cast<const __nv_bfloat16 *>(a.h);
   const __nv_bfloat16 *u = static_cast<const __nv_bfloat16 *>(a.u);
-  const int64_t rows = live_rows(a.valid, a.M);
-  const int64_t groups = (a.N + 127) / 128, tiles = (rows + 31) / 32 * groups;
-  const bool narrow = tiles + gridDim.x <= (int64_t)0xFFFFFFFFu;
+  const uint32_t rows = live_rows(a.valid, a.M), N = (uint32_t)a.N;
   const CodeScale d(a.scale != nullptr ? *a.scale : 1.0f);
   float top = 0.0f;
-  for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-    const TilePlace p = tile_place(tile, groups, narrow, rows, a.N);
-    Vec16<__nv_bfloat16> hv, uv;
-    hv.zero();
-    uv.zero();
-    if (p.in) {
-      hv.load(h + p.row * a.ldh + p.col);
-      if (GATE) uv.load(u + p.row * a.ldu + p.col);
-    }
-    const int64_t at = p.g * a.M + p.row, flat = p.row * a.N + p.col;
-    if (a.hq != nullptr) keep16(hv, a.hq + flat, a.hs, at, a.keep_sfmt, p.in, p.owner);
-    if (GATE && a.uq != nullptr) keep16(uv, a.uq + flat, a.us, at, a.keep_sfmt, p.in, p.owner);
+  for (TileWalk t(rows, N); t.left > 0; t.next()) {
+    const int64_t at = t.scale_at(a.M), flat = t.at(a.N);
+    const bool in = t.row < rows && t.col() < N, owner = t.row < rows && (threadIdx.x & 7u) == 0u;
+    const Words16 hv = load16(h + t.at(a.ldh), in);
+    Words16 uv;
+    if constexpr (GATE) uv = load16(u + t.at(a.ldu), in);
+    // (the checkpoints first: the results' registers are not needed for them)
+    if (a.hq != nullptr) keep16(hv, a.hq + flat, a.hs, at, a.keep_sfmt, in, owner);
+    if (GATE && a.uq != nullptr) keep16(uv, a.uq + flat, a.us, at, a.keep_sfmt, in, owner);
     F2 y[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      y[i] = act_value2<A>(hv.pair(i));
-      if (GATE) y[i] = y[i] * uv.pair(i);
+      y[i] = act_of_word<A>(hv.word(i));
+      if constexpr (GATE) y[i] = y[i] * uv.pair(i);
     }
-    if (a.out != nullptr && p.in)
-      store16(static_cast<__nv_bfloat16 *>(a.out) + p.row * a.ld_out + p.col, y);
-    const uint4 c = a.scale != nullptr
-                        ? code16<F>(y, d, top)
-                        : code16_group<F>(y, a.sfmt, a.scales, at, p.owner);
-    if (p.in) *reinterpret_cast<uint4 *>(a.q + flat) = c;
+    if (a.out != nullptr && in)
+      store16(static_cast<__nv_bfloat16 *>(a.out) + t.at(a.ld_out), y);
+    if (a.scale != nullptr)
+      put_tensor<F>(y, d, top, a.q + flat, in);
+    else
+      put_group<F>(y, max_abs16(y), a.sfmt, a.q + flat, a.scales, at, in, owner);
   }
   if (a.amax != nullptr) block_max_to(__float_as_uint(top), a.amax);
 }
 
+// The fast forms hold for checkpoints of values up to this.
+constexpr float kKeptScaleMax = 0x1p40f;
+
 template <int A, bool GATE, int F>
-__global__ void __launch_bounds__(256) act_checkpoint_grad_kernel(const ActGradArgs a) {
+__global__ void __launch_bounds__(kTileThreads, kGradCtas)
+    act_checkpoint_grad_kernel(const ActGradArgs a) {
   launch_dependents();
   grid_dependency_wait();
   const __nv_bfloat16 *da = static_cast<const __nv_bfloat16 *>(a.da);
-  const int64_t rows = live_rows(a.valid, a.M);
-  const int64_t groups = (a.N + 127) / 128, tiles = (rows + 31) / 32 * groups;
-  const bool narrow = tiles + gridDim.x <= (int64_t)0xFFFFFFFFu;
+  const uint32_t rows = live_rows(a.valid, a.M), N = (uint32_t)a.N;
   const bool tensor = a.tensor != 0;
   const CodeScale dh(a.scale_h != nullptr ? *a.scale_h : 1.0f);
   const CodeScale du(a.scale_u != nullptr ? *a.scale_u : 1.0f);
   float top_h = 0.0f, top_u = 0.0f;
-  for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-    const TilePlace p = tile_place(tile, groups, narrow, rows, a.N);
-    const int64_t at = p.g * a.M + p.row, flat = p.row * a.N + p.col;
-    Vec16<__nv_bfloat16> v;
+  for (TileWalk t(rows, N); t.left > 0; t.next()) {
+    const int64_t at = t.scale_at(a.M), flat = t.at(a.N);
+    const bool in = t.row < rows && t.col() < N;
+    const Words16 v = load16(da + t.at(a.ld_da), in);
     Vec16<uint8_t> hc, uc;
-    v.zero();
     hc.zero();
     uc.zero();
-    F2 hs(0.0f), us(0.0f);
-    if (p.in) {
-      v.load(da + p.row * a.ld_da + p.col);
+    float hs = 0.0f, us = 0.0f;
+    if (in) {
       hc.load(a.hq + flat);
-      hs = F2(kept_scale(a.hs, at, a.keep_sfmt));
-      if (GATE) {
+      hs = kept_scale(a.hs, at, a.keep_sfmt);
+      if constexpr (GATE) {
         uc.load(a.uq + flat);
-        us = F2(kept_scale(a.us, at, a.keep_sfmt));
+        us = kept_scale(a.us, at, a.keep_sfmt);
       }
     }
     F2 yh[8], yu[8];
+    if (__all_sync(0xffffffffu, hs <= kKeptScaleMax)) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      F2 value, slope;
-      const F2 g = v.pair(i);
-      act_both2<A>(kept_pair(hc.w[0], i, hs), value, slope);
-      if (GATE) {
-        yh[i] = g * kept_pair(uc.w[0], i, us) * slope;
-        yu[i] = g * value;
-      } else {
-        yh[i] = g * slope;
+      for (int i = 0; i < 8; ++i) act_both2<A>(kept_pair(hc.w[0], i, F2(hs)), yu[i], yh[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const F2 z = kept_pair(hc.w[0], i, F2(hs));
+        yu[i] = F2(act_value_any<A>(z.v));
+        yh[i] = F2(act_slope_any<A>(z.v));
       }
     }
-    const int64_t qat = p.row * a.ld_q + p.col, dat = p.row * a.ld_d + p.col;
-    if (a.dh != nullptr && p.in) store16(static_cast<__nv_bfloat16 *>(a.dh) + dat, yh);
-    if (GATE && a.du != nullptr && p.in) store16(static_cast<__nv_bfloat16 *>(a.du) + dat, yu);
-    if (a.qh != nullptr) {
-      const uint4 c = tensor ? code16<F>(yh, dh, top_h)
-                             : code16_group<F>(yh, a.sfmt, a.sh, at, p.owner);
-      if (p.in) *reinterpret_cast<uint4 *>(a.qh + qat) = c;
+    if constexpr (GATE) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const F2 g = v.pair(i);
+        yh[i] = g * kept_pair(uc.w[0], i, F2(us)) * yh[i];
+        yu[i] = g * yu[i];
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) yh[i] = v.pair(i) * yh[i];
     }
-    if (GATE && a.qu != nullptr) {
-      const uint4 c = tensor ? code16<F>(yu, du, top_u)
-                             : code16_group<F>(yu, a.sfmt, a.su, at, p.owner);
-      if (p.in) *reinterpret_cast<uint4 *>(a.qu + qat) = c;
+    if (a.dh != nullptr && in) store16(static_cast<__nv_bfloat16 *>(a.dh) + t.at(a.ld_d), yh);
+    if (GATE && a.du != nullptr && in)
+      store16(static_cast<__nv_bfloat16 *>(a.du) + t.at(a.ld_d), yu);
+    const int64_t qat = t.at(a.ld_q);
+    const bool live = t.row < rows;
+    if (tensor) {
+      if (a.qh != nullptr) put_tensor<F>(yh, dh, top_h, a.qh + qat, in);
+      if (GATE && a.qu != nullptr) put_tensor<F>(yu, du, top_u, a.qu + qat, in);
+    } else if (GATE && a.qh != nullptr && a.qu != nullptr) {
+      put_groups<F>(yh, yu, a.sfmt, a.qh + qat, a.qu + qat, a.sh, a.su, at, in, live);
+    } else {
+      const bool owner = live && (threadIdx.x & 7u) == 0u;
+      if (a.qh != nullptr)
+        put_group<F>(yh, max_abs16(yh), a.sfmt, a.qh + qat, a.sh, at, in, owner);
+      if (GATE && a.qu != nullptr)
+        put_group<F>(yu, max_abs16(yu), a.sfmt, a.qu + qat, a.su, at, in, owner);
     }
   }
   if (a.amax_h != nullptr) block_max_to(__float_as_uint(top_h), a.amax_h);
@@ -254,8 +352,8 @@ static cudaError_t clear_maxima(uint32_t *p, uint32_t *q, cudaStream_t st) {
   return launch_serial(clear_maxima_kernel, 1, 32, st, p, q);
 }
 
-static int64_t tile_blocks(int64_t M, int64_t N, int sms) {
-  const int64_t tiles = (M + 31) / 32 * ((N + 127) / 128), most = (int64_t)sms * 8;
+static int64_t tile_blocks(int64_t M, int64_t N, int64_t most) {
+  const int64_t tiles = (M + 31) / 32 * ((N + 127) / 128);
   return tiles < most ? tiles : most;
 }
 
@@ -289,10 +387,11 @@ static void each_act(int act, Fn &&f) {
 cudaError_t launch_act_checkpoint(const ActArgs &a, int sms, cudaStream_t st) {
   cudaError_t e = clear_maxima(a.amax, nullptr, st);
   if (e != cudaSuccess || a.M == 0) return e;
-  const int64_t blocks = tile_blocks(a.M, a.N, sms);
+  const int64_t blocks = tile_blocks(a.M, a.N, (int64_t)sms * kForwardCtas);
   each_act(a.act, [&](auto act) {
     with_gate(a.u != nullptr, a.fmt, [&](auto gate, auto fmt) {
-      e = launch_serial(act_checkpoint_kernel<act.value, gate.value, fmt.value>, blocks, 256, st, a);
+      e = launch_serial(act_checkpoint_kernel<act.value, gate.value, fmt.value>, blocks,
+                        kTileThreads, st, a);
     });
   });
   return e;
@@ -301,11 +400,11 @@ cudaError_t launch_act_checkpoint(const ActArgs &a, int sms, cudaStream_t st) {
 cudaError_t launch_act_checkpoint_grad(const ActGradArgs &a, int sms, cudaStream_t st) {
   cudaError_t e = clear_maxima(a.amax_h, a.amax_u, st);
   if (e != cudaSuccess || a.M == 0) return e;
-  const int64_t blocks = tile_blocks(a.M, a.N, sms);
+  const int64_t blocks = tile_blocks(a.M, a.N, (int64_t)sms * kGradCtas);
   each_act(a.act, [&](auto act) {
     with_gate(a.uq != nullptr, a.fmt, [&](auto gate, auto fmt) {
-      e = launch_serial(act_checkpoint_grad_kernel<act.value, gate.value, fmt.value>, blocks, 256,
-                        st, a);
+      e = launch_serial(act_checkpoint_grad_kernel<act.value, gate.value, fmt.value>, blocks,
+                        kTileThreads, st, a);
     });
   });
   return e;

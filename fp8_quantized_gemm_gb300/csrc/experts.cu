@@ -24,14 +24,19 @@
 namespace fp8k {
 
 // ------------------------------------------------------------------- sort --
-// One cluster of up to eight CTAs of 32 warps; warp g of it owns the g-th run
-// of consecutive pairs.  A pass counts each warp's pairs per expert in shared
-// memory, two prefix sums (over the warps of the cluster, the CTAs' totals
-// exchanged through distributed shared memory, and over the experts) turn the
-// counts into first rows, and a second pass hands the rows out in order: the
-// lanes of 32 pairs that chose the same expert find each other with one match
-// instruction.  No atomic decides an order, no scratch, one launch.
-constexpr int kSortWarps = 32, kSortCluster = 8;
+// One cluster of up to 16 CTAs of 32 warps; warp g of it owns the g-th run
+// of consecutive pairs.  A first pass ranks each pair among its warp's pairs of
+// the same expert: the lanes of 32 pairs that chose the same expert find each
+// other by a vote per bit of the expert's number (the match instruction is one,
+// but 131072 pairs took 25 us with it: its unit was the limit), and the counts
+// so far sit in shared memory.  Two prefix sums (over the warps of the cluster,
+// the CTAs' totals exchanged through distributed shared memory, and over the
+// experts) turn the counts into first rows, which a second pass adds to the
+// ranks.  Both passes have eight loads per lane in flight.  The pairs of the
+// rows are scattered by a kernel of their own on all SMs: a scattered store
+// takes a cycle per lane, 4 us on the cluster's 16 SMs.  No atomic, no
+// scratch.
+constexpr int kSortWarps = 32, kSortCluster = 16, kSortRun = 8;
 
 __device__ __forceinline__ uint32_t ld_shared_cluster_u32(uint32_t cluster_addr) {
   uint32_t v;
@@ -39,7 +44,22 @@ __device__ __forceinline__ uint32_t ld_shared_cluster_u32(uint32_t cluster_addr)
   return v;
 }
 
-template <typename ID>
+// lanes whose value (below 2^bits, bits <= 8) equals this lane's, of those that
+// have one (a lane without gets a mask that means nothing)
+__device__ __forceinline__ uint32_t lanes_alike(uint32_t v, bool has, int bits) {
+  uint32_t same = __ballot_sync(0xffffffffu, has);
+#pragma unroll
+  for (int b = 0; b < 8; ++b) {
+    if (b >= bits) break;
+    const bool one = v >> b & 1u;
+    const uint32_t ones = __ballot_sync(0xffffffffu, one);
+    same &= one ? ones : ~ones;
+  }
+  return same;
+}
+
+// SCATTER: also write pairs (nullable); else experts_pairs_kernel does.
+template <typename ID, bool SCATTER>
 __global__ void __launch_bounds__(32 * kSortWarps)
     experts_sort_kernel(const ID *ids, uint32_t P, int E, int32_t *offsets, int32_t *rows,
                         int32_t *pairs) {
@@ -53,10 +73,10 @@ __global__ void __launch_bounds__(32 * kSortWarps)
   launch_dependents();
   grid_dependency_wait();
   const uint32_t l = lane_id(), w = threadIdx.x >> 5;
-  const uint32_t ctas = gridDim.x, rank = ctas > 1 ? cluster_ctarank() : 0u;
+  const uint32_t ctas = gridDim.x, cta = ctas > 1 ? cluster_ctarank() : 0u;
   const uint32_t warps = ctas * kSortWarps;
   const uint32_t per = (P + warps * 32 - 1) / (warps * 32) * 32;
-  const uint32_t begin = min((rank * kSortWarps + w) * per, P), end = min(begin + per, P);
+  const uint32_t begin = min((cta * kSortWarps + w) * per, P), end = min(begin + per, P);
   uint32_t *const mine = count[w];
   // the expert of pair i; E for a dropped one
   auto expert = [&](uint32_t i) -> uint32_t {
@@ -66,10 +86,35 @@ __global__ void __launch_bounds__(32 * kSortWarps)
 
   for (int e = l; e < E; e += 32) mine[e] = 0u;
   __syncwarp();
-#pragma unroll 4
-  for (uint32_t i = begin + l; i < end; i += 32) {
-    const uint32_t e = expert(i);
-    if (e < (uint32_t)E) atomicAdd(mine + e, 1u);
+  const uint32_t below = (1u << l) - 1u;
+  const int bits = E > 1 ? 32 - __clz(E - 1) : 0;
+  // the experts and ranks of a batch of pairs; a warp's only batch stays here
+  // between the passes, the ranks of others wait in rows
+  const bool whole = per <= 32 * kSortRun;
+  uint32_t e[kSortRun];
+  int32_t rank[kSortRun];
+  auto load = [&](uint32_t i0) {
+#pragma unroll
+    for (int j = 0; j < kSortRun; ++j) {
+      const uint32_t i = i0 + 32 * j + l;
+      e[j] = i < end ? expert(i) : (uint32_t)E;
+    }
+  };
+  for (uint32_t i0 = begin; i0 < end; i0 += 32 * kSortRun) {
+    load(i0);
+#pragma unroll
+    for (int j = 0; j < kSortRun; ++j) {
+      if (i0 + 32 * j >= end) break;
+      const uint32_t i = i0 + 32 * j + l;
+      const bool has = e[j] < (uint32_t)E;
+      const uint32_t same = lanes_alike(e[j], has, bits), ahead = same & below;
+      const uint32_t seen = has ? mine[e[j]] : 0u;
+      __syncwarp();
+      if (has && ahead == 0u) mine[e[j]] = seen + __popc(same);
+      __syncwarp();
+      rank[j] = has ? (int32_t)(seen + __popc(ahead)) : -1;
+      if (!whole && i < end) rows[i] = rank[j];
+    }
   }
   __syncthreads();
 
@@ -110,7 +155,7 @@ __global__ void __launch_bounds__(32 * kSortWarps)
         const uint32_t at = smem_u32(total + e);
         for (uint32_t r = 0; r < ctas; ++r) {
           const uint32_t v = ld_shared_cluster_u32(mapa_shared(at, r));
-          if (r < rank) before += v;
+          if (r < cta) before += v;
           all += v;
         }
       } else {
@@ -131,75 +176,122 @@ __global__ void __launch_bounds__(32 * kSortWarps)
     for (uint32_t i = 0; i < w; ++i) incl += sums[i];
     if (e < E) {
       first[e] = incl - all + before;
-      if (rank == 0) offsets[e] = (int32_t)(incl - all);
+      if (cta == 0) offsets[e] = (int32_t)(incl - all);
       if (e == E - 1) {
         kept = incl;
-        if (rank == 0) offsets[E] = (int32_t)incl;
+        if (cta == 0) offsets[E] = (int32_t)incl;
       }
     }
   }
   __syncthreads();
 
-  const uint32_t below = (1u << l) - 1u;
-  uint32_t next = begin + l < end ? expert(begin + l) : (uint32_t)E;
-  for (uint32_t i0 = begin; i0 < end; i0 += 32) {
-    const uint32_t i = i0 + l, e = next;
-    next = i + 32 < end ? expert(i + 32) : (uint32_t)E;
-    const uint32_t same = __match_any_sync(0xffffffffu, e);
-    uint32_t row = 0;
-    if (e < (uint32_t)E) {
-      row = first[e] + mine[e] + __popc(same & below);
-      if (pairs != nullptr) pairs[row] = (int32_t)i;
+  for (int e = l; e < E; e += 32) mine[e] += first[e];
+  __syncwarp();
+  for (uint32_t i0 = begin; i0 < end; i0 += 32 * kSortRun) {
+    if (!whole) {
+      load(i0);
+#pragma unroll
+      for (int j = 0; j < kSortRun; ++j) {
+        const uint32_t i = i0 + 32 * j + l;
+        rank[j] = i < end ? rows[i] : -1;  // this lane's own of the first pass
+      }
     }
-    if (i < end) rows[i] = e < (uint32_t)E ? (int32_t)row : -1;
-    __syncwarp();
-    if (e < (uint32_t)E && (same & below) == 0u) mine[e] += __popc(same);
-    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < kSortRun; ++j) {
+      const uint32_t i = i0 + 32 * j + l;
+      if (i >= end) break;
+      const int32_t row = e[j] < (uint32_t)E ? (int32_t)mine[e[j]] + rank[j] : -1;
+      rows[i] = row;
+      if (SCATTER && pairs != nullptr && row >= 0) pairs[row] = (int32_t)i;
+    }
   }
-  if (pairs != nullptr)
-    for (uint32_t i = kept + rank * blockDim.x + threadIdx.x; i < P; i += ctas * blockDim.x)
+  if (SCATTER && pairs != nullptr)
+    for (uint32_t i = kept + cta * blockDim.x + threadIdx.x; i < P; i += ctas * blockDim.x)
       pairs[i] = -1;
   if (ctas > 1) cluster_sync();  // no CTA leaves while another may read its totals
 }
 
+// pairs[rows[i]] = i, and -1 behind the last row.
+__global__ void __launch_bounds__(256) experts_pairs_kernel(const int32_t *rows,
+                                                            const int32_t *kept, uint32_t P,
+                                                            int32_t *pairs) {
+  launch_dependents();
+  grid_dependency_wait();
+  const uint32_t i = blockIdx.x * blockDim.x + threadIdx.x;
+  if (i >= P) return;
+  const int32_t row = rows[i];
+  if (row >= 0) pairs[row] = (int32_t)i;
+  if (i >= (uint32_t)*kept) pairs[i] = -1;
+}
+
+// Up to 4096 pairs (128 a warp) one CTA, without the cluster's barriers, and the
+// scatter in place.
+template <typename ID>
+static cudaError_t run_sort(const ID *ids, int64_t P, int E, int32_t *offsets, int32_t *rows,
+                            int32_t *pairs, cudaStream_t st) {
+  if (P <= 4096)
+    return launch_serial(experts_sort_kernel<ID, true>, 1, 32 * kSortWarps, st, ids, (uint32_t)P, E,
+                         offsets, rows, pairs);
+  const cudaError_t e =
+      launch_serial_wide_cluster<experts_sort_kernel<ID, false>>(
+          kSortCluster, 32 * kSortWarps, kSortCluster, st, ids, (uint32_t)P, E, offsets, rows, pairs);
+  if (e != cudaSuccess || pairs == nullptr) return e;
+  return launch_serial(experts_pairs_kernel, (P + 255) / 256, 256, st,
+                       static_cast<const int32_t *>(rows), static_cast<const int32_t *>(offsets + E),
+                       (uint32_t)P, pairs);
+}
+
 cudaError_t launch_experts_sort(const void *ids, bool wide, int64_t P, int E, int32_t *offsets,
                                 int32_t *rows, int32_t *pairs, cudaStream_t st) {
-  const int ctas = P <= 4096 ? 1 : kSortCluster;
-  if (wide)
-    return launch_serial_cluster(experts_sort_kernel<int64_t>, ctas, 32 * kSortWarps, ctas, st,
-                                 static_cast<const int64_t *>(ids), (uint32_t)P, E, offsets, rows,
-                                 pairs);
-  return launch_serial_cluster(experts_sort_kernel<int32_t>, ctas, 32 * kSortWarps, ctas, st,
-                               static_cast<const int32_t *>(ids), (uint32_t)P, E, offsets, rows,
-                               pairs);
+  return wide ? run_sort(static_cast<const int64_t *>(ids), P, E, offsets, rows, pairs, st)
+              : run_sort(static_cast<const int32_t *>(ids), P, E, offsets, rows, pairs, st);
 }
+
+// A warp's walk over the tasks (token, window of columns) warp, warp + warps, ...
+// with the windows of a token next to each other.
+struct TaskWalk {
+  int64_t t, step_t;
+  int32_t win, wins, step_win;
+  __device__ __forceinline__ TaskWalk(int64_t K, int window) {
+    wins = (int32_t)((K + window - 1) / window);
+    const uint32_t warp = (blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+    const uint32_t warps = (gridDim.x * blockDim.x) >> 5;
+    t = warp / (uint32_t)wins;
+    win = (int32_t)(warp % (uint32_t)wins);
+    step_t = warps / (uint32_t)wins;
+    step_win = (int32_t)(warps % (uint32_t)wins);
+  }
+  __device__ __forceinline__ void next() {
+    t += step_t;
+    win += step_win;
+    if (win >= wins) {
+      win -= wins;
+      ++t;
+    }
+  }
+};
 
 // ----------------------------------------------------------------- gather --
 // A warp per (token, 512 columns): lane l holds 16 consecutive elements, so
 // eight lanes form a 1x128 group and each lane stores 16 bytes of codes per
 // row.  The token's rows sit in the lanes, one each; a group's scale for eight
-// rows goes out in one store instruction, one row per lane of the group.
+// rows goes out in one store instruction, one row per lane of the group.  (A
+// resident grid that loads the next task ahead of this one's stores measured
+// slower: 58 against 53 us for 4096 tokens of 7168 columns and eight rows each.)
 template <typename T, int F>
-__global__ void __launch_bounds__(256) experts_gather_kernel(const GatherArgs a) {
+__global__ void __launch_bounds__(256, 3) experts_gather_kernel(const GatherArgs a) {
   constexpr bool kCodes = sizeof(T) == 1;
   launch_dependents();
   grid_dependency_wait();
   const uint32_t l = lane_id();
-  const int64_t wins = (a.K + 511) / 512, tasks = a.T * wins;
-  const int64_t warps = ((int64_t)gridDim.x * blockDim.x) >> 5;
-  const bool narrow = tasks <= (int64_t)0xFFFFFFFFu;
   const float mx = fmt_max(F);
-  for (int64_t task = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5; task < tasks;
-       task += warps) {
-    int64_t t, win;
-    split_task(task, wins, narrow, t, win);
-    const int64_t k = win * 512 + l * 16, g = k >> 7;
+  for (TaskWalk w(a.K, 512); w.t < a.T; w.next()) {
+    const int64_t t = w.t, k = (int64_t)w.win * 512 + l * 16, g = k >> 7;
     const bool in = k < a.K;
+    int32_t mine = l < a.S ? a.rows[t * a.S + l] : -1;
     Vec16<T> v;
-    if (in)
-      v.load(static_cast<const T *>(a.x) + t * a.ldx + k);
-    else
-      v.zero();
+    v.zero();
+    if (in) v.load(static_cast<const T *>(a.x) + t * a.ldx + k);
     uint4 c = make_uint4(0u, 0u, 0u, 0u);
     uint32_t scale = 0u;  // bits of the fp32 scale, or the UE8M0 byte
     if constexpr (kCodes) {
@@ -221,22 +313,22 @@ __global__ void __launch_bounds__(256) experts_gather_kernel(const GatherArgs a)
     }
     for (int64_t s0 = 0; s0 < a.S; s0 += 32) {
       const int n = (int)min((int64_t)32, a.S - s0);
-      const int32_t mine = (int)l < n ? a.rows[t * a.S + s0 + l] : -1;
-      for (int s = 0; s < n; ++s) {
-        const int64_t row = __shfl_sync(0xffffffffu, mine, s);
-        if (row < 0 || row >= a.M || !in) continue;
-        if (a.q != nullptr) *reinterpret_cast<uint4 *>(a.q + row * a.K + k) = c;
-        if constexpr (!kCodes)
-          if (a.out != nullptr) v.store(static_cast<T *>(a.out) + row * a.ld_out + k);
-      }
-      if (a.q == nullptr) continue;
+      if (s0 > 0) mine = (int)l < n ? a.rows[t * a.S + s0 + l] : -1;
+      if (mine >= a.M) mine = -1;
       for (int s = 0; s < n; s += 8) {
-        const int64_t row = __shfl_sync(0xffffffffu, mine, s + (int)(l & 7u));
-        if (row < 0 || row >= a.M || 128 * g >= a.K) continue;
-        if (a.sfmt == 0)
-          static_cast<uint32_t *>(a.scales)[g * a.M + row] = scale;
-        else
-          static_cast<uint8_t *>(a.scales)[g * a.M + row] = (uint8_t)scale;
+        int32_t row[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) row[j] = __shfl_sync(0xffffffffu, mine, s + j);
+        const int32_t lane_row = __shfl_sync(0xffffffffu, mine, s + (int)(l & 7u));
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          if (row[j] < 0 || !in) continue;
+          if (a.q != nullptr) *reinterpret_cast<uint4 *>(a.q + row[j] * a.K + k) = c;
+          if constexpr (!kCodes)
+            if (a.out != nullptr) v.store(static_cast<T *>(a.out) + row[j] * a.ld_out + k);
+        }
+        if (a.q != nullptr && lane_row >= 0 && 128 * g < a.K)
+          store_scale(a.scales, g * a.M + lane_row, scale, a.sfmt);
       }
     }
   }
@@ -265,217 +357,382 @@ cudaError_t launch_experts_gather(const GatherArgs &a, int source, int sms, cuda
   return source == kGatherBf16 ? run_gather<__nv_bfloat16>(a, sms, st) : run_gather<float>(a, sms, st);
 }
 
-// ---------------------------------------------------------------- combine --
-// A warp per (token, 256 columns), eight elements per lane; up to eight rows'
-// loads in flight per lane.  Sums in fp32 in the order of the choices, the
-// residual last, one rounding to the output's type.
-template <typename T, typename O>
-__global__ void __launch_bounds__(256) experts_combine_kernel(const CombineArgs a) {
-  launch_dependents();
-  grid_dependency_wait();
+// --------------------------------------------------------- rows in flight --
+// Combine and its gradient read eight scattered rows (fp32: four) per step of
+// 256 columns, eight elements per lane.  A warp keeps a two-deep ring of steps in
+// shared memory: the rows of the next step are copied asynchronously while this
+// one is added up, and the choices of the step behind it are loaded meanwhile,
+// so that the warp always has 4 KB in flight and no registers hold them.  (Loads
+// into registers, a batch at a time, measured 116 and 151 us on 4096 tokens of
+// 7168 columns with eight rows each.)  A dropped pair's row is a copy of no
+// bytes, which leaves zeros.
+template <typename T>
+constexpr int rows_per_step() {
+  return sizeof(T) == 2 ? 8 : 4;
+}
+
+// 256 elements of a row: lane l's eight.  fp32: the row's 64 vectors go out as
+// whole sectors (lane l copies vectors l and l + 32); vector e sits in half e & 1
+// at column (e / 2) ^ 4 (e & 1), free of bank conflicts both ways.
+template <typename T>
+__device__ __forceinline__ void copy_row_async(uint8_t *slot, const T *src, int32_t left, bool real) {
+  const int32_t l = (int32_t)lane_id();
+  uint4 *dst = reinterpret_cast<uint4 *>(slot);
+  if constexpr (sizeof(T) == 2) {
+    copy16_async(dst + l, src + 8 * l, real && 8 * l < left);
+  } else {
+    const int32_t at = 32 * (l & 1) + ((l >> 1) ^ (4 * (l & 1)));
+    copy16_async(dst + at, src + 4 * l, real && 4 * l < left);
+    copy16_async(dst + at + 16, src + 4 * l + 128, real && 4 * l + 128 < left);
+  }
+}
+template <typename T>
+__device__ __forceinline__ Raw8<T> ring_row(const uint8_t *slot) {
   const uint32_t l = lane_id();
-  const T *x = static_cast<const T *>(a.x);
-  const O *res = static_cast<const O *>(a.residual);
-  const int64_t wins = (a.K + 255) / 256, tasks = a.T * wins;
-  const int64_t warps = ((int64_t)gridDim.x * blockDim.x) >> 5;
-  const bool narrow = tasks <= (int64_t)0xFFFFFFFFu;
-  for (int64_t task = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5; task < tasks;
-       task += warps) {
-    int64_t t, win;
-    split_task(task, wins, narrow, t, win);
-    const int64_t k = win * 256 + l * 8;
-    const bool in = k < a.K;
-    Raw8<O> r;
-    r.zero();
-    if (res != nullptr && in) r.load_stream(res + t * a.ldr + k);
-    F2 acc[4];
-    for (int64_t s0 = 0; s0 < a.S; s0 += 32) {
-      const int n = (int)min((int64_t)32, a.S - s0);
-      int32_t row_l = -1;
-      float w_l = 0.0f;  // a dropped pair: zero times zero
-      if ((int)l < n) {
-        row_l = a.rows[t * a.S + s0 + l];
-        if (row_l < 0 || row_l >= a.M)
-          row_l = -1;
-        else
-          w_l = a.weights != nullptr ? a.weights[t * a.S + s0 + l] : 1.0f;
-      }
-      for (int s = 0; s < n; s += 8) {
-        Raw8<T> v[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int64_t row = __shfl_sync(0xffffffffu, row_l, (s + j) & 31);
-          if (s + j < n && row >= 0 && in)
-            v[j].load_stream(x + row * a.ldx + k);
-          else
-            v[j].zero();
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float w = __shfl_sync(0xffffffffu, w_l, (s + j) & 31);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) acc[i] = fma2(F2(w), raw_pair(v[j], i), acc[i]);
-        }
-      }
+  const uint4 *src = reinterpret_cast<const uint4 *>(slot);
+  Raw8<T> r;
+  r.w[0] = src[l];
+  if constexpr (sizeof(T) == 4) r.w[1] = src[32 + (l ^ 4u)];
+  return r;
+}
+
+// Row and weight of choice s0 + j of token t on the lanes with l % C == j (a
+// dropped pair, and what lies behind the last: no row, weight zero).
+template <int C>
+__device__ __forceinline__ void load_choice(const int32_t *rows, const float *weights, int64_t t,
+                                            int64_t s0, int64_t T, int64_t S, int64_t M,
+                                            int32_t &row, float &wt) {
+  const int64_t s = s0 + (lane_id() & (uint32_t)(C - 1));
+  row = -1;
+  wt = 0.0f;
+  if (t < T && s < S) {
+    const int32_t r = rows[t * S + s];
+    const float v = weights != nullptr ? weights[t * S + s] : 1.0f;
+    if (r >= 0 && r < M) {
+      row = r;
+      wt = v;
     }
-    if (!in) continue;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) acc[i] = acc[i] + raw_pair(r, i);
-    store8(static_cast<O *>(a.out) + t * a.ld_out + k, round8<O>(acc));
   }
 }
 
-template <typename T>
-static cudaError_t run_combine(const CombineArgs &a, int out_dt, int sms, cudaStream_t st) {
-  const int64_t blocks = grid_of(a.T * ((a.K + 255) / 256), 8, (int64_t)sms * 64);
-  return out_dt == 0 ? launch_serial(experts_combine_kernel<T, __nv_bfloat16>, blocks, 256, st, a)
-                     : launch_serial(experts_combine_kernel<T, float>, blocks, 256, st, a);
+constexpr int kRingWarps = 8;  // of a CTA
+
+// ---------------------------------------------------------------- combine --
+// A warp per (token, 256 columns).  Sums in fp32 in the order of the choices, the
+// residual last, one rounding to the output's type.
+template <typename T, typename O>
+constexpr int combine_stage() {
+  return 256 * (rows_per_step<T>() * (int)sizeof(T) + (int)sizeof(O));
+}
+
+template <typename T, typename O>
+__global__ void __launch_bounds__(32 * kRingWarps, 3) experts_combine_kernel(const CombineArgs a) {
+  constexpr int kC = rows_per_step<T>(), kRow = 256 * sizeof(T), kStage = combine_stage<T, O>();
+  extern __shared__ __align__(16) uint8_t smem[];
+  uint8_t *ring = smem + (threadIdx.x >> 5) * (2 * kStage);
+  launch_dependents();
+  grid_dependency_wait();
+  const T *x = static_cast<const T *>(a.x);
+  const O *res = static_cast<const O *>(a.residual);
+  struct Step {
+    TaskWalk w;
+    int64_t s0;
+    __device__ __forceinline__ void next(int64_t S) {
+      s0 += kC;
+      if (s0 >= S) {
+        s0 = 0;
+        w.next();
+      }
+    }
+  };
+  auto fetch = [&](const Step &s, int32_t row, int stage) {
+    if (s.w.t < a.T) {
+      const int64_t k0 = (int64_t)s.w.win * 256;
+      const int32_t left = (int32_t)min((int64_t)256, a.K - k0);
+      uint8_t *slot = ring + stage * kStage;
+      const int n = (int)min((int64_t)kC, a.S - s.s0);
+#pragma unroll
+      for (int j = 0; j < kC; ++j) {
+        const int64_t r = __shfl_sync(0xffffffffu, row, j);
+        if (j < n)  // (a place that may be read, but is not, for a row that does not exist)
+          copy_row_async(slot + j * kRow, r >= 0 ? x + r * a.ldx + k0 : static_cast<const T *>(a.out),
+                         left, r >= 0);
+      }
+      if (res != nullptr && a.S <= kC)
+        copy_row_async(slot + kC * kRow, res + s.w.t * a.ldr + k0, left, true);
+    }
+    copies_commit();
+  };
+  Step cur{TaskWalk(a.K, 256), 0};
+  int32_t row_next;
+  float w_cur, w_next;
+  load_choice<kC>(a.rows, a.weights, cur.w.t, 0, a.T, a.S, a.M, row_next, w_cur);
+  fetch(cur, row_next, 0);
+  Step nxt = cur;
+  nxt.next(a.S);
+  load_choice<kC>(a.rows, a.weights, nxt.w.t, nxt.s0, a.T, a.S, a.M, row_next, w_next);
+  F2 acc[4];
+  for (int stage = 0; cur.w.t < a.T; stage ^= 1) {
+    __syncwarp();  // the other lanes have read what this overwrites
+    fetch(nxt, row_next, stage ^ 1);
+    Step behind = nxt;
+    behind.next(a.S);
+    const float w_l = w_cur;
+    w_cur = w_next;
+    load_choice<kC>(a.rows, a.weights, behind.w.t, behind.s0, a.T, a.S, a.M, row_next, w_next);
+    copies_wait<1>();
+    __syncwarp();
+    const uint8_t *slot = ring + stage * kStage;
+    const int n = (int)min((int64_t)kC, a.S - cur.s0);
+#pragma unroll
+    for (int j = 0; j < kC; ++j) {
+      const F2 wt(__shfl_sync(0xffffffffu, w_l, j));
+      if (j < n) {
+        const Raw8<T> v = ring_row<T>(slot + j * kRow);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[i] = fma2(wt, raw_pair(v, i), acc[i]);
+      }
+    }
+    if (a.S <= kC) {  // the residual is in this step's stage
+      if (res != nullptr) {
+        const Raw8<O> r = ring_row<O>(slot + kC * kRow);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[i] = acc[i] + raw_pair(r, i);
+      }
+    }
+    if (cur.s0 + kC >= a.S) {
+      const int64_t k = (int64_t)cur.w.win * 256 + lane_id() * 8;
+      if (k < a.K) {
+        if (a.S > kC && res != nullptr) {  // (longer lists: its stage has gone)
+          Raw8<O> r;
+          r.load_stream(res + cur.w.t * a.ldr + k);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[i] = acc[i] + raw_pair(r, i);
+        }
+        store8(static_cast<O *>(a.out) + cur.w.t * a.ld_out + k, round8<O>(acc));
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[i] = F2(0.0f);
+    }
+    cur = nxt;
+    nxt = behind;
+  }
+  copies_wait<0>();
+}
+
+template <typename T, typename O>
+static cudaError_t run_combine(const CombineArgs &a, int sms, cudaStream_t st) {
+  const int64_t blocks = grid_of(a.T * ((a.K + 255) / 256), kRingWarps, (int64_t)sms * 3);
+  constexpr int kSmem = kRingWarps * 2 * combine_stage<T, O>();
+  return launch_serial_smem<experts_combine_kernel<T, O>, kSmem>(blocks, 32 * kRingWarps, kSmem, st,
+                                                                 a);
 }
 
 cudaError_t launch_experts_combine(const CombineArgs &a, int x_dt, int out_dt, int sms,
                                    cudaStream_t st) {
   if (a.T == 0) return cudaSuccess;
-  return x_dt == 0 ? run_combine<__nv_bfloat16>(a, out_dt, sms, st)
-                   : run_combine<float>(a, out_dt, sms, st);
+  if (x_dt == 0)
+    return out_dt == 0 ? run_combine<__nv_bfloat16, __nv_bfloat16>(a, sms, st)
+                       : run_combine<__nv_bfloat16, float>(a, sms, st);
+  return out_dt == 0 ? run_combine<float, __nv_bfloat16>(a, sms, st)
+                     : run_combine<float, float>(a, sms, st);
 }
 
 // ------------------------------------------------------- combine, gradient --
-// A CTA per token, a warp per 512 columns of it (16 elements per lane, groups
-// of eight lanes).  |w dy| of a group peaks where |dy| does (rounding is
-// monotone), so the group's maximum of dy is taken once and lane j of the
-// group forms the scale of the j-th of eight rows from it.  The eight rows'
-// dot products stay in registers and are reduced together: a butterfly that
-// halves the rows a lane still holds at each of its first three steps.
+// A CTA per token, each warp every nw-th 256 columns of it, up to eight rows
+// (fp32: four) at a time.  |w dy| of a group (16 lanes) peaks where |dy| does
+// (rounding is monotone), so the group's maximum of dy is taken once and lane j
+// of the group forms the scale of the j-th row from it, and the factor w / scale
+// that takes dy to that row's codes.  The rows' dot products stay in registers and
+// are reduced together: a butterfly that halves the rows a lane still holds at
+// each of its first steps, then a sum over the warps in their order.
+template <typename DY, typename X>
+constexpr int combine_grad_stage() {
+  return 256 * (rows_per_step<X>() * (int)sizeof(X) + (int)sizeof(DY));
+}
+
 template <typename DY, typename X, int F>
-__global__ void __launch_bounds__(512) experts_combine_grad_kernel(const CombineGradArgs a) {
-  __shared__ float part[2][16][8];
+__global__ void __launch_bounds__(32 * kRingWarps, 3)
+    experts_combine_grad_kernel(const CombineGradArgs a) {
+  constexpr int kC = rows_per_step<X>(), kRow = 256 * sizeof(X),
+                kStage = combine_grad_stage<DY, X>();
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ float part[2][kRingWarps][kC];
   launch_dependents();
   grid_dependency_wait();
   const uint32_t l = lane_id(), w = threadIdx.x >> 5, nw = blockDim.x >> 5;
+  uint8_t *ring = smem + w * (2 * kStage);
   const DY *dy = static_cast<const DY *>(a.dy);
   const X *x = static_cast<const X *>(a.x);
-  const float mx = fmt_max(F);
-  const int64_t wins = (a.K + 511) / 512;
-  int phase = 0;
-  for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
-    for (int64_t s0 = 0; s0 < a.S; s0 += 8) {
-      const int n = (int)min((int64_t)8, a.S - s0);
-      // lane j holds row and weight of choice s0 + j % 8
-      const int j_l = (int)(l & 7u);
-      int32_t row_l = -1;
-      float w_l = 0.0f;
-      if (j_l < n) {
-        row_l = a.rows[t * a.S + s0 + j_l];
-        if (row_l < 0 || row_l >= a.M) row_l = -1;
-        w_l = a.weights != nullptr ? a.weights[t * a.S + s0 + j_l] : 1.0f;
-      }
-      float dot[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) dot[j] = 0.0f;
-      for (int64_t win = w; win < wins; win += nw) {
-        const int64_t k = win * 512 + l * 16, g = k >> 7;
-        const bool in = k < a.K;
-        Vec16<DY> v;
-        if (in)
-          v.load(dy + t * a.ld_dy + k);
-        else
-          v.zero();
-        float inv_l = 0.0f, s_l = 1.0f;  // row j's scale, and its reciprocal
-        bool fast = true;
-        if (a.q != nullptr) {
-          const float amax = fabsf(w_l) * __uint_as_float(group8_max(v.max_key()));
-          const bool keep = row_l >= 0 && 128 * g < a.K;
-          if (a.sfmt == 0) {
-            s_l = scale_from_amax(amax, mx);
-            if (keep) static_cast<float *>(a.scales)[g * a.M + row_l] = s_l;
-          } else {
-            const int e = ue8m0_exponent(amax, mx);
-            s_l = exp2_int(e);
-            if (keep) static_cast<uint8_t *>(a.scales)[g * a.M + row_l] = (uint8_t)(e + 127);
-          }
-          const CodeScale d(s_l);
-          inv_l = d.inv;
-          fast = __all_sync(0xffffffffu, d.fast);
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int64_t row = __shfl_sync(0xffffffffu, row_l, j);
-          const float wj = __shfl_sync(0xffffffffu, w_l, j);
-          const int from = (int)(l & 24u) | j;
-          const float inv = __shfl_sync(0xffffffffu, inv_l, from);
-          const float s = __shfl_sync(0xffffffffu, s_l, from);
-          if (row < 0 || !in) continue;
-          if (a.dw != nullptr) {
-            Vec16<X> xv;
-            xv.load(x + row * a.ldx + k);
-            F2 d2(0.0f);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) d2 = fma2(v.pair(i), xv.pair(i), d2);
-            float d0, d1;
-            d2.get(d0, d1);
-            dot[j] += d0 + d1;
-          }
-          if (a.q == nullptr && a.dx == nullptr) continue;
-          F2 y[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) y[i] = v.pair(i) * F2(wj);
-          if (a.dx != nullptr) {
-            if (a.dx_dt == 0)
-              store16(static_cast<__nv_bfloat16 *>(a.dx) + row * a.ld_dx + k, y);
-            else
-              store16(static_cast<float *>(a.dx) + row * a.ld_dx + k, y);
-          }
-          if (a.q != nullptr) {
-            uint4 c;
-            if (fast) {
-#pragma unroll
-              for (int i = 0; i < 8; ++i) y[i] = y[i] * F2(inv);
-              c = pack16<F>(y);
-            } else {
-#pragma unroll
-              for (int i = 0; i < 8; ++i) y[i] = each(y[i], [s](float z) { return __fdiv_rn(z, s); });
-              c = pack16<F>(y);
-            }
-            *reinterpret_cast<uint4 *>(a.q + row * a.K + k) = c;
-          }
+  const int32_t wins = (int32_t)((a.K + 255) / 256);
+  struct Step {
+    int64_t t, s0;
+    int32_t win;
+    __device__ __forceinline__ void next(int32_t wins, int32_t w, int32_t nw, int64_t S) {
+      win += nw;
+      if (win >= wins) {
+        win = w;
+        s0 += kC;
+        if (s0 >= S) {
+          s0 = 0;
+          t += gridDim.x;
         }
       }
-      if (a.dw == nullptr) continue;
-      // rows 4 apart, 2 apart, 1 apart: lane l ends with row (l >> 2) & 7
-#pragma unroll
-      for (int h = 4; h > 0; h >>= 1) {
-        const bool up = (l & (uint32_t)(4 * h)) != 0u;
-#pragma unroll
-        for (int j = 0; j < h; ++j) {
-          const float keep = up ? dot[j + h] : dot[j], give = up ? dot[j] : dot[j + h];
-          dot[j] = keep + __shfl_xor_sync(0xffffffffu, give, 4 * h);
-        }
-      }
-      float v = dot[0];
-      v += __shfl_xor_sync(0xffffffffu, v, 2);
-      v += __shfl_xor_sync(0xffffffffu, v, 1);
-      // (a buffer is written again two barriers after it was read)
-      if ((l & 3u) == 0u) part[phase][w][l >> 2] = v;
-      __syncthreads();
-      if ((int)threadIdx.x < n) {
-        float sum = 0.0f;
-        for (uint32_t i = 0; i < nw; ++i) sum += part[phase][i][threadIdx.x];
-        a.dw[t * a.S + s0 + threadIdx.x] = sum;
-      }
-      phase ^= 1;
     }
+  };
+  auto fetch = [&](const Step &s, int32_t row, int stage) {
+    if (s.t < a.T) {
+      const int64_t k0 = (int64_t)s.win * 256;
+      const int32_t left = (int32_t)min((int64_t)256, a.K - k0);
+      uint8_t *slot = ring + stage * kStage;
+      const DY *d = dy + s.t * a.ld_dy + k0;
+      copy_row_async(slot + kC * kRow, d, left, true);
+      if (a.dw != nullptr) {
+        const int n = (int)min((int64_t)kC, a.S - s.s0);
+#pragma unroll
+        for (int j = 0; j < kC; ++j) {
+          const int64_t r = __shfl_sync(0xffffffffu, row, j);
+          if (j < n)  // (a place that may be read, but is not, for a row that does not exist)
+            copy_row_async(slot + j * kRow, r >= 0 ? x + r * a.ldx + k0 : reinterpret_cast<const X *>(dy),
+                           left, r >= 0);
+        }
+      }
+    }
+    copies_commit();
+  };
+  Step cur{(int64_t)blockIdx.x, 0, (int32_t)w};
+  int32_t row_cur, row_next;
+  float w_cur, w_next;
+  load_choice<kC>(a.rows, a.weights, cur.t, 0, a.T, a.S, a.M, row_cur, w_cur);
+  fetch(cur, row_cur, 0);
+  Step nxt = cur;
+  nxt.next(wins, (int32_t)w, (int32_t)nw, a.S);
+  load_choice<kC>(a.rows, a.weights, nxt.t, nxt.s0, a.T, a.S, a.M, row_next, w_next);
+  float dot[kC];
+#pragma unroll
+  for (int j = 0; j < kC; ++j) dot[j] = 0.0f;
+  int phase = 0;
+  for (int stage = 0; cur.t < a.T; stage ^= 1) {
+    __syncwarp();  // the other lanes have read what this overwrites
+    fetch(nxt, row_next, stage ^ 1);
+    Step behind = nxt;
+    behind.next(wins, (int32_t)w, (int32_t)nw, a.S);
+    const int32_t row_l = row_cur;
+    const float w_l = w_cur;
+    row_cur = row_next;
+    w_cur = w_next;
+    load_choice<kC>(a.rows, a.weights, behind.t, behind.s0, a.T, a.S, a.M, row_next, w_next);
+    copies_wait<1>();
+    __syncwarp();
+    const uint8_t *slot = ring + stage * kStage;
+    const int64_t k = (int64_t)cur.win * 256 + l * 8, g = k >> 7;
+    const bool in = k < a.K;
+    const int n = (int)min((int64_t)kC, a.S - cur.s0);
+    const Raw8<DY> raw = ring_row<DY>(slot + kC * kRow);
+    F2 v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = raw_pair(raw, i);
+    if (a.q != nullptr) {
+      uint32_t ka = 0, kb = 0;
+      raw.max_abs(ka, kb);
+      uint32_t key = Raw8<DY>::merge_keys(ka, kb);
+      key = max(key, __shfl_xor_sync(0xffffffffu, key, 8));
+      const float amax = fabsf(w_l) * __uint_as_float(group8_max(key));
+      GroupScale gs = group_scale<F>(amax, a.sfmt);
+      const float f_l = w_l * gs.inv;
+      const bool fast = __all_sync(
+          0xffffffffu, gs.fast && (w_l == 0.0f || (fabsf(f_l) >= 0x1p-100f && fabsf(f_l) <= 0x1p100f)));
+      if (!fast) gs = group_scale_any<F>(amax, a.sfmt);
+      if (row_l >= 0 && (l & 15u) < (uint32_t)kC && 128 * g < a.K)
+        store_scale(a.scales, g * a.M + row_l, gs.stored, a.sfmt);
+#pragma unroll
+      for (int j = 0; j < kC; ++j) {
+        const int64_t row = __shfl_sync(0xffffffffu, row_l, j);
+        const int from = (int)(l & 16u) | j;
+        uint2 c;
+        if (fast) {
+          const F2 f(__shfl_sync(0xffffffffu, f_l, from));
+          c = make_uint2(pack4<F>(v[0] * f, v[1] * f), pack4<F>(v[2] * f, v[3] * f));
+        } else {
+          const F2 wj(__shfl_sync(0xffffffffu, w_l, j));
+          const float s = __shfl_sync(0xffffffffu, gs.s, from);
+          c = make_uint2(codes4_ieee<F>((v[0] * wj).v, (v[1] * wj).v, s),
+                         codes4_ieee<F>((v[2] * wj).v, (v[3] * wj).v, s));
+        }
+        if (row >= 0 && in) *reinterpret_cast<uint2 *>(a.q + row * a.K + k) = c;
+      }
+    }
+    if (a.dx != nullptr) {
+#pragma unroll
+      for (int j = 0; j < kC; ++j) {
+        const int64_t row = __shfl_sync(0xffffffffu, row_l, j);
+        const F2 wj(__shfl_sync(0xffffffffu, w_l, j));
+        if (row < 0 || !in) continue;
+        const F2 y[4] = {v[0] * wj, v[1] * wj, v[2] * wj, v[3] * wj};
+        if (a.dx_dt == 0)
+          store8(static_cast<__nv_bfloat16 *>(a.dx) + row * a.ld_dx + k, round8<__nv_bfloat16>(y));
+        else
+          store8(static_cast<float *>(a.dx) + row * a.ld_dx + k, round8<float>(y));
+      }
+    }
+    if (a.dw != nullptr) {
+#pragma unroll
+      for (int j = 0; j < kC; ++j) {
+        if (j >= n) continue;
+        const Raw8<X> xv = ring_row<X>(slot + j * kRow);
+        F2 d2(0.0f);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) d2 = fma2(v[i], raw_pair(xv, i), d2);
+        float d0, d1;
+        d2.get(d0, d1);
+        dot[j] += d0 + d1;
+      }
+      if (cur.win + (int32_t)nw >= wins) {  // this warp's last columns of these rows
+        // halves apart, quarters apart, ...: lane l ends with row l / (32 / kC)
+#pragma unroll
+        for (int h = kC / 2; h > 0; h >>= 1) {
+          const uint32_t apart = (uint32_t)(32 / kC * h);
+#pragma unroll
+          for (int j = 0; j < h; ++j) {
+            const float keep = l & apart ? dot[j + h] : dot[j], give = l & apart ? dot[j] : dot[j + h];
+            dot[j] = keep + __shfl_xor_sync(0xffffffffu, give, (int)apart);
+          }
+        }
+        float d = dot[0];
+#pragma unroll
+        for (int o = 16 / kC; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+        // (a buffer is written again two barriers after it was read)
+        if (l % (32 / kC) == 0) part[phase][w][l / (32 / kC)] = d;
+        __syncthreads();
+        if ((int)threadIdx.x < n) {
+          float sum = 0.0f;
+          for (uint32_t i = 0; i < nw; ++i) sum += part[phase][i][threadIdx.x];
+          a.dw[cur.t * a.S + cur.s0 + threadIdx.x] = sum;
+        }
+        phase ^= 1;
+#pragma unroll
+        for (int j = 0; j < kC; ++j) dot[j] = 0.0f;
+      }
+    }
+    cur = nxt;
+    nxt = behind;
   }
+  copies_wait<0>();
 }
 
+// The fewest rounds of up to eight windows, then as few warps as they need.
+template <typename DY, typename X, int F>
+static cudaError_t run_combine_grad(const CombineGradArgs &a, int sms, cudaStream_t st) {
+  const int64_t wins = (a.K + 255) / 256, rounds = (wins + kRingWarps - 1) / kRingWarps;
+  const int warps = (int)((wins + rounds - 1) / rounds);
+  const int64_t most = (int64_t)sms * (3 * kRingWarps / warps);  // resident at once
+  constexpr int kWarpSmem = 2 * combine_grad_stage<DY, X>();
+  return launch_serial_smem<experts_combine_grad_kernel<DY, X, F>, kRingWarps * kWarpSmem>(
+      a.T < most ? a.T : most, 32 * warps, warps * kWarpSmem, st, a);
+}
 template <typename DY, typename X>
 static cudaError_t run_combine_grad(const CombineGradArgs &a, int sms, cudaStream_t st) {
-  const int64_t wins = (a.K + 511) / 512;
-  const int warps = (int)(wins < 16 ? wins : 16);
-  const int64_t most = (int64_t)sms * 32;
-  const int64_t blocks = a.T < most ? a.T : most;
-  return a.fmt == 0
-             ? launch_serial(experts_combine_grad_kernel<DY, X, 0>, blocks, 32 * warps, st, a)
-             : launch_serial(experts_combine_grad_kernel<DY, X, 1>, blocks, 32 * warps, st, a);
+  return a.fmt == 0 ? run_combine_grad<DY, X, 0>(a, sms, st) : run_combine_grad<DY, X, 1>(a, sms, st);
 }
 
 cudaError_t launch_experts_combine_grad(const CombineGradArgs &a, int dy_dt, int x_dt, int sms,

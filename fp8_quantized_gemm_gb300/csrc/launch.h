@@ -8,13 +8,16 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 namespace fp8k {
 
 // `cluster` CTAs of a thread-block cluster (1: none); blocks is a multiple.
 template <typename... KArgs, typename... Args>
 cudaError_t launch_serial_cluster(void (*kern)(KArgs...), int64_t blocks, int threads, int cluster,
-                                  cudaStream_t st, Args... args) {
+                                  int smem, cudaStream_t st, Args... args) {
   cudaLaunchConfig_t cfg = {};
+  cfg.dynamicSmemBytes = (size_t)smem;
   cfg.gridDim = dim3((unsigned)blocks);
   cfg.blockDim = dim3((unsigned)threads);
   cfg.stream = st;
@@ -33,7 +36,41 @@ cudaError_t launch_serial_cluster(void (*kern)(KArgs...), int64_t blocks, int th
 template <typename... KArgs, typename... Args>
 cudaError_t launch_serial(void (*kern)(KArgs...), int64_t blocks, int threads, cudaStream_t st,
                           Args... args) {
-  return launch_serial_cluster(kern, blocks, threads, 1, st, args...);
+  return launch_serial_cluster(kern, blocks, threads, 1, 0, st, args...);
+}
+
+// Sets an attribute of a kernel once per device.
+template <auto KERN, cudaFuncAttribute ATTR>
+cudaError_t allow_once(int value) {
+  static std::atomic<uint64_t> allowed{0};  // a bit per device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = (uint64_t)1 << (dev & 63);
+  if ((allowed.load(std::memory_order_relaxed) & bit) == 0) {
+    e = cudaFuncSetAttribute(KERN, ATTR, value);
+    if (e != cudaSuccess) return e;
+    allowed.fetch_or(bit, std::memory_order_relaxed);
+  }
+  return cudaSuccess;
+}
+
+// With dynamic shared memory that may exceed 48 KB (at most MOST).
+template <auto KERN, int MOST, typename... Args>
+cudaError_t launch_serial_smem(int64_t blocks, int threads, int smem, cudaStream_t st,
+                               Args... args) {
+  const cudaError_t e = allow_once<KERN, cudaFuncAttributeMaxDynamicSharedMemorySize>(MOST);
+  if (e != cudaSuccess) return e;
+  return launch_serial_cluster(KERN, blocks, threads, 1, smem, st, args...);
+}
+
+// In clusters of more than eight CTAs.
+template <auto KERN, typename... Args>
+cudaError_t launch_serial_wide_cluster(int64_t blocks, int threads, int cluster, cudaStream_t st,
+                                       Args... args) {
+  const cudaError_t e = allow_once<KERN, cudaFuncAttributeNonPortableClusterSizeAllowed>(1);
+  if (e != cudaSuccess) return e;
+  return launch_serial_cluster(KERN, blocks, threads, cluster, 0, st, args...);
 }
 
 }  // namespace fp8k

@@ -788,9 +788,9 @@ FP8_API int fp8_experts_combine(const fp8_experts_combine_t *combine, fp8_stream
 /* fp8_experts_combine_backward: with v = w[t,s] dy[t] in fp32 (weights null:
  * dy[t]), for row r = rows[t,s]:
  *   q, scales   nullable together: codes of v (fmt; E4M3 is what
- *               fp8_gemm_group_experts reads) in 1x128 groups, with v times
- *               the rounded reciprocal of a scale in the place of the exact
- *               quotient
+ *               fp8_gemm_group_experts reads) in 1x128 groups, with dy times
+ *               w times the reciprocal of a scale (within an ulp) in the place
+ *               of the exact quotient
  *   dx          nullable [M, ld_dx] of dx_dt: v, rounded once
  *   d_weights   nullable fp32 [T, S] (x given): sum_k dy[t,k] x[r,k], in a
  *               fixed order
@@ -824,7 +824,7 @@ FP8_API int fp8_experts_combine_backward(const fp8_experts_combine_grad_t *grad,
  *
  *   fp8_act_checkpoint            q <- codes of a; h_q, u_q <- h, u as E4M3 codes
  *                                 in 1x128 groups (fp8_quantize_token_group's
- *                                 bytes), 2.06 bytes an element for two bf16
+ *                                 scales), 2.06 bytes an element for two bf16
  *   fp8_act_checkpoint_backward   dh = da u act'(h), du = da act(h) at the values
  *                                 h and u that the checkpoints stand for
  *
@@ -833,8 +833,9 @@ FP8_API int fp8_experts_combine_backward(const fp8_experts_combine_grad_t *grad,
  *   mode   FP8_NORM_TENSOR: codes under scales fixed before the call (delayed
  *          scaling), the maxima (nullable, cleared by the call, not a scale
  *          itself) taken of the fp32 results; FP8_NORM_GROUP: 1x128 groups of
- *          sfmt with scales [ceil(N/128), M].  Values times the rounded
- *          reciprocal of a scale stand in the place of the exact quotient.
+ *          sfmt with scales [ceil(N/128), M].  Here and in the checkpoints
+ *          values times the reciprocal of a scale (within an ulp) stand in the
+ *          place of the exact quotient.
  *   valid_rows  nullable DEVICE int32: rows at and behind valid_rows[0] are
  *          neither read nor written and are in no maximum (offsets + experts of
  *          fp8_experts_sort: the rows that hold no token).

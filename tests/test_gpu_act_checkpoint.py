@@ -111,6 +111,17 @@ def quantizer(x, sfmt):
     return q.contiguous().view(torch.uint8), kept.t().contiguous()
 
 
+def check_kept(q, s, x, sfmt):
+    """A checkpoint of bf16 x: the quantizer's scales, and codes of x times the
+    scale's reciprocal (2^-23 off) rounded once more: 2^-22 and half a step."""
+    _, ws = quantizer(x, sfmt)
+    assert torch.equal(s, ws)
+    sv = (pow2(ws) if sfmt else ws.double()).t()[:, :, None]
+    u = (groups(x.double()) / sv).flatten(1)[:, :x.shape[1]]
+    bad = (q.view(F8[0]).double() - u).abs() > half_step(u, 0) * (1 + 1e-6) + 2.0 ** -22 * u.abs()
+    assert not bad.any(), int(bad.sum())
+
+
 def kept_values(q, s, sfmt):
     """The values that a checkpoint stands for, in 64 bits."""
     s = pow2(s) if sfmt else s.double()
@@ -189,9 +200,7 @@ def test_forward(m, n, act, gate, mode, fmt, sfmt, keep_sfmt, valid, wide):
         check_group(q[:live], sc[:, :live], want, err, fmt, sfmt)
     assert ((out[:live].double() - want).abs() <= 2.0 ** -8 * want.abs() * (1 + REL) + err).all()
     for name, x in zip(names, (h, u)):
-        wq, ws = quantizer(x[:live], keep_sfmt)
-        assert torch.equal(kept[name + "_q"][:live], wq)
-        assert torch.equal(kept[name + "_scales"][:, :live], ws)
+        check_kept(kept[name + "_q"][:live], kept[name + "_scales"][:, :live], x[:live], keep_sfmt)
     # rows behind the valid ones are as they were
     for t in [q, out] + [kept[x + "_q"] for x in names]:
         assert (t[live:] == (0xA5 if t.dtype == torch.uint8 else -7.0)).all()
@@ -291,8 +300,7 @@ def test_limits_and_non_finite_arguments():
         F.fp8_act_checkpoint(h, None, ACTS.index(act), q, scale=scale, out=out, h_q=hq, h_scales=hs)
         assert float(out[0, 0]) == float("inf") and float(out[1, 0]) == 0.0
         assert int(q[0, 0]) == 0x7E and int(q[1, 0]) & 0x7F == 0 and int(q[2, 0]) & 0x7F == 0x7F
-        wq, ws = quantizer(h, 0)
-        assert torch.equal(hs[:, 3], ws[:, 3]) and torch.equal(hq[3], wq[3])
+        check_kept(hq[3:], hs[:, 3:], h[3:], 0)
         dh = fill((4, n), BF)
         F.fp8_act_checkpoint_backward(torch.ones_like(h), ACTS.index(act), hq, hs, dh=dh)
         nan = torch.isnan(dh)
@@ -308,8 +316,7 @@ def test_extreme_scales():
     q, sc = fill((3, n), torch.uint8), fill((1, 3), torch.float32)
     hq, hs = fill((3, n), torch.uint8), fill((1, 3), torch.float32)
     F.fp8_act_checkpoint(h, None, F.ACT_NONE, q, scales=sc, h_q=hq, h_scales=hs)
-    wq, ws = quantizer(h, 0)
-    assert torch.equal(hs, ws) and torch.equal(hq, wq)
+    check_kept(hq, hs, h, 0)
     check_group(q, sc, h.double(), torch.zeros_like(h.double()), 0, 0)
 
 
@@ -323,8 +330,8 @@ def test_rows_beyond_32_bit_offsets():
     g = (n + 127) // 128
     sc, hs = torch.zeros((g, m), device="cuda"), torch.zeros((g, m), device="cuda")
     F.fp8_act_checkpoint(h, None, F.ACT_SILU, q, scales=sc, h_q=hq, h_scales=hs)
-    wq, ws = quantizer(vals, 0)
-    assert torch.equal(hq[first:], wq) and torch.equal(hs[:, first:], ws)
+    wq, ws = hq[first:], hs[:, first:]
+    check_kept(wq, ws, vals, 0)
     want = value(vals.double(), "silu")
     check_group(q[first:], sc[:, first:], want, REL * want.abs() + 1e-38, 0, 0)
     F.fp8_act_checkpoint_backward(h, F.ACT_SILU, hq, hs, dh_q=q, dh_scales=sc, fmt=F.E4M3)
@@ -401,8 +408,8 @@ def test_trainer_with_8_bit_checkpoints():
         for w, slot, y in ((tr.w1q, K1, h), (tr.w3q, K3, u))])
     vals = {}
     for name, y in (("h", h), ("u", u)):
-        q, s = quantizer(y, 0)
-        assert torch.equal(tr.kept[name + "_q"], q) and torch.equal(tr.kept[name + "_scales"], s)
+        q, s = tr.kept[name + "_q"], tr.kept[name + "_scales"]
+        check_kept(q, s, y, 0)
         vals[name] = kept_values(q, s, 0)
     want = value(h.double(), "silu") * u.double()
     check_tensor(tr.aq, tr.amax[A2:A2 + 1], tr.scale[A2], want, REL * want.abs() + 1e-30, 0)
