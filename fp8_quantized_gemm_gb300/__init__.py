@@ -820,55 +820,83 @@ _pack_act, _pack_act_ckpt_grad = _packer(ActCheckpoint), _packer(ActCheckpointGr
 _c_sort, _c_gather = _lib.fp8_experts_sort, _lib.fp8_experts_gather
 _c_combine, _c_combine_grad = _lib.fp8_experts_combine, _lib.fp8_experts_combine_backward
 _c_act, _c_act_grad = _lib.fp8_act_checkpoint, _lib.fp8_act_checkpoint_backward
-_I32 = torch.int32
+_I32, _I64, _U8 = torch.int32, torch.int64, torch.uint8
 
 
-def _here(*tensors):
-    """The tensors (None skipped) lie on the current device."""
-    dev = _get_device()
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            raise ValueError("operands must be on the current device")
+# Checks of one operand each, for calls that sit between decoded tokens' kernels:
+# an attribute of a tensor costs 0.06 to 0.12 us here, a kernel two to three, so
+# each is read once (get_device() is -1 off the GPU and so covers is_cuda).
+
+def _matrix(t, m, n, dtype, dev, what):
+    """(device pointer, row pitch) of a matrix [m, n] with contiguous rows."""
+    if t.dtype is dtype and t.get_device() == dev and t.shape == (m, n):
+        ld, one = t.stride()
+        if m == 1 and one == 1:
+            return t.data_ptr(), n
+        if one == 1 and ld >= n:
+            return t.data_ptr(), ld
+        if m == 0:
+            return 0, n
+    raise ValueError("%s must be a matrix of %s [%d, %d] with contiguous rows on the current device"
+                     % (what, dtype, m, n))
 
 
-def _ints(t, n, what):
-    """Device pointer of n contiguous int32 values (None -> 0)."""
-    if t is None:
-        return 0
-    if t.dtype != _I32 or t.numel() != n or not t.is_cuda or not t.is_contiguous():
-        raise ValueError("%s must be contiguous CUDA int32 [%d]" % (what, n))
-    return t.data_ptr()
+def _list(t, dtype, n, dev, what):
+    """Device pointer of n contiguous values."""
+    if t.dtype is dtype and t.numel() == n and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    raise ValueError("%s must be contiguous %s [%d] on the current device" % (what, dtype, n))
 
 
-def _grouped_rows(t, k, what):
-    """Rows of the grouped side: M of a matrix [M, k]."""
-    if t.dim() != 2 or t.shape[1] != k:
-        raise ValueError("%s must be [M, %d]" % (what, k))
-    return t.shape[0]
-
-
-def _group_codes(q, scales, m, k, sfmt, what):
-    """(codes, scales) pointers of [m, k] in 1x128 groups; both or neither."""
-    if (q is None) != (scales is None):
+def _group_codes(q, scales, m, k, sfmt, dev, what):
+    """Device pointers of codes [m, k] and their 1x128-group scales."""
+    if q is None or scales is None:
         raise ValueError("%s needs its scales, and they it" % what)
-    if q is None:
-        return 0, 0
-    return (_codes(q, m * k, what),
-            _scales(scales, (k + 127) // 128 * m, 4 if sfmt == SCALE_F32 else 1, what + "'s scales"))
+    if (q.element_size() != 1 or q.numel() != m * k or q.get_device() != dev
+            or not q.is_contiguous()):
+        raise ValueError("%s must hold %d contiguous one-byte codes on the current device"
+                         % (what, m * k))
+    return q.data_ptr(), _group_scales(scales, m, k, sfmt, dev, what)
+
+
+def _group_scales(scales, m, k, sfmt, dev, what):
+    """Device pointer of the scales of [m, k] in 1x128 groups, at least."""
+    size = 4 if sfmt == SCALE_F32 else 1
+    if (scales.element_size() != size or scales.numel() < (k + 127) // 128 * m
+            or scales.get_device() != dev or not scales.is_contiguous()):
+        raise ValueError("%s's scales must be %d contiguous %d-byte values on the current device"
+                         % (what, (k + 127) // 128 * m, size))
+    return scales.data_ptr()
+
+
+def _float_type(t, what):
+    if t.dtype is _BF16:
+        return IN_BF16
+    if t.dtype is _F32:
+        return IN_F32
+    raise ValueError("%s must be bf16 or fp32" % what)
 
 
 def fp8_experts_sort(ids, experts, offsets, rows, pairs=None, stream=None):
     """Rows in expert order of the choices ids [T, S] (int32 or int64): offsets
     int32 [experts + 1], rows int32 [T, S] (-1: dropped, an id outside
     [0, experts)), pairs (optional) int32 [T * S], -1 behind the last row."""
+    dev = _get_device()
     t, s = ids.shape
-    if ids.dtype not in (_I32, torch.int64):
+    n = t * s
+    if ids.dtype is _I64:
+        dt = IDS_I64
+    elif ids.dtype is _I32:
+        dt = IDS_I32
+    else:
         raise ValueError("ids must be int32 or int64")
-    _here(ids, offsets, rows, pairs)
-    _check("fp8_experts_sort",
-           _c_sort(_flat(ids), IDS_I32 if ids.dtype == _I32 else IDS_I64, t, s, experts,
-                   _ints(offsets, experts + 1, "offsets"), _ints(rows, t * s, "rows"),
-                   _ints(pairs, t * s, "pairs"), _on(stream)))
+    rc = _c_sort(_list(ids, ids.dtype, n, dev, "ids"), dt, t, s, experts,
+                 _list(offsets, _I32, experts + 1, dev, "offsets"),
+                 _list(rows, _I32, n, dev, "rows"),
+                 0 if pairs is None else _list(pairs, _I32, n, dev, "pairs"),
+                 _raw_stream(dev) if stream is None else _stream(stream))
+    if rc:
+        raise Fp8Error("fp8_experts_sort", rc)
 
 
 def fp8_experts_gather(x, rows, *, q=None, scales=None, fmt=E4M3, sfmt=SCALE_F32, x_scales=None,
@@ -876,45 +904,69 @@ def fp8_experts_gather(x, rows, *, q=None, scales=None, fmt=E4M3, sfmt=SCALE_F32
     """Row rows[t, s] <- x[t]: as 1x128-group codes (q [M, K] with scales
     [ceil(K/128), M]) and / or as it is (out [M, K] of x's type).  x bf16 or
     fp32, or codes with x_scales [ceil(K/128), T], which are moved."""
+    dev = _get_device()
     t, k = x.shape
-    s = rows.shape[1]
-    _here(x, rows, q, scales, x_scales, out)
-    if q is None and out is None:
-        raise ValueError("q or out takes the rows")
-    m = _grouped_rows(out if q is None else q, k, "q and out")
-    pq, ps = _group_codes(q, scales, m, k, sfmt, "q")
+    if rows.dim() != 2 or rows.shape[0] != t:
+        raise ValueError("rows must be [T, S]")
+    n = rows.numel()
+    m = _grouped_rows(out if q is None else q, k, "q or out")
+    pq = ps = po = ldo = px = ldx = dt = pc = pcs = 0
+    if q is not None or scales is not None:
+        pq, ps = _group_codes(q, scales, m, k, sfmt, dev, "q")
     if x_scales is not None:
         if out is not None:
             raise ValueError("codes are moved into q")
-        px, dt, ldx, po, ldo = 0, 0, 0, 0, 0
-        pc, pcs = _group_codes(x, x_scales, t, k, sfmt, "x")
+        pc, pcs = _group_codes(x, x_scales, t, k, sfmt, dev, "x")
     else:
-        (px, ldx), dt, pc, pcs = _rows(x, (t, k), x.dtype, "x"), _in_dt(x), 0, 0
-        po, ldo = _rows(out, (m, k), x.dtype, "out")
-    d = _pack_gather(px, dt, ldx, pc, pcs, _ints(rows, t * s, "rows"), t, s, k, m, fmt, sfmt, pq,
-                     ps, po, ldo)
-    _check("fp8_experts_gather", _c_gather(d, _on(stream)))
+        dt = _float_type(x, "x")
+        px, ldx = _matrix(x, t, k, x.dtype, dev, "x")
+        if out is not None:
+            po, ldo = _matrix(out, m, k, x.dtype, dev, "out")
+    rc = _c_gather(_pack_gather(px, dt, ldx, pc, pcs, _list(rows, _I32, n, dev, "rows"), t,
+                                rows.shape[1], k, m, fmt, sfmt, pq, ps, po, ldo),
+                   _raw_stream(dev) if stream is None else _stream(stream))
+    if rc:
+        raise Fp8Error("fp8_experts_gather", rc)
 
 
-def _weights(weights, rows):
-    if weights is not None and weights.shape != rows.shape:
+def _grouped_rows(t, k, what):
+    """Rows of the grouped side: M of a matrix [M, k]."""
+    if t is None:
+        raise ValueError("%s takes the rows" % what)
+    m, kt = t.shape
+    if kt != k:
+        raise ValueError("%s must be [M, %d]" % (what, k))
+    return m
+
+
+def _weights(weights, rows, n, dev):
+    if weights is None:
+        return 0
+    if weights.shape != rows.shape:
         raise ValueError("weights must have the shape of rows")
-    return _vector(weights, rows.numel(), "weights")
+    return _list(weights, _F32, n, dev, "weights")
 
 
 def fp8_experts_combine(x, rows, weights, out, *, residual=None, stream=None):
     """out[t] = residual[t] + sum_s weights[t, s] x[rows[t, s]] (weights None:
     ones, the gradient of fp8_experts_gather).  x [M, K], out and residual
     [T, K]: bf16 or fp32."""
+    dev = _get_device()
     t, s = rows.shape
     m, k = x.shape
-    _here(x, rows, weights, out, residual)
-    px, ldx = _rows(x, (m, k), x.dtype, "x")
-    pr, ldr = _rows(residual, (t, k), out.dtype, "residual")
-    po, ldo = _rows(out, (t, k), out.dtype, "out")
-    d = _pack_combine(px, _in_dt(x), ldx, _ints(rows, t * s, "rows"), _weights(weights, rows), t,
-                      s, k, m, pr, ldr, po, _in_dt(out), ldo)
-    _check("fp8_experts_combine", _c_combine(d, _on(stream)))
+    n = t * s
+    xdt, odt = _float_type(x, "x"), _float_type(out, "out")
+    px, ldx = _matrix(x, m, k, x.dtype, dev, "x")
+    po, ldo = _matrix(out, t, k, out.dtype, dev, "out")
+    pr = ldr = 0
+    if residual is not None:
+        pr, ldr = _matrix(residual, t, k, out.dtype, dev, "residual")
+    rc = _c_combine(_pack_combine(px, xdt, ldx, _list(rows, _I32, n, dev, "rows"),
+                                  _weights(weights, rows, n, dev), t, s, k, m, pr, ldr, po, odt,
+                                  ldo),
+                    _raw_stream(dev) if stream is None else _stream(stream))
+    if rc:
+        raise Fp8Error("fp8_experts_combine", rc)
 
 
 def fp8_experts_combine_backward(dy, rows, weights, *, x=None, d_weights=None, q=None, scales=None,
@@ -922,26 +974,33 @@ def fp8_experts_combine_backward(dy, rows, weights, *, x=None, d_weights=None, q
     """The gradient of fp8_experts_combine: row rows[t, s] of q (1x128-group
     codes with scales) and / or dx (bf16 or fp32) <- weights[t, s] dy[t];
     d_weights fp32 [T, S] <- <dy[t], x[rows[t, s]]> (x: what combine read)."""
+    dev = _get_device()
     t, s = rows.shape
-    k = dy.shape[1]
-    _here(dy, rows, weights, x, d_weights, q, scales, dx)
-    grouped = q if q is not None else dx if dx is not None else x
-    if grouped is None or (d_weights is not None and x is None):
-        raise ValueError("q, dx or d_weights (with x) takes the gradient")
-    m = _grouped_rows(grouped, k, "q, dx and x")
-    pdy, ldy = _rows(dy, (t, k), dy.dtype, "dy")
-    px, xdt, ldx = 0, IN_BF16, 0
+    n, k = t * s, dy.shape[1]
+    m = _grouped_rows(q if q is not None else dx if dx is not None else x, k, "q, dx or x")
+    ddt = _float_type(dy, "dy")
+    pdy, ldy = _matrix(dy, t, k, dy.dtype, dev, "dy")
+    px = ldx = pdx = lddx = pq = ps = pdw = 0
+    xdt = dxdt = IN_BF16
     if x is not None:
-        (px, ldx), xdt = _rows(x, (m, k), x.dtype, "x"), _in_dt(x)
-    pdx, dxdt, lddx = 0, IN_BF16, 0
+        xdt = _float_type(x, "x")
+        px, ldx = _matrix(x, m, k, x.dtype, dev, "x")
+    if d_weights is not None:
+        if x is None:
+            raise ValueError("d_weights needs x")
+        pdw = _list(d_weights, _F32, n, dev, "d_weights")
     if dx is not None:
-        (pdx, lddx), dxdt = _rows(dx, (m, k), dx.dtype, "dx"), _in_dt(dx)
-    pq, ps = _group_codes(q, scales, m, k, sfmt, "q")
-    d = _pack_combine_grad(pdy, _in_dt(dy), ldy, px, xdt, ldx, _ints(rows, t * s, "rows"),
-                           _weights(weights, rows), t, s, k, m,
-                           _vector(d_weights, t * s, "d_weights"), pq, ps, fmt, sfmt, pdx, dxdt,
-                           lddx)
-    _check("fp8_experts_combine_backward", _c_combine_grad(d, _on(stream)))
+        dxdt = _float_type(dx, "dx")
+        pdx, lddx = _matrix(dx, m, k, dx.dtype, dev, "dx")
+    if q is not None or scales is not None:
+        pq, ps = _group_codes(q, scales, m, k, sfmt, dev, "q")
+    rc = _c_combine_grad(
+        _pack_combine_grad(pdy, ddt, ldy, px, xdt, ldx, _list(rows, _I32, n, dev, "rows"),
+                           _weights(weights, rows, n, dev), t, s, k, m, pdw, pq, ps, fmt, sfmt,
+                           pdx, dxdt, lddx),
+        _raw_stream(dev) if stream is None else _stream(stream))
+    if rc:
+        raise Fp8Error("fp8_experts_combine_backward", rc)
 
 
 def fp8_act_checkpoint(h, u, act, q, *, fmt=E4M3, scale=None, amax_out=None, scales=None,
@@ -952,35 +1011,50 @@ def fp8_act_checkpoint(h, u, act, q, *, fmt=E4M3, scale=None, amax_out=None, sca
     neither) <- the checkpoints of h and u: E4M3 codes with 1x128-group scales
     of keep_sfmt; out: a in bf16.  valid_rows: device int32, rows from it on
     are left alone."""
-    shape = h.shape
-    m, n = shape
-    _here(h, u, q, scale, amax_out, scales, h_q, h_scales, u_q, u_scales, out, valid_rows)
-    if (scale is None) == (scales is None):
-        raise ValueError("one of scale and scales selects the quantization")
-    ph, ldh = _rows(h, shape, _BF16, "h")
-    pu, ldu = _rows(u, shape, _BF16, "u")
-    po, ldo = _rows(out, shape, _BF16, "out")
+    dev = _get_device()
+    m, n = h.shape
+    ph, ldh = _matrix(h, m, n, _BF16, dev, "h")
+    pu = ldu = po = ldo = ps = psc = pa = phq = phs = puq = pus = pv = 0
+    if u is not None:
+        pu, ldu = _matrix(u, m, n, _BF16, dev, "u")
     if scale is not None:
-        mode, pq, ps = NORM_TENSOR, _codes(q, m * n, "q"), 0
-    else:
+        if scales is not None:
+            raise ValueError("one of scale and scales selects the quantization")
+        mode, psc = NORM_TENSOR, _list(scale, _F32, 1, dev, "scale")
+        if (q.element_size() != 1 or q.numel() != m * n or q.get_device() != dev
+                or not q.is_contiguous()):
+            raise ValueError("q must hold %d contiguous one-byte codes on the current device"
+                             % (m * n))
+        pq = q.data_ptr()
+        if amax_out is not None:
+            pa = _list(amax_out, _F32, 1, dev, "amax_out")
+    elif scales is not None:
         mode = NORM_GROUP
-        pq, ps = _group_codes(q, scales, m, n, sfmt, "q")
-    phq, phs = _group_codes(h_q, h_scales, m, n, keep_sfmt, "h_q")
-    puq, pus = _group_codes(u_q, u_scales, m, n, keep_sfmt, "u_q")
-    d = _pack_act(act, ph, ldh, pu, ldu, m, n, _ints(valid_rows, 1, "valid_rows"), mode, fmt, sfmt,
-                  pq, _vector(scale, 1, "scale"), ps, _vector(amax_out, 1, "amax_out"), keep_sfmt,
-                  phq, phs, puq, pus, po, ldo)
-    _check("fp8_act_checkpoint", _c_act(d, _on(stream)))
+        pq, ps = _group_codes(q, scales, m, n, sfmt, dev, "q")
+        if amax_out is not None:
+            raise ValueError("amax_out goes with scale")
+    else:
+        raise ValueError("one of scale and scales selects the quantization")
+    if h_q is not None or h_scales is not None:
+        phq, phs = _group_codes(h_q, h_scales, m, n, keep_sfmt, dev, "h_q")
+    if u_q is not None or u_scales is not None:
+        puq, pus = _group_codes(u_q, u_scales, m, n, keep_sfmt, dev, "u_q")
+    if out is not None:
+        po, ldo = _matrix(out, m, n, _BF16, dev, "out")
+    if valid_rows is not None:
+        pv = _list(valid_rows, _I32, 1, dev, "valid_rows")
+    rc = _c_act(_pack_act(act, ph, ldh, pu, ldu, m, n, pv, mode, fmt, sfmt, pq, psc, ps, pa,
+                          keep_sfmt, phq, phs, puq, pus, po, ldo),
+                _raw_stream(dev) if stream is None else _stream(stream))
+    if rc:
+        raise Fp8Error("fp8_act_checkpoint", rc)
 
 
-def _code_rows(t, shape, what):
-    """(device pointer, row pitch in bytes) of one-byte codes with contiguous
-    rows (None -> NULL)."""
-    if t is None:
-        return 0, 0
+def _code_rows(t, m, n, dev, what):
+    """(device pointer, row pitch in bytes) of codes with contiguous rows."""
     if t.element_size() != 1:
         raise ValueError("%s must hold one-byte codes" % what)
-    return _rows(t, shape, t.dtype, what)
+    return _matrix(t, m, n, t.dtype, dev, what)
 
 
 def fp8_act_checkpoint_backward(da, act, h_q, h_scales, u_q=None, u_scales=None, *,
@@ -992,38 +1066,56 @@ def fp8_act_checkpoint_backward(da, act, h_q, h_scales, u_q=None, u_scales=None,
     checkpoints (u_q None: no gate): codes dh_q, du_q of one row pitch, per
     tensor (scale_dh, scale_du, amaxes) or per 1x128 group (dh_scales,
     du_scales, sfmt), and / or dh, du in bf16 (of one row pitch)."""
-    shape = da.shape
-    m, n = shape
-    _here(da, h_q, h_scales, u_q, u_scales, dh_q, du_q, scale_dh, scale_du, amax_dh, amax_du,
-          dh_scales, du_scales, dh, du, valid_rows)
-    group = dh_scales is not None or du_scales is not None
-    if group and (scale_dh is not None or scale_du is not None):
-        raise ValueError("scales per tensor or per group, not both")
-    pda, ldda = _rows(da, shape, _BF16, "da")
-    phq, phs = _group_codes(h_q, h_scales, m, n, keep_sfmt, "h_q")
-    puq, pus = _group_codes(u_q, u_scales, m, n, keep_sfmt, "u_q")
-    pqh, ldqh = _code_rows(dh_q, shape, "dh_q")
-    pqu, ldqu = _code_rows(du_q, shape, "du_q")
-    pdh, ldh = _rows(dh, shape, _BF16, "dh")
-    pdu, ldu = _rows(du, shape, _BF16, "du")
-    if (pqh and pqu and ldqh != ldqu) or (pdh and pdu and ldh != ldu):
-        raise ValueError("dh and du must have one row pitch")
-    psh = psu = 0
-    if group:
-        count, size = (n + 127) // 128 * m, 4 if sfmt == SCALE_F32 else 1
+    dev = _get_device()
+    m, n = da.shape
+    pda, ldda = _matrix(da, m, n, _BF16, dev, "da")
+    phq, phs = _group_codes(h_q, h_scales, m, n, keep_sfmt, dev, "h_q")
+    puq = pus = pqh = pqu = ldq = psh = psu = psch = pscu = pah = pau = pdh = pdu = ldd = pv = 0
+    if u_q is not None or u_scales is not None:
+        puq, pus = _group_codes(u_q, u_scales, m, n, keep_sfmt, dev, "u_q")
+    if dh_q is not None:
+        pqh, ldq = _code_rows(dh_q, m, n, dev, "dh_q")
+    if du_q is not None:
+        pqu, ld = _code_rows(du_q, m, n, dev, "du_q")
+        if dh_q is not None and ld != ldq:
+            raise ValueError("dh_q and du_q must have one row pitch")
+        ldq = ld
+    if dh_scales is not None or du_scales is not None:
+        mode = NORM_GROUP
+        if (scale_dh is not None or scale_du is not None or amax_dh is not None
+                or amax_du is not None):
+            raise ValueError("scales per tensor or per group, not both")
         if (dh_q is None) != (dh_scales is None) or (du_q is None) != (du_scales is None):
             raise ValueError("codes need their scales, and they them")
         if dh_q is not None:
-            psh = _scales(dh_scales, count, size, "dh_scales")
+            psh = _group_scales(dh_scales, m, n, sfmt, dev, "dh_q")
         if du_q is not None:
-            psu = _scales(du_scales, count, size, "du_scales")
-    d = _pack_act_ckpt_grad(act, pda, ldda, phq, phs, puq, pus, keep_sfmt, m, n,
-                            _ints(valid_rows, 1, "valid_rows"), NORM_GROUP if group else NORM_TENSOR,
-                            fmt, sfmt, pqh, pqu, ldqh or ldqu, _vector(scale_dh, 1, "scale_dh"),
-                            _vector(scale_du, 1, "scale_du"), psh, psu,
-                            _vector(amax_dh, 1, "amax_dh"), _vector(amax_du, 1, "amax_du"), pdh,
-                            pdu, ldh or ldu)
-    _check("fp8_act_checkpoint_backward", _c_act_grad(d, _on(stream)))
+            psu = _group_scales(du_scales, m, n, sfmt, dev, "du_q")
+    else:
+        mode = NORM_TENSOR
+        if scale_dh is not None:
+            psch = _list(scale_dh, _F32, 1, dev, "scale_dh")
+        if scale_du is not None:
+            pscu = _list(scale_du, _F32, 1, dev, "scale_du")
+        if amax_dh is not None:
+            pah = _list(amax_dh, _F32, 1, dev, "amax_dh")
+        if amax_du is not None:
+            pau = _list(amax_du, _F32, 1, dev, "amax_du")
+    if dh is not None:
+        pdh, ldd = _matrix(dh, m, n, _BF16, dev, "dh")
+    if du is not None:
+        pdu, ld = _matrix(du, m, n, _BF16, dev, "du")
+        if dh is not None and ld != ldd:
+            raise ValueError("dh and du must have one row pitch")
+        ldd = ld
+    if valid_rows is not None:
+        pv = _list(valid_rows, _I32, 1, dev, "valid_rows")
+    rc = _c_act_grad(
+        _pack_act_ckpt_grad(act, pda, ldda, phq, phs, puq, pus, keep_sfmt, m, n, pv, mode, fmt,
+                            sfmt, pqh, pqu, ldq, psch, pscu, psh, psu, pah, pau, pdh, pdu, ldd),
+        _raw_stream(dev) if stream is None else _stream(stream))
+    if rc:
+        raise Fp8Error("fp8_act_checkpoint_backward", rc)
 
 
 def fp8_get_last_device_error(stream=None):
