@@ -323,7 +323,7 @@ __global__ void __launch_bounds__(256, 3) experts_gather_kernel(const GatherArgs
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           if (row[j] < 0 || !in) continue;
-          if (a.q != nullptr) *reinterpret_cast<uint4 *>(a.q + row[j] * a.K + k) = c;
+          if (a.q != nullptr) __stcs(reinterpret_cast<uint4 *>(a.q + row[j] * a.K + k), c);
           if constexpr (!kCodes)
             if (a.out != nullptr) v.store(static_cast<T *>(a.out) + row[j] * a.ld_out + k);
         }
@@ -371,21 +371,27 @@ constexpr int rows_per_step() {
   return sizeof(T) == 2 ? 8 : 4;
 }
 
-// 256 elements of a row: lane l's eight.  fp32: the row's 64 vectors go out as
-// whole sectors (lane l copies vectors l and l + 32); vector e sits in half e & 1
-// at column (e / 2) ^ 4 (e & 1), free of bank conflicts both ways.
+// 256 elements of a row, of which the first `left` exist: lane l's eight.  fp32:
+// the row's 64 vectors go out as whole sectors (lane l copies vectors l and
+// l + 32); vector e sits in half e & 1 at column (e / 2) ^ 4 (e & 1), free of bank
+// conflicts both ways.
 template <typename T>
-__device__ __forceinline__ void copy_row_async(uint8_t *slot, const T *src, int32_t left, bool real) {
-  const int32_t l = (int32_t)lane_id();
-  uint4 *dst = reinterpret_cast<uint4 *>(slot);
-  if constexpr (sizeof(T) == 2) {
-    copy16_async(dst + l, src + 8 * l, real && 8 * l < left);
-  } else {
-    const int32_t at = 32 * (l & 1) + ((l >> 1) ^ (4 * (l & 1)));
-    copy16_async(dst + at, src + 4 * l, real && 4 * l < left);
-    copy16_async(dst + at + 16, src + 4 * l + 128, real && 4 * l + 128 < left);
+struct RowCopy {
+  uint32_t dst, bytes, bytes2;  // this lane's place in a slot, and what it copies
+  int64_t offset;               // in bytes from the row's first column
+  __device__ __forceinline__ RowCopy(uint32_t ring, int64_t k0, int32_t left) {
+    const int32_t l = (int32_t)lane_id(), per = 16 / (int32_t)sizeof(T);
+    dst = ring + 16 * (sizeof(T) == 2 ? l : 32 * (l & 1) + ((l >> 1) ^ (4 * (l & 1))));
+    bytes = per * l < left ? 16u : 0u;
+    bytes2 = per * (l + 32) < left ? 16u : 0u;
+    offset = k0 * (int64_t)sizeof(T) + 16 * l;
   }
-}
+  // into the slot at `slot` bytes of the ring, from the row at src + offset
+  __device__ __forceinline__ void operator()(int slot, const char *src, bool real) const {
+    copy16_async(dst + slot, src, real ? bytes : 0u);
+    if constexpr (sizeof(T) == 4) copy16_async(dst + slot + 256, src + 512, real ? bytes2 : 0u);
+  }
+};
 template <typename T>
 __device__ __forceinline__ Raw8<T> ring_row(const uint8_t *slot) {
   const uint32_t l = lane_id();
@@ -396,24 +402,30 @@ __device__ __forceinline__ Raw8<T> ring_row(const uint8_t *slot) {
   return r;
 }
 
-// Row and weight of choice s0 + j of token t on the lanes with l % C == j (a
-// dropped pair, and what lies behind the last: no row, weight zero).
+// The rows and weights of choices s0 .. s0 + C - 1 of a token, choice j's on the
+// lanes with l % C == j (without a row: -1 and weight zero).
 template <int C>
-__device__ __forceinline__ void load_choice(const int32_t *rows, const float *weights, int64_t t,
-                                            int64_t s0, int64_t T, int64_t S, int64_t M,
-                                            int32_t &row, float &wt) {
-  const int64_t s = s0 + (lane_id() & (uint32_t)(C - 1));
-  row = -1;
-  wt = 0.0f;
-  if (t < T && s < S) {
-    const int32_t r = rows[t * S + s];
-    const float v = weights != nullptr ? weights[t * S + s] : 1.0f;
-    if (r >= 0 && r < M) {
-      row = r;
-      wt = v;
+struct Choices {
+  int32_t row;
+  float wt;
+  __device__ __forceinline__ void load(const int32_t *rows, const float *weights, int64_t t,
+                                       int32_t s0, int64_t T, int32_t S, int64_t M) {
+    const int32_t s = s0 + (int32_t)(lane_id() & (uint32_t)(C - 1));
+    int32_t r = -1;
+    float v = 1.0f;
+    if (t < T && s < S) {
+      r = rows[t * S + s];
+      if (weights != nullptr) v = weights[t * S + s];
     }
+    const bool has = r >= 0 && r < M;
+    row = has ? r : -1;
+    wt = has ? v : 0.0f;
   }
-}
+  // bit j: choice j has a row
+  __device__ __forceinline__ uint32_t kept() const {
+    return __ballot_sync(0xffffffffu, row >= 0) & ((1u << C) - 1u);
+  }
+};
 
 constexpr int kRingWarps = 8;  // of a CTA
 
@@ -430,14 +442,16 @@ __global__ void __launch_bounds__(32 * kRingWarps, 3) experts_combine_kernel(con
   constexpr int kC = rows_per_step<T>(), kRow = 256 * sizeof(T), kStage = combine_stage<T, O>();
   extern __shared__ __align__(16) uint8_t smem[];
   uint8_t *ring = smem + (threadIdx.x >> 5) * (2 * kStage);
+  const uint32_t ring_at = smem_u32(ring);
   launch_dependents();
   grid_dependency_wait();
-  const T *x = static_cast<const T *>(a.x);
   const O *res = static_cast<const O *>(a.residual);
+  const int32_t S = (int32_t)a.S;
+  const uint32_t pitch = (uint32_t)a.ldx * (uint32_t)sizeof(T);
   struct Step {
     TaskWalk w;
-    int64_t s0;
-    __device__ __forceinline__ void next(int64_t S) {
+    int32_t s0;
+    __device__ __forceinline__ void next(int32_t S) {
       s0 += kC;
       if (s0 >= S) {
         s0 = 0;
@@ -445,45 +459,48 @@ __global__ void __launch_bounds__(32 * kRingWarps, 3) experts_combine_kernel(con
       }
     }
   };
-  auto fetch = [&](const Step &s, int32_t row, int stage) {
+  auto fetch = [&](const Step &s, const Choices<kC> &c, int stage) {
     if (s.w.t < a.T) {
       const int64_t k0 = (int64_t)s.w.win * 256;
-      const int32_t left = (int32_t)min((int64_t)256, a.K - k0);
-      uint8_t *slot = ring + stage * kStage;
-      const int n = (int)min((int64_t)kC, a.S - s.s0);
+      const int32_t left = (int32_t)min((int64_t)256, a.K - k0), n = min(kC, S - s.s0);
+      const uint32_t kept = c.kept();
+      const RowCopy<T> copy(ring_at + stage * kStage, k0, left);
+      const char *x = static_cast<const char *>(a.x) + copy.offset;
 #pragma unroll
       for (int j = 0; j < kC; ++j) {
-        const int64_t r = __shfl_sync(0xffffffffu, row, j);
-        if (j < n)  // (a place that may be read, but is not, for a row that does not exist)
-          copy_row_async(slot + j * kRow, r >= 0 ? x + r * a.ldx + k0 : static_cast<const T *>(a.out),
-                         left, r >= 0);
+        const uint32_t r = (uint32_t)max(__shfl_sync(0xffffffffu, c.row, j), 0);
+        if (j < n) copy(j * kRow, x + (uint64_t)r * pitch, kept >> j & 1u);
       }
-      if (res != nullptr && a.S <= kC)
-        copy_row_async(slot + kC * kRow, res + s.w.t * a.ldr + k0, left, true);
+      if (res != nullptr && S <= kC) {
+        const RowCopy<O> copy_res(ring_at + stage * kStage, k0, left);
+        copy_res(kC * kRow, reinterpret_cast<const char *>(res + s.w.t * a.ldr) + copy_res.offset, true);
+      }
     }
     copies_commit();
   };
+  auto choices = [&](const Step &s, Choices<kC> &c) {
+    c.load(a.rows, a.weights, s.w.t, s.s0, a.T, S, a.M);
+  };
   Step cur{TaskWalk(a.K, 256), 0};
-  int32_t row_next;
-  float w_cur, w_next;
-  load_choice<kC>(a.rows, a.weights, cur.w.t, 0, a.T, a.S, a.M, row_next, w_cur);
-  fetch(cur, row_next, 0);
+  Choices<kC> c_cur, c_next;
+  choices(cur, c_cur);
+  fetch(cur, c_cur, 0);
   Step nxt = cur;
-  nxt.next(a.S);
-  load_choice<kC>(a.rows, a.weights, nxt.w.t, nxt.s0, a.T, a.S, a.M, row_next, w_next);
+  nxt.next(S);
+  choices(nxt, c_next);
   F2 acc[4];
   for (int stage = 0; cur.w.t < a.T; stage ^= 1) {
     __syncwarp();  // the other lanes have read what this overwrites
-    fetch(nxt, row_next, stage ^ 1);
+    fetch(nxt, c_next, stage ^ 1);
     Step behind = nxt;
-    behind.next(a.S);
-    const float w_l = w_cur;
-    w_cur = w_next;
-    load_choice<kC>(a.rows, a.weights, behind.w.t, behind.s0, a.T, a.S, a.M, row_next, w_next);
+    behind.next(S);
+    const float w_l = c_cur.wt;
+    c_cur = c_next;
+    choices(behind, c_next);
     copies_wait<1>();
     __syncwarp();
     const uint8_t *slot = ring + stage * kStage;
-    const int n = (int)min((int64_t)kC, a.S - cur.s0);
+    const int32_t n = min(kC, S - cur.s0);
 #pragma unroll
     for (int j = 0; j < kC; ++j) {
       const F2 wt(__shfl_sync(0xffffffffu, w_l, j));
@@ -493,19 +510,15 @@ __global__ void __launch_bounds__(32 * kRingWarps, 3) experts_combine_kernel(con
         for (int i = 0; i < 4; ++i) acc[i] = fma2(wt, raw_pair(v, i), acc[i]);
       }
     }
-    if (a.S <= kC) {  // the residual is in this step's stage
-      if (res != nullptr) {
-        const Raw8<O> r = ring_row<O>(slot + kC * kRow);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[i] = acc[i] + raw_pair(r, i);
-      }
-    }
-    if (cur.s0 + kC >= a.S) {
+    if (cur.s0 + kC >= S) {
       const int64_t k = (int64_t)cur.w.win * 256 + lane_id() * 8;
       if (k < a.K) {
-        if (a.S > kC && res != nullptr) {  // (longer lists: its stage has gone)
+        if (res != nullptr) {
           Raw8<O> r;
-          r.load_stream(res + cur.w.t * a.ldr + k);
+          if (S <= kC)
+            r = ring_row<O>(slot + kC * kRow);
+          else  // (a longer list has other stages behind the first)
+            r.load_stream(res + cur.w.t * a.ldr + k);
 #pragma unroll
           for (int i = 0; i < 4; ++i) acc[i] = acc[i] + raw_pair(r, i);
         }
@@ -562,72 +575,73 @@ __global__ void __launch_bounds__(32 * kRingWarps, 3)
   grid_dependency_wait();
   const uint32_t l = lane_id(), w = threadIdx.x >> 5, nw = blockDim.x >> 5;
   uint8_t *ring = smem + w * (2 * kStage);
+  const uint32_t ring_at = smem_u32(ring);
   const DY *dy = static_cast<const DY *>(a.dy);
-  const X *x = static_cast<const X *>(a.x);
-  const int32_t wins = (int32_t)((a.K + 255) / 256);
+  const int32_t wins = (int32_t)((a.K + 255) / 256), S = (int32_t)a.S;
+  const uint32_t pitch = (uint32_t)a.ldx * (uint32_t)sizeof(X), K = (uint32_t)a.K;
   struct Step {
-    int64_t t, s0;
-    int32_t win;
-    __device__ __forceinline__ void next(int32_t wins, int32_t w, int32_t nw, int64_t S) {
+    int64_t t;
+    int32_t s0, win;
+    // true: another list of choices
+    __device__ __forceinline__ bool next(int32_t wins, int32_t w, int32_t nw, int32_t S) {
       win += nw;
-      if (win >= wins) {
-        win = w;
-        s0 += kC;
-        if (s0 >= S) {
-          s0 = 0;
-          t += gridDim.x;
-        }
+      if (win < wins) return false;
+      win = w;
+      s0 += kC;
+      if (s0 >= S) {
+        s0 = 0;
+        t += gridDim.x;
       }
+      return true;
     }
   };
-  auto fetch = [&](const Step &s, int32_t row, int stage) {
+  auto fetch = [&](const Step &s, const Choices<kC> &c, int stage) {
     if (s.t < a.T) {
       const int64_t k0 = (int64_t)s.win * 256;
       const int32_t left = (int32_t)min((int64_t)256, a.K - k0);
-      uint8_t *slot = ring + stage * kStage;
-      const DY *d = dy + s.t * a.ld_dy + k0;
-      copy_row_async(slot + kC * kRow, d, left, true);
-      if (a.dw != nullptr) {
-        const int n = (int)min((int64_t)kC, a.S - s.s0);
+      const RowCopy<DY> copy_dy(ring_at + stage * kStage, k0, left);
+      copy_dy(kC * kRow, reinterpret_cast<const char *>(dy + s.t * a.ld_dy) + copy_dy.offset, true);
+      if (a.dw != nullptr && a.M > 0) {
+        const int32_t n = min(kC, S - s.s0);
+        const uint32_t kept = c.kept();
+        const RowCopy<X> copy(ring_at + stage * kStage, k0, left);
+        const char *x = static_cast<const char *>(a.x) + copy.offset;
 #pragma unroll
         for (int j = 0; j < kC; ++j) {
-          const int64_t r = __shfl_sync(0xffffffffu, row, j);
-          if (j < n)  // (a place that may be read, but is not, for a row that does not exist)
-            copy_row_async(slot + j * kRow, r >= 0 ? x + r * a.ldx + k0 : reinterpret_cast<const X *>(dy),
-                           left, r >= 0);
+          const uint32_t r = (uint32_t)max(__shfl_sync(0xffffffffu, c.row, j), 0);
+          if (j < n) copy(j * kRow, x + (uint64_t)r * pitch, kept >> j & 1u);
         }
       }
     }
     copies_commit();
   };
+  auto choices = [&](const Step &s, Choices<kC> &c) {
+    c.load(a.rows, a.weights, s.t, s.s0, a.T, S, a.M);
+  };
   Step cur{(int64_t)blockIdx.x, 0, (int32_t)w};
-  int32_t row_cur, row_next;
-  float w_cur, w_next;
-  load_choice<kC>(a.rows, a.weights, cur.t, 0, a.T, a.S, a.M, row_cur, w_cur);
-  fetch(cur, row_cur, 0);
+  Choices<kC> c_cur, c_next;
+  choices(cur, c_cur);
+  fetch(cur, c_cur, 0);
   Step nxt = cur;
-  nxt.next(wins, (int32_t)w, (int32_t)nw, a.S);
-  load_choice<kC>(a.rows, a.weights, nxt.t, nxt.s0, a.T, a.S, a.M, row_next, w_next);
-  float dot[kC];
-#pragma unroll
-  for (int j = 0; j < kC; ++j) dot[j] = 0.0f;
+  c_next = c_cur;
+  if (nxt.next(wins, (int32_t)w, (int32_t)nw, S)) choices(nxt, c_next);
+  F2 dot[kC];
   int phase = 0;
   for (int stage = 0; cur.t < a.T; stage ^= 1) {
     __syncwarp();  // the other lanes have read what this overwrites
-    fetch(nxt, row_next, stage ^ 1);
+    fetch(nxt, c_next, stage ^ 1);
     Step behind = nxt;
-    behind.next(wins, (int32_t)w, (int32_t)nw, a.S);
-    const int32_t row_l = row_cur;
-    const float w_l = w_cur;
-    row_cur = row_next;
-    w_cur = w_next;
-    load_choice<kC>(a.rows, a.weights, behind.t, behind.s0, a.T, a.S, a.M, row_next, w_next);
+    const bool fresh = behind.next(wins, (int32_t)w, (int32_t)nw, S);
+    const int32_t row_l = c_cur.row;
+    const float w_l = c_cur.wt;
+    const uint32_t kept = c_cur.kept();
+    c_cur = c_next;
+    if (fresh) choices(behind, c_next);
     copies_wait<1>();
     __syncwarp();
     const uint8_t *slot = ring + stage * kStage;
-    const int64_t k = (int64_t)cur.win * 256 + l * 8, g = k >> 7;
-    const bool in = k < a.K;
-    const int n = (int)min((int64_t)kC, a.S - cur.s0);
+    const uint32_t k = (uint32_t)cur.win * 256 + l * 8, g = k >> 7;
+    const bool in = k < K;
     const Raw8<DY> raw = ring_row<DY>(slot + kC * kRow);
     F2 v[4];
 #pragma unroll
@@ -643,11 +657,12 @@ __global__ void __launch_bounds__(32 * kRingWarps, 3)
       const bool fast = __all_sync(
           0xffffffffu, gs.fast && (w_l == 0.0f || (fabsf(f_l) >= 0x1p-100f && fabsf(f_l) <= 0x1p100f)));
       if (!fast) gs = group_scale_any<F>(amax, a.sfmt);
-      if (row_l >= 0 && (l & 15u) < (uint32_t)kC && 128 * g < a.K)
-        store_scale(a.scales, g * a.M + row_l, gs.stored, a.sfmt);
+      if (row_l >= 0 && (l & 15u) < (uint32_t)kC && 128 * g < K)
+        store_scale(a.scales, (int64_t)g * a.M + row_l, gs.stored, a.sfmt);
+      uint8_t *q = a.q + k;
 #pragma unroll
       for (int j = 0; j < kC; ++j) {
-        const int64_t row = __shfl_sync(0xffffffffu, row_l, j);
+        const uint32_t row = (uint32_t)__shfl_sync(0xffffffffu, row_l, j);
         const int from = (int)(l & 16u) | j;
         uint2 c;
         if (fast) {
@@ -659,7 +674,7 @@ __global__ void __launch_bounds__(32 * kRingWarps, 3)
           c = make_uint2(codes4_ieee<F>((v[0] * wj).v, (v[1] * wj).v, s),
                          codes4_ieee<F>((v[2] * wj).v, (v[3] * wj).v, s));
         }
-        if (row >= 0 && in) *reinterpret_cast<uint2 *>(a.q + row * a.K + k) = c;
+        if ((kept >> j & 1u) && in) *reinterpret_cast<uint2 *>(q + (uint64_t)row * K) = c;
       }
     }
     if (a.dx != nullptr) {
@@ -676,42 +691,45 @@ __global__ void __launch_bounds__(32 * kRingWarps, 3)
       }
     }
     if (a.dw != nullptr) {
+      const int32_t n = min(kC, S - cur.s0);
 #pragma unroll
       for (int j = 0; j < kC; ++j) {
-        if (j >= n) continue;
+        if (j >= n || a.M == 0) continue;
         const Raw8<X> xv = ring_row<X>(slot + j * kRow);
-        F2 d2(0.0f);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) d2 = fma2(v[i], raw_pair(xv, i), d2);
-        float d0, d1;
-        d2.get(d0, d1);
-        dot[j] += d0 + d1;
+        for (int i = 0; i < 4; ++i) dot[j] = fma2(v[i], raw_pair(xv, i), dot[j]);
       }
       if (cur.win + (int32_t)nw >= wins) {  // this warp's last columns of these rows
+        float d[kC];
+#pragma unroll
+        for (int j = 0; j < kC; ++j) {
+          float d0, d1;
+          dot[j].get(d0, d1);
+          d[j] = d0 + d1;
+          dot[j] = F2(0.0f);
+        }
         // halves apart, quarters apart, ...: lane l ends with row l / (32 / kC)
 #pragma unroll
         for (int h = kC / 2; h > 0; h >>= 1) {
           const uint32_t apart = (uint32_t)(32 / kC * h);
 #pragma unroll
           for (int j = 0; j < h; ++j) {
-            const float keep = l & apart ? dot[j + h] : dot[j], give = l & apart ? dot[j] : dot[j + h];
-            dot[j] = keep + __shfl_xor_sync(0xffffffffu, give, (int)apart);
+            const float keep = l & apart ? d[j + h] : d[j], give = l & apart ? d[j] : d[j + h];
+            d[j] = keep + __shfl_xor_sync(0xffffffffu, give, (int)apart);
           }
         }
-        float d = dot[0];
+        float sum = d[0];
 #pragma unroll
-        for (int o = 16 / kC; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+        for (int o = 16 / kC; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         // (a buffer is written again two barriers after it was read)
-        if (l % (32 / kC) == 0) part[phase][w][l / (32 / kC)] = d;
+        if (l % (32 / kC) == 0) part[phase][w][l / (32 / kC)] = sum;
         __syncthreads();
         if ((int)threadIdx.x < n) {
-          float sum = 0.0f;
-          for (uint32_t i = 0; i < nw; ++i) sum += part[phase][i][threadIdx.x];
-          a.dw[cur.t * a.S + cur.s0 + threadIdx.x] = sum;
+          float all = 0.0f;
+          for (uint32_t i = 0; i < nw; ++i) all += part[phase][i][threadIdx.x];
+          a.dw[cur.t * S + cur.s0 + threadIdx.x] = all;
         }
         phase ^= 1;
-#pragma unroll
-        for (int j = 0; j < kC; ++j) dot[j] = 0.0f;
       }
     }
     cur = nxt;

@@ -42,6 +42,12 @@ int check_rows(const void *p, int64_t ld, int64_t cols) {
   return aligned_to(p, 16) && ld % 8 == 0 ? FP8_OK : FP8_ERR_MISALIGNED;
 }
 
+// The same for the expert-row calls, whose kernels keep a row's bytes in 32 bits.
+int check_expert_rows(const void *p, int64_t ld, int64_t cols) {
+  const int rc = check_rows(p, ld, cols);
+  return rc == FP8_OK && p != nullptr && ld >= kMaxDim / 2 ? FP8_ERR_UNSUPPORTED : rc;
+}
+
 // The sizes of the expert-row calls.
 int check_tokens(int64_t T, int64_t S, int64_t K, int64_t M, const int32_t *rows) {
   if (T < 0 || S < 1 || K < 1 || M < 0) return FP8_ERR_INVALID_ARG;
@@ -89,8 +95,8 @@ int fp8_experts_gather(const fp8_experts_gather_t *gather, fp8_stream_t stream) 
     if (codes && (n.x_scales == nullptr || n.q == nullptr)) return FP8_ERR_INVALID_ARG;
     if (n.q == nullptr && n.out == nullptr) return FP8_ERR_INVALID_ARG;
   }
-  if (!codes && (rc = check_rows(n.x, n.ld_x, n.K)) != FP8_OK) return rc;
-  if ((rc = check_rows(n.out, n.ld_out, n.K)) != FP8_OK) return rc;
+  if (!codes && (rc = check_expert_rows(n.x, n.ld_x, n.K)) != FP8_OK) return rc;
+  if ((rc = check_expert_rows(n.out, n.ld_out, n.K)) != FP8_OK) return rc;
   if (!aligned_to(n.xq, 16) || !aligned_to(n.q, 16) || !scales_aligned(n.scales, n.sfmt) ||
       !scales_aligned(n.x_scales, n.sfmt))
     return FP8_ERR_MISALIGNED;
@@ -116,9 +122,9 @@ int fp8_experts_combine(const fp8_experts_combine_t *combine, fp8_stream_t strea
   if (rc != FP8_OK) return rc;
   if (!valid_in(n.x_dt) || !valid_in(n.out_dt)) return FP8_ERR_INVALID_ARG;
   if (n.T > 0 && (n.out == nullptr || (n.M > 0 && n.x == nullptr))) return FP8_ERR_INVALID_ARG;
-  if ((rc = check_rows(n.x, n.ld_x, n.K)) != FP8_OK) return rc;
-  if ((rc = check_rows(n.residual, n.ld_residual, n.K)) != FP8_OK) return rc;
-  if ((rc = check_rows(n.out, n.ld_out, n.K)) != FP8_OK) return rc;
+  if ((rc = check_expert_rows(n.x, n.ld_x, n.K)) != FP8_OK) return rc;
+  if ((rc = check_expert_rows(n.residual, n.ld_residual, n.K)) != FP8_OK) return rc;
+  if ((rc = check_expert_rows(n.out, n.ld_out, n.K)) != FP8_OK) return rc;
   // in place each element is read before it is written, at the same place
   if (n.residual != nullptr && n.residual == n.out && n.ld_residual != n.ld_out)
     return FP8_ERR_INVALID_ARG;
@@ -147,9 +153,9 @@ int fp8_experts_combine_backward(const fp8_experts_combine_grad_t *grad, fp8_str
     if (n.d_weights != nullptr && n.M > 0 && n.x == nullptr) return FP8_ERR_INVALID_ARG;
     if (n.q == nullptr && n.dx == nullptr && n.d_weights == nullptr) return FP8_ERR_INVALID_ARG;
   }
-  if ((rc = check_rows(n.dy, n.ld_dy, n.K)) != FP8_OK) return rc;
-  if ((rc = check_rows(n.x, n.ld_x, n.K)) != FP8_OK) return rc;
-  if ((rc = check_rows(n.dx, n.ld_dx, n.K)) != FP8_OK) return rc;
+  if ((rc = check_expert_rows(n.dy, n.ld_dy, n.K)) != FP8_OK) return rc;
+  if ((rc = check_expert_rows(n.x, n.ld_x, n.K)) != FP8_OK) return rc;
+  if ((rc = check_expert_rows(n.dx, n.ld_dx, n.K)) != FP8_OK) return rc;
   if (!aligned_to(n.weights, 4) || !aligned_to(n.d_weights, 4) || !aligned_to(n.q, 16) ||
       !scales_aligned(n.scales, n.sfmt))
     return FP8_ERR_MISALIGNED;

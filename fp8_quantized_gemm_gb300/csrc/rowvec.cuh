@@ -77,10 +77,9 @@ __device__ __forceinline__ uint4 pack16(const F2 (&y)[8]) {
 }
 
 // Asynchronous 16-byte copies to shared memory.
-__device__ __forceinline__ void copy16_async(uint4 *dst, const void *src, bool in) {
-  const uint32_t bytes = in ? 16u : 0u;  // 0: sixteen zero bytes, nothing is read
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src),
-               "r"(bytes)
+// (bytes 16, or 0: sixteen zero bytes, nothing is read)
+__device__ __forceinline__ void copy16_async(uint32_t dst, const void *src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
                : "memory");
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }

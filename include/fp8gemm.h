@@ -719,8 +719,9 @@ FP8_API int fp8_rmsnorm_backward(const fp8_rmsnorm_grad_t *grad, fp8_stream_t st
  *   M      rows of the grouped side, e.g. T * S; rows that no pair owns are
  *          left as they were.
  * Matrices are bf16 or fp32 (fp8_in_dtype_t) with contiguous 16-byte aligned
- * rows; pitches in elements, >= K and multiples of 8; K % 16 == 0.  Codes are
- * [M, K] contiguous, 16-byte aligned; group scales [ceil(K/128), M] of sfmt.
+ * rows; pitches in elements, >= K, multiples of 8 and below 2^30
+ * (FP8_ERR_UNSUPPORTED from there on); K % 16 == 0.  Codes are [M, K]
+ * contiguous, 16-byte aligned; group scales [ceil(K/128), M] of sfmt.
  * T == 0 or M == 0 is allowed; T * S < 2^31.  No call allocates or keeps
  * scratch; all are launched with programmatic stream serialization, as the
  * per-group calls, and give the same bits on every run.

@@ -74,7 +74,7 @@ def combine(**kw):
     (dict(x_dt=2), INVALID), (dict(out_dt=-1), INVALID), (dict(K=8, ld_x=8), MISALIGNED),
     (dict(ld_x=8), INVALID), (dict(ld_residual=260), MISALIGNED), (dict(out=P + 2), MISALIGNED),
     (dict(residual=2 * P, ld_residual=512), INVALID),  # in place, another pitch
-    (dict(weights=P + 2), MISALIGNED)])
+    (dict(weights=P + 2), MISALIGNED), (dict(ld_x=1 << 30), UNSUPPORTED)])
 def test_combine(kw, status):
     assert combine(**kw) == status
 
