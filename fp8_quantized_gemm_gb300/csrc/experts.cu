@@ -232,9 +232,10 @@ static cudaError_t run_sort(const ID *ids, int64_t P, int E, int32_t *offsets, i
   if (P <= 4096)
     return launch_serial(experts_sort_kernel<ID, true>, 1, 32 * kSortWarps, st, ids, (uint32_t)P, E,
                          offsets, rows, pairs);
+  const int ctas = widest_cluster<experts_sort_kernel<ID, false>>(kSortCluster, 32 * kSortWarps);
   const cudaError_t e =
-      launch_serial_wide_cluster<experts_sort_kernel<ID, false>>(
-          kSortCluster, 32 * kSortWarps, kSortCluster, st, ids, (uint32_t)P, E, offsets, rows, pairs);
+      launch_serial_cluster(experts_sort_kernel<ID, false>, ctas, 32 * kSortWarps, ctas, 0, st, ids,
+                            (uint32_t)P, E, offsets, rows, pairs);
   if (e != cudaSuccess || pairs == nullptr) return e;
   return launch_serial(experts_pairs_kernel, (P + 255) / 256, 256, st,
                        static_cast<const int32_t *>(rows), static_cast<const int32_t *>(offsets + E),
@@ -544,6 +545,13 @@ static cudaError_t run_combine(const CombineArgs &a, int sms, cudaStream_t st) {
 cudaError_t launch_experts_combine(const CombineArgs &a, int x_dt, int out_dt, int sms,
                                    cudaStream_t st) {
   if (a.T == 0) return cudaSuccess;
+  if (a.M == 0) {  // no row is read; the copies of no bytes have an address all the same
+    CombineArgs b = a;
+    b.x = a.out;
+    b.ldx = 0;
+    b.M = -1;
+    return launch_experts_combine(b, x_dt, out_dt, sms, st);
+  }
   if (x_dt == 0)
     return out_dt == 0 ? run_combine<__nv_bfloat16, __nv_bfloat16>(a, sms, st)
                        : run_combine<__nv_bfloat16, float>(a, sms, st);

@@ -69,6 +69,8 @@ int fp8_experts_sort(const void *ids, int id_dt, int64_t T, int64_t S, int exper
   if (T < 0 || S < 1 || T >= kMaxDim || S >= kMaxDim || T * S >= kMaxDim) return FP8_ERR_INVALID_ARG;
   if (experts < 1 || experts > fp8k::kMaxExperts) return FP8_ERR_INVALID_ARG;
   if (offsets == nullptr || (T > 0 && (ids == nullptr || rows == nullptr))) return FP8_ERR_INVALID_ARG;
+  // the ranks wait in rows while ids are read again
+  if (rows != nullptr && (rows == ids || rows == pairs || rows == offsets)) return FP8_ERR_INVALID_ARG;
   if (!aligned_to(ids, id_dt == FP8_IDS_I64 ? 8 : 4) || !aligned_to(offsets, 4) ||
       !aligned_to(rows, 4) || !aligned_to(pairs, 4))
     return FP8_ERR_MISALIGNED;

@@ -64,13 +64,34 @@ cudaError_t launch_serial_smem(int64_t blocks, int threads, int smem, cudaStream
   return launch_serial_cluster(KERN, blocks, threads, 1, smem, st, args...);
 }
 
-// In clusters of more than eight CTAs.
-template <auto KERN, typename... Args>
-cudaError_t launch_serial_wide_cluster(int64_t blocks, int threads, int cluster, cudaStream_t st,
-                                       Args... args) {
-  const cudaError_t e = allow_once<KERN, cudaFuncAttributeNonPortableClusterSizeAllowed>(1);
-  if (e != cudaSuccess) return e;
-  return launch_serial_cluster(KERN, blocks, threads, cluster, 0, st, args...);
+// `most` (more than eight) where the device can hold a cluster of that many of
+// this kernel's CTAs, else eight; asked once per device.
+template <auto KERN>
+int widest_cluster(int most, int threads) {
+  static std::atomic<uint64_t> asked{0}, wide{0};  // a bit per device
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 8;
+  const uint64_t bit = (uint64_t)1 << (dev & 63);
+  if ((asked.load(std::memory_order_acquire) & bit) == 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)most);
+    cfg.blockDim = dim3((unsigned)threads);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)most;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int held = 0;
+    if (cudaFuncSetAttribute(KERN, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+        cudaOccupancyMaxActiveClusters(&held, KERN, &cfg) == cudaSuccess && held > 0)
+      wide.fetch_or(bit, std::memory_order_relaxed);
+    else
+      (void)cudaGetLastError();
+    asked.fetch_or(bit, std::memory_order_release);
+  }
+  return wide.load(std::memory_order_relaxed) & bit ? most : 8;
 }
 
 }  // namespace fp8k

@@ -81,7 +81,7 @@ class ExpertsMLP:
         t, s = ids.shape
         m, dev, n = t * s, x.device, self.ffn
         out = torch.empty((t, self.d), dtype=torch.bfloat16, device=dev)
-        self.saved = None
+        self.saved = (None, None, weights, None, None) if keep and t == 0 else None
         if t == 0:
             return out
         offsets = torch.empty(self.E + 1, dtype=torch.int32, device=dev)
@@ -105,10 +105,12 @@ class ExpertsMLP:
 
     def backward(self, dout):
         """(dx [T, d] bf16, d_weights fp32 [T, S]) for the gradient dout [T, d]
-        of the last call with keep=True.  (The residual's gradient is dout.)"""
+        of the last call, made with keep=True.  (The residual's gradient is dout.)"""
         if self.w13t is None or self.saved is None:
             raise ValueError("backward needs ExpertsMLP(backward=True) and a call with keep=True")
         offsets, rows, weights, y, kept = self.saved
+        if rows is None:  # no tokens
+            return torch.empty_like(dout, dtype=torch.bfloat16), torch.empty_like(weights)
         m, dev, n = rows.numel(), dout.device, self.ffn
         dw = torch.empty_like(weights)
         yq, ys = self._codes(m, self.d, dev)

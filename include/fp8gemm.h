@@ -722,8 +722,9 @@ FP8_API int fp8_rmsnorm_backward(const fp8_rmsnorm_grad_t *grad, fp8_stream_t st
  * rows; pitches in elements, >= K, multiples of 8 and below 2^30
  * (FP8_ERR_UNSUPPORTED from there on); K % 16 == 0.  Codes are [M, K]
  * contiguous, 16-byte aligned; group scales [ceil(K/128), M] of sfmt.
- * T == 0 or M == 0 is allowed; T * S < 2^31.  No call allocates or keeps
- * scratch; all are launched with programmatic stream serialization, as the
+ * T == 0 or M == 0 is allowed; T * S < 2^31.  No output may overlap an input or
+ * another output but where it says so.  No call allocates or keeps scratch; all
+ * are launched with programmatic stream serialization, as the
  * per-group calls, and give the same bits on every run.
  *
  * fp8_experts_sort: rows[t,s] = number of pairs with a smaller expert + number
@@ -845,7 +846,8 @@ FP8_API int fp8_experts_combine_backward(const fp8_experts_combine_grad_t *grad,
  * and checkpoints 16-byte aligned; N % 16 == 0.  M == 0 writes only the maxima
  * (0).  A NaN argument is kept as one, and the rest of its group under a scale
  * of 1; a group that holds an infinity is kept as NaN (UE8M0 scales: the
- * infinity is kept, the rest of its group as zeros).
+ * infinity is kept, the rest of its group as zeros).  No output may overlap an
+ * input or another output.
  * Launched with programmatic stream serialization, as the per-group calls.
  *
  * fp8_act_checkpoint:
@@ -886,7 +888,7 @@ FP8_API int fp8_act_checkpoint(const fp8_act_checkpoint_t *act, fp8_stream_t str
  *           only with a gate: side by side in one [M, 2N] operand with ld_q = 2N.
  *           scale_dh, scale_du, amax_dh, amax_du (nullable, distinct) per tensor;
  *           dh_scales, du_scales per group
- *   dh, du  nullable bf16 [M, ld_d]; may not overlap da. */
+ *   dh, du  nullable bf16 [M, ld_d]. */
 typedef struct {
   int act;
   const void *da;

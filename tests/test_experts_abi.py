@@ -21,7 +21,7 @@ def call(name, s):
 
 
 def sort(**kw):
-    d = dict(ids=P, id_dt=1, T=4, S=2, experts=8, offsets=P, rows=P, pairs=P)
+    d = dict(ids=P, id_dt=1, T=4, S=2, experts=8, offsets=2 * P, rows=3 * P, pairs=4 * P)
     d.update(kw)
     return F._lib.fp8_experts_sort(*d.values(), None)
 
@@ -32,7 +32,7 @@ def sort(**kw):
     (dict(T=1 << 30, S=2), INVALID), (dict(experts=0), INVALID), (dict(experts=257), INVALID),
     (dict(ids=P + 4), MISALIGNED), (dict(id_dt=0, ids=P + 2), MISALIGNED),
     (dict(rows=P + 2), MISALIGNED), (dict(pairs=P + 1), MISALIGNED),
-    (dict(offsets=P + 2), MISALIGNED)])
+    (dict(offsets=P + 2), MISALIGNED), (dict(rows=P), INVALID), (dict(pairs=3 * P), INVALID)])
 def test_sort(kw, status):
     assert sort(**kw) == status
 

@@ -465,6 +465,49 @@ def test_captured_graphs_and_side_streams(t):
             assert torch.equal(a, b)
 
 
+FIRST = """
+import torch
+import fp8_quantized_gemm_gb300 as F
+t, s, e, k = 700, 8, 256, 1024
+ids = torch.randint(0, e, (t, s), device="cuda")
+new = lambda *sh, dt=torch.float32: torch.zeros(*sh, dtype=dt, device="cuda")
+x, w = torch.randn(t, k, device="cuda").bfloat16(), torch.rand(t, s, device="cuda")
+off, rows, pairs = new(e + 1, dt=torch.int32), new(t, s, dt=torch.int32), new(t * s, dt=torch.int32)
+q, sc, y = new(t * s, k, dt=torch.uint8), new(k // 128, t * s), new(t, k, dt=torch.bfloat16)
+grouped, dw, hq = new(t * s, k, dt=torch.bfloat16), new(t, s), new(t, k, dt=torch.uint8)
+hs, am, one = new(k // 128, t), new(1), torch.ones(1, device="cuda")
+def run():
+    F.fp8_experts_sort(ids, e, off, rows, pairs)
+    F.fp8_experts_gather(x, rows, q=q, scales=sc, out=grouped)
+    F.fp8_experts_combine(grouped, rows, w, y)
+    F.fp8_experts_combine_backward(y, rows, w, x=grouped, d_weights=dw, q=q, scales=sc)
+    F.fp8_act_checkpoint(x, None, F.ACT_SILU, hq, scale=one, amax_out=am)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    run()
+g.replay()
+torch.cuda.synchronize()
+got = [v.clone() for v in (off, rows, pairs, q, sc, y, dw, hq, am)]
+run()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(got, (off, rows, pairs, q, sc, y, dw, hq, am)))
+assert int(off[-1]) == t * s and float(am) > 0
+print("fine")
+"""
+
+
+def test_first_calls_of_a_process_may_be_captured():
+    """The kernels' attributes are set by their first launch."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST], cwd=root, capture_output=True, text=True,
+                       timeout=300)
+    assert r.returncode == 0 and "fine" in r.stdout, r.stderr[-2000:]
+
+
 def test_binding_refuses():
     F = lib()
     t, s, e, k = 4, 2, 3, 256

@@ -112,6 +112,10 @@ def test_no_tokens_and_refusals():
     x = randn((3, 128), 3, 1.0).to(BF)
     empty = torch.empty((0, 2), device="cuda")
     assert mlp(x[:0], empty.long(), empty).shape == (0, 128)
+    grad = ExpertsMLP(w13, w2, backward=True)
+    grad(x[:0], empty.long(), empty, keep=True)
+    dx, dw = grad.backward(x[:0])
+    assert dx.shape == (0, 128) and dw.shape == (0, 2)
     ids = torch.full((3, 2), -1, dtype=torch.int64, device="cuda")
     assert (mlp(x, ids, torch.ones((3, 2), device="cuda")) == 0).all()  # no expert takes any
     with pytest.raises(ValueError):
