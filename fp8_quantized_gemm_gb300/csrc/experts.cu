@@ -24,18 +24,22 @@
 namespace fp8k {
 
 // ------------------------------------------------------------------- sort --
-// One cluster of up to 16 CTAs of 32 warps; warp g of it owns the g-th run
-// of consecutive pairs.  A first pass ranks each pair among its warp's pairs of
-// the same expert: the lanes of 32 pairs that chose the same expert find each
-// other by a vote per bit of the expert's number (the match instruction is one,
-// but 131072 pairs took 25 us with it: its unit was the limit), and the counts
-// so far sit in shared memory.  Two prefix sums (over the warps of the cluster,
-// the CTAs' totals exchanged through distributed shared memory, and over the
-// experts) turn the counts into first rows, which a second pass adds to the
-// ranks.  Both passes have eight loads per lane in flight.  The pairs of the
-// rows are scattered by a kernel of their own on all SMs: a scattered store
-// takes a cycle per lane, 4 us on the cluster's 16 SMs.  No atomic, no
-// scratch.
+// One cluster of up to 16 CTAs of 32 warps; warp g of it owns the g-th run of
+// consecutive pairs.  A first pass ranks each pair among its warp's pairs of the
+// same expert: the lanes of 32 pairs that chose the same expert find each other by
+// a vote per bit of the expert's number, and the counts so far sit in shared
+// memory.  Two prefix sums (over the warps of the cluster, the CTAs' totals
+// exchanged through distributed shared memory, and over the experts) turn the
+// counts into first rows, which a second pass adds to the ranks.  A warp's pairs
+// are loaded eight per lane at once, and stay in registers between the passes
+// where that is all of them.  The pairs of the rows are scattered by a kernel of
+// their own on all SMs (a scattered store takes a cycle per lane of one SM).  No
+// atomic, no scratch.
+//
+// Bound by the instructions of the passes on the cluster's SMs: 131072 pairs of 256
+// experts 11.3 us (17.3 on eight CTAs; with the match instruction in the place of
+// the votes and the scatter in the same kernel 25), 512 pairs 3.5 us, most of it
+// launch and latency.
 constexpr int kSortWarps = 32, kSortCluster = 16, kSortRun = 8;
 
 __device__ __forceinline__ uint32_t ld_shared_cluster_u32(uint32_t cluster_addr) {
@@ -44,16 +48,15 @@ __device__ __forceinline__ uint32_t ld_shared_cluster_u32(uint32_t cluster_addr)
   return v;
 }
 
-// lanes whose value (below 2^bits, bits <= 8) equals this lane's, of those that
-// have one (a lane without gets a mask that means nothing)
-__device__ __forceinline__ uint32_t lanes_alike(uint32_t v, bool has, int bits) {
+// lanes whose value (below 256) equals this lane's, of those that have one (a
+// lane without gets a mask that means nothing)
+__device__ __forceinline__ uint32_t lanes_alike(uint32_t v, bool has) {
   uint32_t same = __ballot_sync(0xffffffffu, has);
 #pragma unroll
   for (int b = 0; b < 8; ++b) {
-    if (b >= bits) break;
-    const bool one = v >> b & 1u;
+    const bool one = (v & (1u << b)) != 0u;
     const uint32_t ones = __ballot_sync(0xffffffffu, one);
-    same &= one ? ones : ~ones;
+    same &= ones ^ (one ? 0u : 0xffffffffu);
   }
   return same;
 }
@@ -87,7 +90,6 @@ __global__ void __launch_bounds__(32 * kSortWarps)
   for (int e = l; e < E; e += 32) mine[e] = 0u;
   __syncwarp();
   const uint32_t below = (1u << l) - 1u;
-  const int bits = E > 1 ? 32 - __clz(E - 1) : 0;
   // the experts and ranks of a batch of pairs; a warp's only batch stays here
   // between the passes, the ranks of others wait in rows
   const bool whole = per <= 32 * kSortRun;
@@ -107,7 +109,7 @@ __global__ void __launch_bounds__(32 * kSortWarps)
       if (i0 + 32 * j >= end) break;
       const uint32_t i = i0 + 32 * j + l;
       const bool has = e[j] < (uint32_t)E;
-      const uint32_t same = lanes_alike(e[j], has, bits), ahead = same & below;
+      const uint32_t same = lanes_alike(e[j], has), ahead = same & below;
       const uint32_t seen = has ? mine[e[j]] : 0u;
       __syncwarp();
       if (has && ahead == 0u) mine[e[j]] = seen + __popc(same);
@@ -276,9 +278,12 @@ struct TaskWalk {
 // A warp per (token, 512 columns): lane l holds 16 consecutive elements, so
 // eight lanes form a 1x128 group and each lane stores 16 bytes of codes per
 // row.  The token's rows sit in the lanes, one each; a group's scale for eight
-// rows goes out in one store instruction, one row per lane of the group.  (A
-// resident grid that loads the next task ahead of this one's stores measured
-// slower: 58 against 53 us for 4096 tokens of 7168 columns and eight rows each.)
+// rows goes out in one store instruction, one row per lane of the group.
+//
+// Bound by HBM: 4096 tokens of 7168 bf16 columns to eight rows each in 47.4 us, 94%
+// of the copy rate (scattering the scales, four bytes per row and group, costs 2 to
+// 6 us of it).  Codes leave L2 first (plain stores: 52 us).  A resident grid that
+// loads the next task ahead of this one's stores was no faster (58 against 53 then).
 template <typename T, int F>
 __global__ void __launch_bounds__(256, 3) experts_gather_kernel(const GatherArgs a) {
   constexpr bool kCodes = sizeof(T) == 1;
@@ -365,41 +370,61 @@ cudaError_t launch_experts_gather(const GatherArgs &a, int source, int sms, cuda
 // one is added up, and the choices of the step behind it are loaded meanwhile,
 // so that the warp always has 4 KB in flight and no registers hold them.  (Loads
 // into registers, a batch at a time, measured 116 and 151 us on 4096 tokens of
-// 7168 columns with eight rows each.)  A dropped pair's row is a copy of no
-// bytes, which leaves zeros.
-template <typename T>
+// 7168 columns with eight rows each.)  Shorter lists of choices take W windows of
+// 256 columns a step, so that as many rows' pieces are in flight: a quarter of them
+// left two choices at 348 us where the copy rate allows 140 (the gradient, 16384
+// tokens).  A dropped pair's row is a copy of no bytes, which leaves zeros.
+template <typename T, int W>
 constexpr int rows_per_step() {
-  return sizeof(T) == 2 ? 8 : 4;
+  return (sizeof(T) == 2 ? 8 : 4) / W;
+}
+// Bytes of a stage: the rows' pieces, then those of a row of type V.
+template <typename T, typename V, int W>
+constexpr int ring_stage() {
+  return 256 * W * (rows_per_step<T, W>() * (int)sizeof(T) + (int)sizeof(V));
+}
+// Warps of a CTA, of which three share an SM (74 KB of its shared memory each).
+constexpr int ring_warps(int stage) {
+  const int n = 74 * 1024 / (2 * stage);
+  return n < 8 ? n : 8;
+}
+// The most windows a step (1, 2 or 4; fp32 rows 1 or 2) that still hold the whole
+// list, and of which more than half exist.
+template <typename T, typename Fn>
+static cudaError_t with_windows(int64_t S, int64_t K, Fn &&f) {
+  const int64_t all = rows_per_step<T, 1>();
+  int w = sizeof(T) == 2 ? 4 : 2;
+  while (w > 1 && (S > all / w || K <= 128 * w)) w /= 2;
+  if constexpr (sizeof(T) == 2)
+    if (w == 4) return f(std::integral_constant<int, 4>{});
+  return w == 2 ? f(std::integral_constant<int, 2>{}) : f(std::integral_constant<int, 1>{});
 }
 
-// 256 elements of a row, of which the first `left` exist: lane l's eight.  fp32:
-// the row's 64 vectors go out as whole sectors (lane l copies vectors l and
-// l + 32); vector e sits in half e & 1 at column (e / 2) ^ 4 (e & 1), free of bank
-// conflicts both ways.
+// 256 elements of a row, of which the first `left` exist: the row's 16-byte vectors
+// in their order (lane l copies vector l, and l + 32 of fp32 rows), lane l's eight
+// elements read back.  (The two lanes that share a 32-byte sector copy to one place:
+// apart, as a layout without bank conflicts for fp32 has them, the copies took L2
+// twice the requests: 313 us instead of 170 for the sums of 4096 x 8 rows of 7168.)
 template <typename T>
 struct RowCopy {
-  uint32_t dst, bytes, bytes2;  // this lane's place in a slot, and what it copies
-  int64_t offset;               // in bytes from the row's first column
-  __device__ __forceinline__ RowCopy(uint32_t ring, int64_t k0, int32_t left) {
-    const int32_t l = (int32_t)lane_id(), per = 16 / (int32_t)sizeof(T);
-    dst = ring + 16 * (sizeof(T) == 2 ? l : 32 * (l & 1) + ((l >> 1) ^ (4 * (l & 1))));
-    bytes = per * l < left ? 16u : 0u;
-    bytes2 = per * (l + 32) < left ? 16u : 0u;
-    offset = k0 * (int64_t)sizeof(T) + 16 * l;
+  // in bytes from a row's first element: this lane's first vector at column k0
+  static __device__ __forceinline__ int64_t offset(int64_t k0) {
+    return k0 * (int64_t)sizeof(T) + 16 * lane_id();
   }
-  // into the slot at `slot` bytes of the ring, from the row at src + offset
-  __device__ __forceinline__ void operator()(int slot, const char *src, bool real) const {
-    copy16_async(dst + slot, src, real ? bytes : 0u);
-    if constexpr (sizeof(T) == 4) copy16_async(dst + slot + 256, src + 512, real ? bytes2 : 0u);
+  // dst and src: this lane's first vector's
+  static __device__ __forceinline__ void copy(uint32_t dst, const char *src, int32_t left, bool real) {
+    const int32_t l = (int32_t)lane_id(), per = 16 / (int32_t)sizeof(T);
+    copy16_async(dst, src, real && per * l < left ? 16u : 0u);
+    if constexpr (sizeof(T) == 4)
+      copy16_async(dst + 512, src + 512, real && per * (l + 32) < left ? 16u : 0u);
   }
 };
 template <typename T>
 __device__ __forceinline__ Raw8<T> ring_row(const uint8_t *slot) {
-  const uint32_t l = lane_id();
-  const uint4 *src = reinterpret_cast<const uint4 *>(slot);
   Raw8<T> r;
-  r.w[0] = src[l];
-  if constexpr (sizeof(T) == 4) r.w[1] = src[32 + (l ^ 4u)];
+#pragma unroll
+  for (int i = 0; i < Raw8<T>::kWords; ++i)
+    r.w[i] = reinterpret_cast<const uint4 *>(slot)[Raw8<T>::kWords * lane_id() + i];
   return r;
 }
 
@@ -428,19 +453,15 @@ struct Choices {
   }
 };
 
-constexpr int kRingWarps = 8;  // of a CTA
-
 // ---------------------------------------------------------------- combine --
-// A warp per (token, 256 columns).  Sums in fp32 in the order of the choices, the
-// residual last, one rounding to the output's type.
-template <typename T, typename O>
-constexpr int combine_stage() {
-  return 256 * (rows_per_step<T>() * (int)sizeof(T) + (int)sizeof(O));
-}
-
-template <typename T, typename O>
-__global__ void __launch_bounds__(32 * kRingWarps, 3) experts_combine_kernel(const CombineArgs a) {
-  constexpr int kC = rows_per_step<T>(), kRow = 256 * sizeof(T), kStage = combine_stage<T, O>();
+// A warp per (token, W windows).  Sums in fp32 in the order of the choices, the
+// residual last, one rounding to the output's type.  4096 tokens of 7168 columns,
+// eight bf16 rows each and a residual: 86.4 us, the copy rate.
+template <typename T, typename O, int W>
+__global__ void __launch_bounds__(32 * ring_warps(ring_stage<T, O, W>()), 3)
+    experts_combine_kernel(const CombineArgs a) {
+  constexpr int kC = rows_per_step<T, W>(), kRow = 256 * sizeof(T), kRes = 256 * sizeof(O),
+                kStage = ring_stage<T, O, W>();
   extern __shared__ __align__(16) uint8_t smem[];
   uint8_t *ring = smem + (threadIdx.x >> 5) * (2 * kStage);
   const uint32_t ring_at = smem_u32(ring);
@@ -462,19 +483,27 @@ __global__ void __launch_bounds__(32 * kRingWarps, 3) experts_combine_kernel(con
   };
   auto fetch = [&](const Step &s, const Choices<kC> &c, int stage) {
     if (s.w.t < a.T) {
-      const int64_t k0 = (int64_t)s.w.win * 256;
-      const int32_t left = (int32_t)min((int64_t)256, a.K - k0), n = min(kC, S - s.s0);
-      const uint32_t kept = c.kept();
-      const RowCopy<T> copy(ring_at + stage * kStage, k0, left);
-      const char *x = static_cast<const char *>(a.x) + copy.offset;
+      const int32_t n = min(kC, S - s.s0);
+      const uint32_t kept = c.kept(), at = ring_at + stage * kStage + 16 * lane_id();
+      const int64_t k0 = (int64_t)s.w.win * (256 * W);
+      const int32_t left = (int32_t)min((int64_t)256 * W, a.K - k0);
+      const char *x = static_cast<const char *>(a.x) + RowCopy<T>::offset(k0);
+      uint32_t r[kC];
+#pragma unroll
+      for (int j = 0; j < kC; ++j) r[j] = (uint32_t)max(__shfl_sync(0xffffffffu, c.row, j), 0);
 #pragma unroll
       for (int j = 0; j < kC; ++j) {
-        const uint32_t r = (uint32_t)max(__shfl_sync(0xffffffffu, c.row, j), 0);
-        if (j < n) copy(j * kRow, x + (uint64_t)r * pitch, kept >> j & 1u);
+        if (j >= n) continue;
+        const char *row = x + (uint64_t)r[j] * pitch;
+#pragma unroll
+        for (int u = 0; u < W; ++u)
+          RowCopy<T>::copy(at + (u * kC + j) * kRow, row + u * kRow, left - 256 * u, kept >> j & 1u);
       }
       if (res != nullptr && S <= kC) {
-        const RowCopy<O> copy_res(ring_at + stage * kStage, k0, left);
-        copy_res(kC * kRow, reinterpret_cast<const char *>(res + s.w.t * a.ldr) + copy_res.offset, true);
+        const char *v = reinterpret_cast<const char *>(res + s.w.t * a.ldr) + RowCopy<O>::offset(k0);
+#pragma unroll
+        for (int u = 0; u < W; ++u)
+          RowCopy<O>::copy(at + W * kC * kRow + u * kRes, v + u * kRes, left - 256 * u, true);
       }
     }
     copies_commit();
@@ -482,14 +511,14 @@ __global__ void __launch_bounds__(32 * kRingWarps, 3) experts_combine_kernel(con
   auto choices = [&](const Step &s, Choices<kC> &c) {
     c.load(a.rows, a.weights, s.w.t, s.s0, a.T, S, a.M);
   };
-  Step cur{TaskWalk(a.K, 256), 0};
+  Step cur{TaskWalk(a.K, 256 * W), 0};
   Choices<kC> c_cur, c_next;
   choices(cur, c_cur);
   fetch(cur, c_cur, 0);
   Step nxt = cur;
   nxt.next(S);
   choices(nxt, c_next);
-  F2 acc[4];
+  F2 acc[W][4];
   for (int stage = 0; cur.w.t < a.T; stage ^= 1) {
     __syncwarp();  // the other lanes have read what this overwrites
     fetch(nxt, c_next, stage ^ 1);
@@ -505,28 +534,33 @@ __global__ void __launch_bounds__(32 * kRingWarps, 3) experts_combine_kernel(con
 #pragma unroll
     for (int j = 0; j < kC; ++j) {
       const F2 wt(__shfl_sync(0xffffffffu, w_l, j));
-      if (j < n) {
-        const Raw8<T> v = ring_row<T>(slot + j * kRow);
+      if (j >= n) continue;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[i] = fma2(wt, raw_pair(v, i), acc[i]);
+      for (int u = 0; u < W; ++u) {
+        const Raw8<T> v = ring_row<T>(slot + (u * kC + j) * kRow);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[u][i] = fma2(wt, raw_pair(v, i), acc[u][i]);
       }
     }
     if (cur.s0 + kC >= S) {
-      const int64_t k = (int64_t)cur.w.win * 256 + lane_id() * 8;
-      if (k < a.K) {
-        if (res != nullptr) {
-          Raw8<O> r;
-          if (S <= kC)
-            r = ring_row<O>(slot + kC * kRow);
-          else  // (a longer list has other stages behind the first)
-            r.load_stream(res + cur.w.t * a.ldr + k);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) acc[i] = acc[i] + raw_pair(r, i);
+      for (int u = 0; u < W; ++u) {
+        const int64_t k = (int64_t)cur.w.win * (256 * W) + 256 * u + lane_id() * 8;
+        if (k < a.K) {
+          if (res != nullptr) {
+            Raw8<O> r;
+            if (S <= kC)
+              r = ring_row<O>(slot + W * kC * kRow + u * kRes);
+            else  // (a longer list has other stages behind the first)
+              r.load_stream(res + cur.w.t * a.ldr + k);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[u][i] = acc[u][i] + raw_pair(r, i);
+          }
+          store8(static_cast<O *>(a.out) + cur.w.t * a.ld_out + k, round8<O>(acc[u]));
         }
-        store8(static_cast<O *>(a.out) + cur.w.t * a.ld_out + k, round8<O>(acc));
-      }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc[i] = F2(0.0f);
+        for (int i = 0; i < 4; ++i) acc[u][i] = F2(0.0f);
+      }
     }
     cur = nxt;
     nxt = behind;
@@ -536,10 +570,13 @@ __global__ void __launch_bounds__(32 * kRingWarps, 3) experts_combine_kernel(con
 
 template <typename T, typename O>
 static cudaError_t run_combine(const CombineArgs &a, int sms, cudaStream_t st) {
-  const int64_t blocks = grid_of(a.T * ((a.K + 255) / 256), kRingWarps, (int64_t)sms * 3);
-  constexpr int kSmem = kRingWarps * 2 * combine_stage<T, O>();
-  return launch_serial_smem<experts_combine_kernel<T, O>, kSmem>(blocks, 32 * kRingWarps, kSmem, st,
-                                                                 a);
+  return with_windows<T>(a.S, a.K, [&](auto windows) {
+    constexpr int kW = windows.value, kStage = ring_stage<T, O, kW>(), kWarps = ring_warps(kStage);
+    constexpr int kSmem = kWarps * 2 * kStage;
+    const int64_t tasks = a.T * ((a.K + 256 * kW - 1) / (256 * kW));
+    return launch_serial_smem<experts_combine_kernel<T, O, kW>, kSmem>(
+        grid_of(tasks, kWarps, (int64_t)sms * 3), 32 * kWarps, kSmem, st, a);
+  });
 }
 
 cudaError_t launch_experts_combine(const CombineArgs &a, int x_dt, int out_dt, int sms,
@@ -560,32 +597,29 @@ cudaError_t launch_experts_combine(const CombineArgs &a, int x_dt, int out_dt, i
 }
 
 // ------------------------------------------------------- combine, gradient --
-// A CTA per token, each warp every nw-th 256 columns of it, up to eight rows
-// (fp32: four) at a time.  |w dy| of a group (16 lanes) peaks where |dy| does
-// (rounding is monotone), so the group's maximum of dy is taken once and lane j
-// of the group forms the scale of the j-th row from it, and the factor w / scale
-// that takes dy to that row's codes.  The rows' dot products stay in registers and
-// are reduced together: a butterfly that halves the rows a lane still holds at
-// each of its first steps, then a sum over the warps in their order.
-template <typename DY, typename X>
-constexpr int combine_grad_stage() {
-  return 256 * (rows_per_step<X>() * (int)sizeof(X) + (int)sizeof(DY));
-}
-
-template <typename DY, typename X, int F>
-__global__ void __launch_bounds__(32 * kRingWarps, 3)
+// A CTA per token, each warp every nw-th W windows of it.  |w dy| of a group (16
+// lanes) peaks where |dy| does (rounding is monotone), so the group's maximum of dy
+// is taken once and lane j of the group forms the scale of the j-th row from it,
+// and the factor w / scale that takes dy to that row's codes.  The rows' dot
+// products stay in registers and are reduced together: a butterfly that halves the
+// rows a lane still holds at each of its first steps, then a sum over the warps in
+// their order.  4096 tokens of 7168 columns, eight bf16 rows each, codes and dw: 122
+// us, 93% of the copy rate (121 without the codes' stores: the instructions of a
+// step bound it).
+template <typename DY, typename X, int F, int W>
+__global__ void __launch_bounds__(32 * ring_warps(ring_stage<X, DY, W>()), 3)
     experts_combine_grad_kernel(const CombineGradArgs a) {
-  constexpr int kC = rows_per_step<X>(), kRow = 256 * sizeof(X),
-                kStage = combine_grad_stage<DY, X>();
+  constexpr int kC = rows_per_step<X, W>(), kRow = 256 * sizeof(X), kDy = 256 * sizeof(DY),
+                kStage = ring_stage<X, DY, W>(), kWarps = ring_warps(kStage);
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ float part[2][kRingWarps][kC];
+  __shared__ float part[2][kWarps][kC];
   launch_dependents();
   grid_dependency_wait();
   const uint32_t l = lane_id(), w = threadIdx.x >> 5, nw = blockDim.x >> 5;
   uint8_t *ring = smem + w * (2 * kStage);
   const uint32_t ring_at = smem_u32(ring);
   const DY *dy = static_cast<const DY *>(a.dy);
-  const int32_t wins = (int32_t)((a.K + 255) / 256), S = (int32_t)a.S;
+  const int32_t wins = (int32_t)((a.K + 256 * W - 1) / (256 * W)), S = (int32_t)a.S;
   const uint32_t pitch = (uint32_t)a.ldx * (uint32_t)sizeof(X), K = (uint32_t)a.K;
   struct Step {
     int64_t t;
@@ -605,19 +639,23 @@ __global__ void __launch_bounds__(32 * kRingWarps, 3)
   };
   auto fetch = [&](const Step &s, const Choices<kC> &c, int stage) {
     if (s.t < a.T) {
-      const int64_t k0 = (int64_t)s.win * 256;
-      const int32_t left = (int32_t)min((int64_t)256, a.K - k0);
-      const RowCopy<DY> copy_dy(ring_at + stage * kStage, k0, left);
-      copy_dy(kC * kRow, reinterpret_cast<const char *>(dy + s.t * a.ld_dy) + copy_dy.offset, true);
+      const int32_t n = min(kC, S - s.s0);
+      const uint32_t kept = c.kept(), at = ring_at + stage * kStage + 16 * lane_id();
+      const int64_t k0 = (int64_t)s.win * (256 * W);
+      const int32_t left = (int32_t)min((int64_t)256 * W, a.K - k0);
+      const char *d = reinterpret_cast<const char *>(dy + s.t * a.ld_dy) + RowCopy<DY>::offset(k0);
+#pragma unroll
+      for (int u = 0; u < W; ++u)
+        RowCopy<DY>::copy(at + W * kC * kRow + u * kDy, d + u * kDy, left - 256 * u, true);
       if (a.dw != nullptr && a.M > 0) {
-        const int32_t n = min(kC, S - s.s0);
-        const uint32_t kept = c.kept();
-        const RowCopy<X> copy(ring_at + stage * kStage, k0, left);
-        const char *x = static_cast<const char *>(a.x) + copy.offset;
+        const char *x = static_cast<const char *>(a.x) + RowCopy<X>::offset(k0);
 #pragma unroll
         for (int j = 0; j < kC; ++j) {
-          const uint32_t r = (uint32_t)max(__shfl_sync(0xffffffffu, c.row, j), 0);
-          if (j < n) copy(j * kRow, x + (uint64_t)r * pitch, kept >> j & 1u);
+          const char *row = x + (uint64_t)max(__shfl_sync(0xffffffffu, c.row, j), 0) * pitch;
+          if (j >= n) continue;
+#pragma unroll
+          for (int u = 0; u < W; ++u)
+            RowCopy<X>::copy(at + (u * kC + j) * kRow, row + u * kRow, left - 256 * u, kept >> j & 1u);
         }
       }
     }
@@ -647,98 +685,102 @@ __global__ void __launch_bounds__(32 * kRingWarps, 3)
     if (fresh) choices(behind, c_next);
     copies_wait<1>();
     __syncwarp();
-    const uint8_t *slot = ring + stage * kStage;
-    const uint32_t k = (uint32_t)cur.win * 256 + l * 8, g = k >> 7;
-    const bool in = k < K;
-    const Raw8<DY> raw = ring_row<DY>(slot + kC * kRow);
-    F2 v[4];
+    const int32_t n = min(kC, S - cur.s0);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = raw_pair(raw, i);
-    if (a.q != nullptr) {
-      uint32_t ka = 0, kb = 0;
-      raw.max_abs(ka, kb);
-      uint32_t key = Raw8<DY>::merge_keys(ka, kb);
-      key = max(key, __shfl_xor_sync(0xffffffffu, key, 8));
-      const float amax = fabsf(w_l) * __uint_as_float(group8_max(key));
-      GroupScale gs = group_scale<F>(amax, a.sfmt);
-      const float f_l = w_l * gs.inv;
-      const bool fast = __all_sync(
-          0xffffffffu, gs.fast && (w_l == 0.0f || (fabsf(f_l) >= 0x1p-100f && fabsf(f_l) <= 0x1p100f)));
-      if (!fast) gs = group_scale_any<F>(amax, a.sfmt);
-      if (row_l >= 0 && (l & 15u) < (uint32_t)kC && 128 * g < K)
-        store_scale(a.scales, (int64_t)g * a.M + row_l, gs.stored, a.sfmt);
-      uint8_t *q = a.q + k;
+    for (int u = 0; u < W; ++u) {
+      const uint8_t *slot = ring + stage * kStage + u * kC * kRow;
+      const uint32_t k = (uint32_t)cur.win * (256 * W) + 256 * u + l * 8, g = k >> 7;
+      const bool in = k < K;
+      const Raw8<DY> raw = ring_row<DY>(ring + stage * kStage + W * kC * kRow + u * kDy);
+      F2 v[4];
 #pragma unroll
-      for (int j = 0; j < kC; ++j) {
-        const uint32_t row = (uint32_t)__shfl_sync(0xffffffffu, row_l, j);
-        const int from = (int)(l & 16u) | j;
-        uint2 c;
-        if (fast) {
-          const F2 f(__shfl_sync(0xffffffffu, f_l, from));
-          c = make_uint2(pack4<F>(v[0] * f, v[1] * f), pack4<F>(v[2] * f, v[3] * f));
-        } else {
-          const F2 wj(__shfl_sync(0xffffffffu, w_l, j));
-          const float s = __shfl_sync(0xffffffffu, gs.s, from);
-          c = make_uint2(codes4_ieee<F>((v[0] * wj).v, (v[1] * wj).v, s),
-                         codes4_ieee<F>((v[2] * wj).v, (v[3] * wj).v, s));
-        }
-        if ((kept >> j & 1u) && in) *reinterpret_cast<uint2 *>(q + (uint64_t)row * K) = c;
-      }
-    }
-    if (a.dx != nullptr) {
-#pragma unroll
-      for (int j = 0; j < kC; ++j) {
-        const int64_t row = __shfl_sync(0xffffffffu, row_l, j);
-        const F2 wj(__shfl_sync(0xffffffffu, w_l, j));
-        if (row < 0 || !in) continue;
-        const F2 y[4] = {v[0] * wj, v[1] * wj, v[2] * wj, v[3] * wj};
-        if (a.dx_dt == 0)
-          store8(static_cast<__nv_bfloat16 *>(a.dx) + row * a.ld_dx + k, round8<__nv_bfloat16>(y));
-        else
-          store8(static_cast<float *>(a.dx) + row * a.ld_dx + k, round8<float>(y));
-      }
-    }
-    if (a.dw != nullptr) {
-      const int32_t n = min(kC, S - cur.s0);
-#pragma unroll
-      for (int j = 0; j < kC; ++j) {
-        if (j >= n || a.M == 0) continue;
-        const Raw8<X> xv = ring_row<X>(slot + j * kRow);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) dot[j] = fma2(v[i], raw_pair(xv, i), dot[j]);
-      }
-      if (cur.win + (int32_t)nw >= wins) {  // this warp's last columns of these rows
-        float d[kC];
+      for (int i = 0; i < 4; ++i) v[i] = raw_pair(raw, i);
+      if (a.q != nullptr) {
+        uint32_t ka = 0, kb = 0;
+        raw.max_abs(ka, kb);
+        uint32_t key = Raw8<DY>::merge_keys(ka, kb);
+        key = max(key, __shfl_xor_sync(0xffffffffu, key, 8));
+        const float amax = fabsf(w_l) * __uint_as_float(group8_max(key));
+        GroupScale gs = group_scale<F>(amax, a.sfmt);
+        const float f_l = w_l * gs.inv;
+        const bool fast =
+            __all_sync(0xffffffffu, gs.fast && (w_l == 0.0f || (fabsf(f_l) >= 0x1p-100f &&
+                                                                fabsf(f_l) <= 0x1p100f)));
+        if (!fast) gs = group_scale_any<F>(amax, a.sfmt);
+        if (row_l >= 0 && (l & 15u) < (uint32_t)kC && 128 * g < K)
+          store_scale(a.scales, (int64_t)g * a.M + row_l, gs.stored, a.sfmt);
+        uint8_t *q = a.q + k;
 #pragma unroll
         for (int j = 0; j < kC; ++j) {
-          float d0, d1;
-          dot[j].get(d0, d1);
-          d[j] = d0 + d1;
-          dot[j] = F2(0.0f);
-        }
-        // halves apart, quarters apart, ...: lane l ends with row l / (32 / kC)
-#pragma unroll
-        for (int h = kC / 2; h > 0; h >>= 1) {
-          const uint32_t apart = (uint32_t)(32 / kC * h);
-#pragma unroll
-          for (int j = 0; j < h; ++j) {
-            const float keep = l & apart ? d[j + h] : d[j], give = l & apart ? d[j] : d[j + h];
-            d[j] = keep + __shfl_xor_sync(0xffffffffu, give, (int)apart);
+          const uint32_t row = (uint32_t)__shfl_sync(0xffffffffu, row_l, j);
+          const int from = (int)(l & 16u) | j;
+          uint2 c;
+          if (fast) {
+            const F2 f(__shfl_sync(0xffffffffu, f_l, from));
+            c = make_uint2(pack4<F>(v[0] * f, v[1] * f), pack4<F>(v[2] * f, v[3] * f));
+          } else {
+            const F2 wj(__shfl_sync(0xffffffffu, w_l, j));
+            const float s = __shfl_sync(0xffffffffu, gs.s, from);
+            c = make_uint2(codes4_ieee<F>((v[0] * wj).v, (v[1] * wj).v, s),
+                           codes4_ieee<F>((v[2] * wj).v, (v[3] * wj).v, s));
           }
+          if ((kept >> j & 1u) && in) *reinterpret_cast<uint2 *>(q + (uint64_t)row * K) = c;
         }
-        float sum = d[0];
-#pragma unroll
-        for (int o = 16 / kC; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        // (a buffer is written again two barriers after it was read)
-        if (l % (32 / kC) == 0) part[phase][w][l / (32 / kC)] = sum;
-        __syncthreads();
-        if ((int)threadIdx.x < n) {
-          float all = 0.0f;
-          for (uint32_t i = 0; i < nw; ++i) all += part[phase][i][threadIdx.x];
-          a.dw[cur.t * S + cur.s0 + threadIdx.x] = all;
-        }
-        phase ^= 1;
       }
+      if (a.dx != nullptr) {
+#pragma unroll
+        for (int j = 0; j < kC; ++j) {
+          const int64_t row = __shfl_sync(0xffffffffu, row_l, j);
+          const F2 wj(__shfl_sync(0xffffffffu, w_l, j));
+          if (row < 0 || !in) continue;
+          const F2 y[4] = {v[0] * wj, v[1] * wj, v[2] * wj, v[3] * wj};
+          if (a.dx_dt == 0)
+            store8(static_cast<__nv_bfloat16 *>(a.dx) + row * a.ld_dx + k, round8<__nv_bfloat16>(y));
+          else
+            store8(static_cast<float *>(a.dx) + row * a.ld_dx + k, round8<float>(y));
+        }
+      }
+      if (a.dw != nullptr && a.M > 0) {
+#pragma unroll
+        for (int j = 0; j < kC; ++j) {
+          if (j >= n) continue;
+          const Raw8<X> xv = ring_row<X>(slot + j * kRow);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) dot[j] = fma2(v[i], raw_pair(xv, i), dot[j]);
+        }
+      }
+    }
+    if (a.dw != nullptr && cur.win + (int32_t)nw >= wins) {  // this warp's last columns of these rows
+      float d[kC];
+#pragma unroll
+      for (int j = 0; j < kC; ++j) {
+        float d0, d1;
+        dot[j].get(d0, d1);
+        d[j] = d0 + d1;
+        dot[j] = F2(0.0f);
+      }
+      // halves apart, quarters apart, ...: lane l ends with row l / (32 / kC)
+#pragma unroll
+      for (int h = kC / 2; h > 0; h >>= 1) {
+        const uint32_t apart = (uint32_t)(32 / kC * h);
+#pragma unroll
+        for (int j = 0; j < h; ++j) {
+          const float keep = l & apart ? d[j + h] : d[j], give = l & apart ? d[j] : d[j + h];
+          d[j] = keep + __shfl_xor_sync(0xffffffffu, give, (int)apart);
+        }
+      }
+      float sum = d[0];
+#pragma unroll
+      for (int o = 16 / kC; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      // (a buffer is written again two barriers after it was read)
+      if (l % (32 / kC) == 0) part[phase][w][l / (32 / kC)] = sum;
+      __syncthreads();
+      if ((int)threadIdx.x < n) {
+        float all = 0.0f;
+        for (uint32_t i = 0; i < nw; ++i) all += part[phase][i][threadIdx.x];
+        a.dw[cur.t * S + cur.s0 + threadIdx.x] = all;
+      }
+      phase ^= 1;
     }
     cur = nxt;
     nxt = behind;
@@ -746,15 +788,17 @@ __global__ void __launch_bounds__(32 * kRingWarps, 3)
   copies_wait<0>();
 }
 
-// The fewest rounds of up to eight windows, then as few warps as they need.
+// The fewest rounds of a token's steps, then as few warps as they need.
 template <typename DY, typename X, int F>
 static cudaError_t run_combine_grad(const CombineGradArgs &a, int sms, cudaStream_t st) {
-  const int64_t wins = (a.K + 255) / 256, rounds = (wins + kRingWarps - 1) / kRingWarps;
-  const int warps = (int)((wins + rounds - 1) / rounds);
-  const int64_t most = (int64_t)sms * (3 * kRingWarps / warps);  // resident at once
-  constexpr int kWarpSmem = 2 * combine_grad_stage<DY, X>();
-  return launch_serial_smem<experts_combine_grad_kernel<DY, X, F>, kRingWarps * kWarpSmem>(
-      a.T < most ? a.T : most, 32 * warps, warps * kWarpSmem, st, a);
+  return with_windows<X>(a.S, a.K, [&](auto windows) {
+    constexpr int kW = windows.value, kStage = ring_stage<X, DY, kW>(), kMost = ring_warps(kStage);
+    const int64_t steps = (a.K + 256 * kW - 1) / (256 * kW), rounds = (steps + kMost - 1) / kMost;
+    const int warps = (int)((steps + rounds - 1) / rounds);
+    const int64_t most = (int64_t)sms * (3 * kMost / warps);  // resident at once
+    return launch_serial_smem<experts_combine_grad_kernel<DY, X, F, kW>, kMost * 2 * kStage>(
+        a.T < most ? a.T : most, 32 * warps, warps * 2 * kStage, st, a);
+  });
 }
 template <typename DY, typename X>
 static cudaError_t run_combine_grad(const CombineGradArgs &a, int sms, cudaStream_t st) {

@@ -4,9 +4,9 @@
 Tolerances.  combine: an fp32 chain of at most S fused steps and the residual's
 addition, each within 2^-24 of a partial sum that is at most the sum of the
 magnitudes; the result is rounded once to the output's type (half a step).
-dw: a lane adds 8 pairs per 512 columns and each warp takes at most every second
-window up to K = 16384, then two halves, five shuffles and 16 warps: 64 steps of
-2^-24 on the sum of the magnitudes cover it.  Codes of w dy: one rounding each
+dw: a lane adds four pairs per 256 columns and a CTA has at least four warps up
+to K = 16384 (16 windows each: 64 steps), then two halves, five shuffles and at
+most eight warps: 80 steps of 2^-24 on the sum of the magnitudes cover it.  Codes of w dy: one rounding each
 of the product, the maximum's product, the scale, its reciprocal and the
 quotient, below 2^-21 together, and half a step of the format.  gather forms the
 exact quotient: the bytes themselves are checked.
@@ -204,7 +204,11 @@ COMBINE = [  # t, s, e, k, dt, out, res, weights, drop, pad
     (1, 1, 1, 16, "bf16", "bf16", False, True, 0, 0), (1, 8, 256, 7168, "bf16", "bf16", True, True, 0, 0),
     (63, 2, 8, 256, "f32", "f32", True, False, 0.4, 8), (40, 9, 16, 1040, "bf16", "f32", False, True, 0.3, 16),
     (7, 33, 64, 144, "f32", "bf16", True, True, 0.2, 0), (300, 6, 32, 2064, "bf16", "bf16", True, False, 0, 24),
-    (3, 70, 70, 528, "bf16", "bf16", False, True, 0.9, 0), (1500, 8, 64, 4096, "bf16", "bf16", True, True, 0, 0)]
+    (3, 70, 70, 528, "bf16", "bf16", False, True, 0.9, 0), (1500, 8, 64, 4096, "bf16", "bf16", True, True, 0, 0),
+    # short lists, of which several windows of columns go at once
+    (90, 2, 8, 2064, "bf16", "bf16", True, True, 0.2, 8), (33, 1, 4, 1040, "bf16", "f32", True, False, 0, 0),
+    (50, 3, 5, 1296, "bf16", "bf16", False, True, 0.3, 0), (700, 4, 9, 4112, "bf16", "f32", True, True, 0.1, 16),
+    (41, 2, 8, 1040, "f32", "bf16", True, True, 0.2, 0), (300, 1, 8, 7168, "f32", "f32", False, True, 0, 8)]
 
 
 @pytest.mark.parametrize("t,s,e,k,dt,odt,res,weights,drop,pad", COMBINE)
@@ -268,7 +272,11 @@ GRAD = [  # t, s, e, k, dt, dydt, sfmt, fmt, dw, weights, drop, pad
     (19, 2, 8, 2064, "f32", "f32", 0, 1, True, True, 0.3, 8), (50, 9, 16, 144, "bf16", "f32", 1, 0, True, True, 0.3, 0),
     (7, 33, 64, 528, "f32", "bf16", 0, 0, True, False, 0.2, 16), (300, 6, 32, 1040, "bf16", "bf16", 1, 1, False, True, 0, 0),
     (3, 70, 70, 640, "bf16", "bf16", 0, 0, True, True, 0.8, 0), (800, 8, 64, 4096, "bf16", "bf16", 0, 0, True, True, 0, 0),
-    (5, 4, 8, 16384, "bf16", "f32", 0, 0, True, True, 0, 0)]
+    (5, 4, 8, 16384, "bf16", "f32", 0, 0, True, True, 0, 0),
+    # short lists, of which several windows of columns go at once
+    (90, 2, 8, 2064, "bf16", "bf16", 0, 0, True, True, 0.2, 8), (33, 1, 4, 1040, "bf16", "f32", 1, 1, True, False, 0, 0),
+    (50, 3, 5, 1296, "bf16", "bf16", 0, 1, True, True, 0.3, 0), (700, 4, 9, 4112, "bf16", "f32", 0, 0, True, True, 0.1, 16),
+    (300, 1, 8, 7168, "f32", "bf16", 0, 0, True, True, 0, 8), (64, 2, 8, 16384, "bf16", "bf16", 0, 0, True, True, 0, 0)]
 
 
 @pytest.mark.parametrize("t,s,e,k,dt,dydt,sfmt,fmt,dw,weights,drop,pad", GRAD)
@@ -326,7 +334,7 @@ def test_combine_backward(t, s, e, k, dt, dydt, sfmt, fmt, dw, weights, drop, pa
         mag = torch.zeros_like(want)
         prod = dy.double()[tok] * x.double()[at]
         want[pair], mag[pair] = prod.sum(1), prod.abs().sum(1)
-        assert ((dwv.double().view(-1) - want).abs() <= 64 * 2.0 ** -24 * mag + 1e-40).all()
+        assert ((dwv.double().view(-1) - want).abs() <= 80 * 2.0 ** -24 * mag + 1e-40).all()
         alone = torch.empty_like(dwv)
         F.fp8_experts_combine_backward(pitched(dy, pad), rows, w, x=pitched(x, pad), d_weights=alone)
         assert torch.equal(alone, dwv)
@@ -405,7 +413,7 @@ def test_rows_beyond_32_bit_offsets():
     dw = torch.empty((2, 2), device="cuda")
     F.fp8_experts_combine_backward(x, rows, None, x=out, d_weights=dw, q=q, scales=sc)
     want = (x.double() ** 2).sum(1)
-    assert ((dw.double() - want[:, None]).abs() <= 64 * 2.0 ** -24 * want[:, None]).all()
+    assert ((dw.double() - want[:, None]).abs() <= 80 * 2.0 ** -24 * want[:, None]).all()
 
 
 def chain(F, ids, x, w, e, bufs):
