@@ -13,6 +13,9 @@
 // 2 + 2.06 in, 2 out.  A CTA takes tiles of 32 rows by 128 columns, a row's
 // group on eight lanes of 16 elements each (32-byte accesses, and the scales of
 // a tile are 32 neighbours of the group-major layout); tiles go by column first.
+// 16384 x 14336 gated: forward 260 us (94% of the copy rate), backward 231 (92%).
+// Gelu is bound by its instructions (without a gate 203 us both ways, where silu
+// takes 155 and 149).
 #include "act_checkpoint.h"
 #include "activation.cuh"
 #include "common.cuh"
@@ -41,16 +44,6 @@ __device__ __forceinline__ void act_both2(F2 z, F2 &value, F2 &slope) {
     slope = act_slope2<A>(z);
   }
 }
-// The bounded forms, for values of any size; out of line.
-template <int A>
-__device__ __noinline__ uint64_t act_value_any(uint64_t z) {
-  return act_value2<A>(F2(z)).v;
-}
-template <int A>
-__device__ __noinline__ uint64_t act_slope_any(uint64_t z) {
-  return act_slope2<A>(F2(z)).v;
-}
-
 // Eight pairs of the activation's values from raw bf16 arguments.  silu and the
 // tanh form need their argument bounded on the left (-inf times a factor that has
 // vanished): two at a time on the bf16 pair.
@@ -97,9 +90,17 @@ __device__ __forceinline__ F2 e4m3_pair(uint32_t two) {
       : "r"(h2));
   return F2(lo, hi);
 }
-__device__ __forceinline__ float kept_scale(const void *scales, int64_t at, int sfmt) {
-  return sfmt == 0 ? static_cast<const float *>(scales)[at]
-                   : exp2_int((int)static_cast<const uint8_t *>(scales)[at] - 127);
+// A checkpoint's scale as loaded (KEPT 0: fp32 bits, 1: the UE8M0 byte; nothing is
+// done with it before the tile that it was loaded ahead for), and its value.
+template <int KEPT>
+__device__ __forceinline__ uint32_t kept_bits(const void *scales, int64_t at) {
+  if constexpr (KEPT == 0) return static_cast<const uint32_t *>(scales)[at];
+  return static_cast<const uint8_t *>(scales)[at];
+}
+template <int KEPT>
+__device__ __forceinline__ float kept_scale(uint32_t bits) {
+  if constexpr (KEPT == 0) return __uint_as_float(bits);
+  return __uint_as_float(max(bits << 23, 0x00400000u));  // 2^(e - 127)
 }
 // the i-th pair of 16 codes under their scale
 __device__ __forceinline__ F2 kept_pair(const uint4 &c, int i, F2 s) {
@@ -145,10 +146,12 @@ struct TileWalk {
   }
 };
 
-// Threads of a CTA, and CTAs that share an SM (85 registers a thread: the next
-// tile's operands wait in registers.  Without them, and 64 registers, the backward
-// pass of 16384 x 14336 took 254 us instead of 234, the forward pass 263 for 260).
-constexpr int kTileThreads = 256, kForwardCtas = 3, kGradCtas = 3;
+// Threads of a CTA, and CTAs that share an SM.  With a gate three (85 registers a
+// thread: the next tile's operands wait in registers; 16384 x 14336 in 260 us
+// forward and 231 backward, 287 and 281 on four, which spill); without one four
+// (silu 155 us forward and 149 backward, 181 and 160 on three).
+constexpr int kTileThreads = 256;
+constexpr int ctas_per_sm(bool gate) { return gate ? 3 : 4; }
 
 // 16 values from p, or zeros
 __device__ __forceinline__ Words16 load16(const __nv_bfloat16 *p, bool in) {
@@ -160,44 +163,52 @@ __device__ __forceinline__ Words16 load16(const __nv_bfloat16 *p, bool in) {
   return v;
 }
 
-// Codes of 16 results under the scale of their group (group: 8 lanes), stored
-// with it.
-template <int F>
-__device__ __forceinline__ void put_group(const F2 (&y)[8], float amax, int sfmt, uint8_t *q,
-                                          void *scales, int64_t at, bool in, bool owner) {
-  const float top = __uint_as_float(group8_max(__float_as_uint(amax)));
-  GroupScale g = group_scale<F>(top, sfmt);
-  uint4 c;
-  if (__all_sync(0xffffffffu, g.fast)) {
-    c = codes16_times<F>(y, g.inv);
-  } else {
-    g = group_scale_any<F>(top, sfmt);
-    c = codes16_any<F>(y, g.s);
-  }
-  if (owner) store_scale(scales, at, g.stored, sfmt);
-  if (in) *reinterpret_cast<uint4 *>(q) = c;
-}
-// Under the tensor's scale d, the maximum into `top`.
-template <int F>
-__device__ __forceinline__ void put_tensor(const F2 (&y)[8], const CodeScale &d, float &top,
-                                           uint8_t *q, bool in) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) top = max_abs2(top, y[i]);
-  const uint4 c = d.fast ? codes16_times<F>(y, d.inv) : codes16_any<F>(y, d.s);
-  if (in) *reinterpret_cast<uint4 *>(q) = c;
-}
 __device__ __forceinline__ float max_abs16(const F2 (&y)[8]) {
   float m = 0.0f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) m = max_abs2(m, y[i]);
   return m;
 }
+__device__ __forceinline__ void pairs_of(const Words16 &v, F2 (&x)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = v.pair(i);
+}
+__device__ __forceinline__ void put16(uint8_t *q, const uint4 &c, bool in) {
+  if (in) *reinterpret_cast<uint4 *>(q) = c;
+}
 
+// The kernels' loops hold the common case: scales far from the ends of fp32
+// (GroupScale::fast) and, backward, checkpoints of values below 2^49.  A warp whose
+// four rows of a tile are another case leaves them, and goes over its tiles again
+// behind its loop, out of line, with IEEE quotients and bounded
+// activations.  (The same code inside the loop cost the backward pass 30 us of 262:
+// registers kept across its calls.)
+
+// Codes of 16 results under the scale of their group (group: 8 lanes), stored
+// with it; false where the scale is not of the common case.
+template <int F>
+__device__ __forceinline__ bool put_group(const F2 (&y)[8], float amax, int sfmt, uint8_t *q,
+                                          void *scales, int64_t at, bool in, bool owner) {
+  const float top = __uint_as_float(group8_max(__float_as_uint(amax)));
+  const GroupScale g = group_scale<F>(top, sfmt);
+  if (!__all_sync(0xffffffffu, g.fast)) return false;
+  if (owner) store_scale(scales, at, g.stored, sfmt);
+  put16(q, codes16_times<F>(y, g.inv), in);
+  return true;
+}
+template <int F>
+__device__ __forceinline__ void put_group_any(const F2 (&y)[8], float amax, int sfmt, uint8_t *q,
+                                              void *scales, int64_t at, bool in, bool owner) {
+  const GroupScale g =
+      group_scale_any<F>(__uint_as_float(group8_max(__float_as_uint(amax))), sfmt);
+  if (owner) store_scale(scales, at, g.stored, sfmt);
+  put16(q, codes16_any<F>(y, g.s), in);
+}
 // Two results of the same group at once: the first step of the reduction leaves
 // the maximum of y to even lanes and that of z to odd ones, so that each lane
 // forms one scale instead of two.
 template <int F>
-__device__ __forceinline__ void put_groups(const F2 (&y)[8], const F2 (&z)[8], int sfmt,
+__device__ __forceinline__ bool put_groups(const F2 (&y)[8], const F2 (&z)[8], int sfmt,
                                            uint8_t *qy, uint8_t *qz, void *sy, void *sz, int64_t at,
                                            bool in, bool live) {
   const bool odd = threadIdx.x & 1u;
@@ -206,31 +217,86 @@ __device__ __forceinline__ void put_groups(const F2 (&y)[8], const F2 (&z)[8], i
   key = max(key, __shfl_xor_sync(0xffffffffu, odd ? ky : kz, 1));
   key = max(key, __shfl_xor_sync(0xffffffffu, key, 2));
   key = max(key, __shfl_xor_sync(0xffffffffu, key, 4));
-  const float top = __uint_as_float(key);
-  GroupScale g = group_scale<F>(top, sfmt);
-  const bool fast = __all_sync(0xffffffffu, g.fast);
-  if (!fast) g = group_scale_any<F>(top, sfmt);
-  const float mine = fast ? g.inv : g.s, other = __shfl_xor_sync(0xffffffffu, mine, 1);
-  const float fy = odd ? other : mine, fz = odd ? mine : other;
+  const GroupScale g = group_scale<F>(__uint_as_float(key), sfmt);
+  if (!__all_sync(0xffffffffu, g.fast)) return false;
+  const float other = __shfl_xor_sync(0xffffffffu, g.inv, 1);
   if (live && (threadIdx.x & 7u) < 2u) store_scale(odd ? sz : sy, at, g.stored, sfmt);
-  const uint4 cy = fast ? codes16_times<F>(y, fy) : codes16_any<F>(y, fy);
-  if (in) *reinterpret_cast<uint4 *>(qy) = cy;
-  const uint4 cz = fast ? codes16_times<F>(z, fz) : codes16_any<F>(z, fz);
-  if (in) *reinterpret_cast<uint4 *>(qz) = cz;
+  put16(qy, codes16_times<F>(y, odd ? other : g.inv), in);
+  put16(qz, codes16_times<F>(z, odd ? g.inv : other), in);
+  return true;
+}
+// Under the tensor's scale d, the maximum into `top`.
+template <int F>
+__device__ __forceinline__ void put_tensor(const F2 (&y)[8], const CodeScale &d, float &top,
+                                           uint8_t *q, bool in) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) top = max_abs2(top, y[i]);
+  put16(q, codes16_times<F>(y, d.inv), in);
+}
+template <int F>
+__device__ __forceinline__ void put_tensor_any(const F2 (&y)[8], const CodeScale &d, float &top,
+                                               uint8_t *q, bool in) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) top = max_abs2(top, y[i]);
+  put16(q, codes16_any<F>(y, d.s), in);
 }
 
-// The checkpoint of 16 bf16 values.
-__device__ __forceinline__ void keep16(const Words16 &v, uint8_t *q, void *scales, int64_t at,
-                                       int sfmt, bool in, bool owner) {
-  F2 x[8];
+// The activation by its number.
+__device__ __noinline__ uint64_t act_value_any(uint64_t z, int act) {
+  F2 r(z);
+  with_act<true>(act, [&](auto a) { r = act_value2<a.value>(F2(z)); });
+  return r.v;
+}
+__device__ __noinline__ uint64_t act_slope_any(uint64_t z, int act) {
+  F2 r(1.0f);
+  with_act(act, [&](auto a) { r = act_slope2<a.value>(F2(z)); });
+  return r.v;
+}
+
+// This warp's tiles that its loop left, found by the bit TileWalk::left % 32 (tiles
+// that share it are done again, to the same values within a rounding).
+template <int F>
+__device__ __noinline__ float act_slow_walk(const ActArgs &a, uint32_t rows, float top,
+                                             uint32_t slow) {
+  const __nv_bfloat16 *h = static_cast<const __nv_bfloat16 *>(a.h);
+  const __nv_bfloat16 *u = static_cast<const __nv_bfloat16 *>(a.u);
+  const uint32_t N = (uint32_t)a.N;
+  const CodeScale d(a.scale != nullptr ? *a.scale : 1.0f);
+#pragma unroll 1
+  for (TileWalk t(rows, N); t.left > 0; t.next()) {
+    if (((slow >> (t.left & 31)) & 1u) == 0u) continue;
+    const int64_t at = t.scale_at(a.M), flat = t.at(a.N);
+    const bool in = t.row < rows && t.col() < N, owner = t.row < rows && (threadIdx.x & 7u) == 0u;
+    const Words16 hv = load16(h + t.at(a.ldh), in);
+    Words16 uv = hv;
+    if (u != nullptr) uv = load16(u + t.at(a.ldu), in);
+    F2 y[8], x[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = v.pair(i);
-  put_group<0>(x, v.max_abs(), sfmt, q, scales, at, in, owner);
+    for (int i = 0; i < 8; ++i) {
+      y[i] = F2(act_value_any(hv.pair(i).v, a.act));
+      if (u != nullptr) y[i] = y[i] * uv.pair(i);
+    }
+    if (a.hq != nullptr) {
+      pairs_of(hv, x);
+      put_group_any<0>(x, hv.max_abs(), a.keep_sfmt, a.hq + flat, a.hs, at, in, owner);
+    }
+    if (a.uq != nullptr) {
+      pairs_of(uv, x);
+      put_group_any<0>(x, uv.max_abs(), a.keep_sfmt, a.uq + flat, a.us, at, in, owner);
+    }
+    if (a.out != nullptr && in)
+      store16(static_cast<__nv_bfloat16 *>(a.out) + t.at(a.ld_out), y);
+    if (a.scale != nullptr)
+      put_tensor_any<F>(y, d, top, a.q + flat, in);
+    else
+      put_group_any<F>(y, max_abs16(y), a.sfmt, a.q + flat, a.scales, at, in, owner);
+  }
+  return top;
 }
 
 template <int A, bool GATE, int F>
-__global__ void __launch_bounds__(kTileThreads, kForwardCtas)
-    act_checkpoint_kernel(const ActArgs a) {
+__global__ void __launch_bounds__(kTileThreads, ctas_per_sm(GATE))
+    act_checkpoint_kernel(const __grid_constant__ ActArgs a) {
   launch_dependents();
   grid_dependency_wait();
   const __nv_bfloat16 *h = static_cast<const __nv_bfloat16 *>(a.h);
@@ -238,7 +304,12 @@ __global__ void __launch_bounds__(kTileThreads, kForwardCtas)
   const uint32_t rows = live_rows(a.valid, a.M), N = (uint32_t)a.N;
   const CodeScale d(a.scale != nullptr ? *a.scale : 1.0f);
   float top = 0.0f;
+  uint32_t slow = 0u;
   TileWalk w(rows, N);
+  if (!d.fast) {
+    slow = ~0u;
+    w.left = 0;
+  }
   Words16 hn, un;  // the next tile's
   auto fetch = [&]() {
     const bool in = w.left > 0 && w.row < rows && w.col() < N;
@@ -256,9 +327,18 @@ __global__ void __launch_bounds__(kTileThreads, kForwardCtas)
     w.next();
     fetch();
     // (the checkpoints first: the results' registers are not needed for them)
-    if (a.hq != nullptr) keep16(hv, a.hq + flat, a.hs, at, a.keep_sfmt, in, owner);
-    if (GATE && a.uq != nullptr) keep16(uv, a.uq + flat, a.us, at, a.keep_sfmt, in, owner);
     F2 y[8];
+    bool fast = true;
+    if (a.hq != nullptr) {
+      pairs_of(hv, y);
+      fast = put_group<0>(y, hv.max_abs(), a.keep_sfmt, a.hq + flat, a.hs, at, in, owner);
+      if constexpr (GATE) {
+        if (a.uq != nullptr) {
+          pairs_of(uv, y);
+          fast &= put_group<0>(y, uv.max_abs(), a.keep_sfmt, a.uq + flat, a.us, at, in, owner);
+        }
+      }
+    }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       y[i] = act_of_word<A>(hv.word(i));
@@ -269,17 +349,71 @@ __global__ void __launch_bounds__(kTileThreads, kForwardCtas)
     if (a.scale != nullptr)
       put_tensor<F>(y, d, top, a.q + flat, in);
     else
-      put_group<F>(y, max_abs16(y), a.sfmt, a.q + flat, a.scales, at, in, owner);
+      fast &= put_group<F>(y, max_abs16(y), a.sfmt, a.q + flat, a.scales, at, in, owner);
+    if (!fast) slow |= 1u << (t.left & 31);
   }
+  if (slow != 0u) top = act_slow_walk<F>(a, rows, top, slow);
   if (a.amax != nullptr) block_max_to(__float_as_uint(top), a.amax);
 }
 
-// The fast forms hold for checkpoints of values up to this.
+// The loop's forms hold for checkpoints of values up to this.
 constexpr float kKeptScaleMax = 0x1p40f;
 
-template <int A, bool GATE, int F>
-__global__ void __launch_bounds__(kTileThreads, kGradCtas)
-    act_checkpoint_grad_kernel(const ActGradArgs a) {
+// This warp's tiles that its loop left, found by the bit TileWalk::left % 32 (tiles
+// that share it are done again, to the same values within a rounding).
+template <int F>
+__device__ __noinline__ void act_grad_slow_walk(const ActGradArgs &a, uint32_t rows, uint32_t slow,
+                                                float &top_h, float &top_u) {
+  const __nv_bfloat16 *da = static_cast<const __nv_bfloat16 *>(a.da);
+  const uint32_t N = (uint32_t)a.N;
+  const bool gate = a.uq != nullptr;
+  const CodeScale dh(a.scale_h != nullptr ? *a.scale_h : 1.0f);
+  const CodeScale du(a.scale_u != nullptr ? *a.scale_u : 1.0f);
+#pragma unroll 1
+  for (TileWalk t(rows, N); t.left > 0; t.next()) {
+    if (((slow >> (t.left & 31)) & 1u) == 0u) continue;
+    const int64_t at = t.scale_at(a.M), flat = t.at(a.N);
+    const bool in = t.row < rows && t.col() < N, owner = t.row < rows && (threadIdx.x & 7u) == 0u;
+    const Words16 v = load16(da + t.at(a.ld_da), in);
+    Vec16<uint8_t> hc, uc;
+    hc.zero();
+    uc.zero();
+    float hs = 0.0f, us = 0.0f;
+    if (in) {
+      hc.load(a.hq + flat);
+      if (gate) uc.load(a.uq + flat);
+      hs = a.keep_sfmt == 0 ? kept_scale<0>(kept_bits<0>(a.hs, at))
+                            : kept_scale<1>(kept_bits<1>(a.hs, at));
+      if (gate)
+        us = a.keep_sfmt == 0 ? kept_scale<0>(kept_bits<0>(a.us, at))
+                              : kept_scale<1>(kept_bits<1>(a.us, at));
+    }
+    F2 yh[8], yu[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const F2 z = kept_pair(hc.w[0], i, F2(hs)), g = v.pair(i);
+      yu[i] = g * F2(act_value_any(z.v, a.act));
+      const F2 slope(act_slope_any(z.v, a.act));
+      yh[i] = gate ? g * kept_pair(uc.w[0], i, F2(us)) * slope : g * slope;
+    }
+    if (a.dh != nullptr && in) store16(static_cast<__nv_bfloat16 *>(a.dh) + t.at(a.ld_d), yh);
+    if (a.du != nullptr && in) store16(static_cast<__nv_bfloat16 *>(a.du) + t.at(a.ld_d), yu);
+    const int64_t qat = t.at(a.ld_q);
+    if (a.tensor != 0) {
+      if (a.qh != nullptr) put_tensor_any<F>(yh, dh, top_h, a.qh + qat, in);
+      if (a.qu != nullptr) put_tensor_any<F>(yu, du, top_u, a.qu + qat, in);
+    } else {
+      if (a.qh != nullptr)
+        put_group_any<F>(yh, max_abs16(yh), a.sfmt, a.qh + qat, a.sh, at, in, owner);
+      if (a.qu != nullptr)
+        put_group_any<F>(yu, max_abs16(yu), a.sfmt, a.qu + qat, a.su, at, in, owner);
+    }
+  }
+}
+
+template <int A, bool GATE, int F, int KEPT>
+__global__ void __launch_bounds__(kTileThreads, ctas_per_sm(GATE))
+    act_checkpoint_grad_kernel(const __grid_constant__ ActGradArgs a) {
   launch_dependents();
   grid_dependency_wait();
   const __nv_bfloat16 *da = static_cast<const __nv_bfloat16 *>(a.da);
@@ -288,23 +422,28 @@ __global__ void __launch_bounds__(kTileThreads, kGradCtas)
   const CodeScale dh(a.scale_h != nullptr ? *a.scale_h : 1.0f);
   const CodeScale du(a.scale_u != nullptr ? *a.scale_u : 1.0f);
   float top_h = 0.0f, top_u = 0.0f;
+  uint32_t slow = 0u;
   TileWalk w(rows, N);
+  if (!(dh.fast && du.fast)) {
+    slow = ~0u;
+    w.left = 0;
+  }
   Words16 vn;  // the next tile's operands
   Vec16<uint8_t> hn, un;
-  float hsn = 0.0f, usn = 0.0f;
+  uint32_t hsn = 0u, usn = 0u;
   auto fetch = [&]() {
     const int64_t at = w.scale_at(a.M), flat = w.at(a.N);
     const bool in = w.left > 0 && w.row < rows && w.col() < N;
     vn = load16(da + w.at(a.ld_da), in);
     hn.zero();
     un.zero();
-    hsn = usn = 0.0f;
+    hsn = usn = 0u;
     if (in) {
       hn.load(a.hq + flat);
-      hsn = kept_scale(a.hs, at, a.keep_sfmt);
+      hsn = kept_bits<KEPT>(a.hs, at);
       if constexpr (GATE) {
         un.load(a.uq + flat);
-        usn = kept_scale(a.us, at, a.keep_sfmt);
+        usn = kept_bits<KEPT>(a.us, at);
       }
     }
   };
@@ -315,49 +454,50 @@ __global__ void __launch_bounds__(kTileThreads, kGradCtas)
     const bool in = t.row < rows && t.col() < N;
     const Words16 v = vn;
     const Vec16<uint8_t> hc = hn, uc = un;
-    const float hs = hsn, us = usn;
+    const float hs = kept_scale<KEPT>(hsn), us = kept_scale<KEPT>(usn);
     w.next();
     fetch();
-    F2 yh[8], yu[8];
-    if (__all_sync(0xffffffffu, hs <= kKeptScaleMax)) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) act_both2<A>(kept_pair(hc.w[0], i, F2(hs)), yu[i], yh[i]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const F2 z = kept_pair(hc.w[0], i, F2(hs));
-        yu[i] = F2(act_value_any<A>(z.v));
-        yh[i] = F2(act_slope_any<A>(z.v));
-      }
+    if (!__all_sync(0xffffffffu, hs <= kKeptScaleMax)) {
+      slow |= 1u << (t.left & 31);
+      continue;
     }
-    if constexpr (GATE) {
+    F2 yh[8], yu[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const F2 g = v.pair(i);
+    for (int i = 0; i < 8; ++i) {
+      act_both2<A>(kept_pair(hc.w[0], i, F2(hs)), yu[i], yh[i]);
+      const F2 g = v.pair(i);
+      if constexpr (GATE) {
         yh[i] = g * kept_pair(uc.w[0], i, F2(us)) * yh[i];
         yu[i] = g * yu[i];
+      } else {
+        yh[i] = g * yh[i];
       }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) yh[i] = v.pair(i) * yh[i];
     }
     if (a.dh != nullptr && in) store16(static_cast<__nv_bfloat16 *>(a.dh) + t.at(a.ld_d), yh);
     if (GATE && a.du != nullptr && in)
       store16(static_cast<__nv_bfloat16 *>(a.du) + t.at(a.ld_d), yu);
     const int64_t qat = t.at(a.ld_q);
     const bool live = t.row < rows;
+    bool fast = true;
     if (tensor) {
       if (a.qh != nullptr) put_tensor<F>(yh, dh, top_h, a.qh + qat, in);
       if (GATE && a.qu != nullptr) put_tensor<F>(yu, du, top_u, a.qu + qat, in);
     } else if (GATE && a.qh != nullptr && a.qu != nullptr) {
-      put_groups<F>(yh, yu, a.sfmt, a.qh + qat, a.qu + qat, a.sh, a.su, at, in, live);
+      fast = put_groups<F>(yh, yu, a.sfmt, a.qh + qat, a.qu + qat, a.sh, a.su, at, in, live);
     } else {
       const bool owner = live && (threadIdx.x & 7u) == 0u;
       if (a.qh != nullptr)
-        put_group<F>(yh, max_abs16(yh), a.sfmt, a.qh + qat, a.sh, at, in, owner);
+        fast = put_group<F>(yh, max_abs16(yh), a.sfmt, a.qh + qat, a.sh, at, in, owner);
       if (GATE && a.qu != nullptr)
-        put_group<F>(yu, max_abs16(yu), a.sfmt, a.qu + qat, a.su, at, in, owner);
+        fast &= put_group<F>(yu, max_abs16(yu), a.sfmt, a.qu + qat, a.su, at, in, owner);
     }
+    if (!fast) slow |= 1u << (t.left & 31);
+  }
+  if (slow != 0u) {
+    float th = top_h, tu = top_u;
+    act_grad_slow_walk<F>(a, rows, slow, th, tu);
+    top_h = th;
+    top_u = tu;
   }
   if (a.amax_h != nullptr) block_max_to(__float_as_uint(top_h), a.amax_h);
   if (GATE && a.amax_u != nullptr) {
@@ -414,7 +554,7 @@ static void each_act(int act, Fn &&f) {
 cudaError_t launch_act_checkpoint(const ActArgs &a, int sms, cudaStream_t st) {
   cudaError_t e = clear_maxima(a.amax, nullptr, st);
   if (e != cudaSuccess || a.M == 0) return e;
-  const int64_t blocks = tile_blocks(a.M, a.N, (int64_t)sms * kForwardCtas);
+  const int64_t blocks = tile_blocks(a.M, a.N, (int64_t)sms * ctas_per_sm(a.u != nullptr));
   each_act(a.act, [&](auto act) {
     with_gate(a.u != nullptr, a.fmt, [&](auto gate, auto fmt) {
       e = launch_serial(act_checkpoint_kernel<act.value, gate.value, fmt.value>, blocks,
@@ -427,11 +567,14 @@ cudaError_t launch_act_checkpoint(const ActArgs &a, int sms, cudaStream_t st) {
 cudaError_t launch_act_checkpoint_grad(const ActGradArgs &a, int sms, cudaStream_t st) {
   cudaError_t e = clear_maxima(a.amax_h, a.amax_u, st);
   if (e != cudaSuccess || a.M == 0) return e;
-  const int64_t blocks = tile_blocks(a.M, a.N, (int64_t)sms * kGradCtas);
+  const int64_t blocks = tile_blocks(a.M, a.N, (int64_t)sms * ctas_per_sm(a.uq != nullptr));
   each_act(a.act, [&](auto act) {
     with_gate(a.uq != nullptr, a.fmt, [&](auto gate, auto fmt) {
-      e = launch_serial(act_checkpoint_grad_kernel<act.value, gate.value, fmt.value>, blocks,
-                        kTileThreads, st, a);
+      e = a.keep_sfmt == 0
+              ? launch_serial(act_checkpoint_grad_kernel<act.value, gate.value, fmt.value, 0>, blocks,
+                              kTileThreads, st, a)
+              : launch_serial(act_checkpoint_grad_kernel<act.value, gate.value, fmt.value, 1>, blocks,
+                              kTileThreads, st, a);
     });
   });
   return e;
