@@ -320,6 +320,80 @@ def test_extreme_scales():
     check_group(q, sc, h.double(), torch.zeros_like(h.double()), 0, 0)
 
 
+@pytest.mark.parametrize("act,gate,fmt", [("silu", True, 0), ("gelu", False, 1)])
+def test_extreme_rows_among_many(act, gate, fmt):
+    """Rows whose scales leave the common range among rows that stay, where every
+    CTA walks over several tiles."""
+    F = lib()
+    m, n = 16389, 272
+    at = torch.tensor([0, 77, 5000, 9001, 16384, 16388], device="cuda")
+    by = torch.tensor([1e-32, 1e32, 1e32, 1e-32, 1e-32, 1e32], device="cuda")[:, None]
+    h, u = inputs(m, n, 21), inputs(m, n, 22) if gate else None
+    da, g = inputs(m, n, 23, 1e-3), 3
+    h[at] = (h[at].float() * by).to(BF)
+    da[at + 1 - 2 * (at == m - 1).long()] *= 1e-32
+
+    def run():
+        r = dict(q=fill((m, n), torch.uint8), scales=fill((g, m), torch.float32))
+        kept = {}
+        for x in ("h", "u") if gate else ("h",):
+            kept[x + "_q"], kept[x + "_scales"] = fill((m, n), torch.uint8), fill((g, m), torch.float32)
+            r["d%s_q" % x] = fill((m, n), torch.uint8)
+            r["d%s_scales" % x] = fill((g, m), torch.float32)
+        F.fp8_act_checkpoint(h, u, ACTS.index(act), r["q"], scales=r["scales"], fmt=fmt, **kept)
+        F.fp8_act_checkpoint_backward(da, ACTS.index(act), fmt=fmt, **kept,
+                                      **{k: v for k, v in r.items() if k[0] == "d"})
+        return {**r, **kept}
+
+    got = run()
+    hv, dv = kept_values(got["h_q"], got["h_scales"], 0), da.double()
+    check_kept(got["h_q"], got["h_scales"], h, 0)
+    y = value(h.double(), act) * (u.double() if gate else 1.0)
+    check_group(got["q"], got["scales"], y, REL * y.abs() + 1e-38, fmt, 0)
+    sl = slope(hv, act)
+    dh, err = dv * sl, REL * dv.abs() * sl.abs().clamp_min(1.0)
+    if gate:
+        uv = kept_values(got["u_q"], got["u_scales"], 0)
+        check_kept(got["u_q"], got["u_scales"], u, 0)
+        dh, err = dh * uv, err * uv.abs()
+        du = dv * value(hv, act)
+        check_group(got["du_q"], got["du_scales"], du, REL * du.abs() + 1e-38, fmt, 0)
+    check_group(got["dh_q"], got["dh_scales"], dh, err + 1e-38, fmt, 0)
+
+
+@pytest.mark.parametrize("act,gate,fmt", [("silu", True, 0), ("relu2", False, 1)])
+def test_extreme_tensor_scales(act, gate, fmt):
+    """Per-tensor scales beyond the range of the rounded reciprocal."""
+    F = lib()
+    m, n = 1000, 272
+    h, u = inputs(m, n, 31), inputs(m, n, 32) if gate else None
+    q, amax = fill((m, n), torch.uint8), fill((1,), torch.float32)
+    kept, outs, kw, vals = {}, {}, {}, {}
+    for name, x in zip(("h", "u"), (h, u)):
+        if x is None:
+            continue
+        kept[name + "_q"], kept[name + "_scales"] = quantizer(x, 0)
+        vals[name] = kept_values(kept[name + "_q"], kept[name + "_scales"], 0)
+        outs["d%s_q" % name] = fill((m, n), torch.uint8)
+        kw["scale_d" + name] = torch.full((1,), 2e-31 / TOP[fmt], device="cuda")
+        kw["amax_d" + name] = fill((1,), torch.float32)
+    da = inputs(m, n, 33, 1e-3) * 1e-29
+    F.fp8_act_checkpoint_backward(da, ACTS.index(act), fmt=fmt, **kept, **outs, **kw)
+    dv, sl = da.double(), slope(vals["h"], act)
+    dh, err = dv * sl, REL * dv.abs() * sl.abs().clamp_min(1.0)
+    if gate:
+        dh, err = dh * vals["u"], err * vals["u"].abs()
+        du = dv * value(vals["h"], act)
+        check_tensor(outs["du_q"], kw["amax_du"], kw["scale_du"], du, REL * du.abs(), fmt)
+    check_tensor(outs["dh_q"], kw["amax_dh"], kw["scale_dh"], dh, err, fmt)
+    if gate:  # forward: the gate's rows carry the size
+        w = (u.float() * 1e-32).to(BF)
+        scale = torch.full((1,), 5e-32 / TOP[fmt], device="cuda")
+        F.fp8_act_checkpoint(h, w, ACTS.index(act), q, scale=scale, amax_out=amax, fmt=fmt)
+        y = value(h.double(), act) * w.double()
+        check_tensor(q, amax, scale, y, REL * y.abs(), fmt)
+
+
 def test_rows_beyond_32_bit_offsets():
     F = lib()
     m, n, first = 300016, 14400, 300000  # 4.3e9 elements
