@@ -778,7 +778,8 @@ __global__ void __launch_bounds__(32 * ring_warps(ring_stage<X, DY, W>()), 3)
       if ((int)threadIdx.x < n) {
         float all = 0.0f;
         for (uint32_t i = 0; i < nw; ++i) all += part[phase][i][threadIdx.x];
-        a.dw[cur.t * S + cur.s0 + threadIdx.x] = all;
+        // (a dropped pair's sum would be dy's infinities times zeros)
+        a.dw[cur.t * S + cur.s0 + threadIdx.x] = kept >> threadIdx.x & 1u ? all : 0.0f;
       }
       phase ^= 1;
     }

@@ -11,6 +11,8 @@ of the product, the maximum's product, the scale, its reciprocal and the
 quotient, below 2^-21 together, and half a step of the format.  gather forms the
 exact quotient: the bytes themselves are checked.
 """
+import math
+
 import pytest
 import torch
 
@@ -360,6 +362,26 @@ def test_combine_backward_extreme_scales():
     u = (v.double().view(4, 2, 128) / want.double()[:, :, None]).view(4, k)
     err = (q.view(F8[0]).double() - u).abs()
     assert (err <= half_step(u, 0) * (1 + 1e-6) + REL * u.abs()).all()
+
+
+@pytest.mark.parametrize("s,dt", [(2, torch.bfloat16), (5, torch.float32), (11, torch.bfloat16)])
+def test_dropped_pairs_beside_non_finite_gradients(s, dt):
+    """A dropped pair's dw is 0 whatever dy holds, and its neighbours' are the sums."""
+    F = lib()
+    t, k = 6, 528
+    ids = choices(t, s, 4, s, 0.4)
+    _, rows, _ = order(ids, 4)
+    x, dy = randn((t * s, k), dt, 1), randn((t, k), dt, 2)
+    dy[0, 3], dy[1, 300], dy[2, 527], dy[3] = math.inf, -math.inf, math.nan, math.inf
+    dw = filled((t, s), torch.float32)
+    F.fp8_experts_combine_backward(dy, rows, torch.ones((t, s), device="cuda"), x=x, d_weights=dw)
+    gone = rows < 0
+    assert gone.any() and (dw[gone] == 0).all()
+    assert not dw[:4][~gone[:4]].isfinite().any()
+    want = (dy.double()[:, None] * x.double()[rows.clamp_min(0).long()]).sum(2)
+    size = (dy.double()[:, None] * x.double()[rows.clamp_min(0).long()]).abs().sum(2)
+    ok = (dw.double() - want).abs() <= 80 * 2.0 ** -24 * size
+    assert ok[4:][~gone[4:]].all()
 
 
 def test_gather_is_the_transpose_of_combine():
