@@ -275,66 +275,90 @@ struct TaskWalk {
 };
 
 // ----------------------------------------------------------------- gather --
-// A warp per (token, 512 columns): lane l holds 16 consecutive elements, so
-// eight lanes form a 1x128 group and each lane stores 16 bytes of codes per
-// row.  The token's rows sit in the lanes, one each; a group's scale for eight
-// rows goes out in one store instruction, one row per lane of the group.
+// A warp per (token, W windows of 512 columns): lane l holds 16 consecutive
+// elements of each, so eight lanes form a 1x128 group and each lane stores 16 bytes
+// of codes per row.  The token's rows sit in the lanes, one each; a group's scale
+// for eight rows goes out in one store instruction, one row per lane of the group.
 //
-// Bound by HBM: 4096 tokens of 7168 bf16 columns to eight rows each in 47.4 us, 94%
+// Bound by HBM: 4096 tokens of 7168 bf16 columns to eight rows each in 46.5 us, 95%
 // of the copy rate (scattering the scales, four bytes per row and group, costs 2 to
-// 6 us of it).  Codes leave L2 first (plain stores: 52 us).  A resident grid that
-// loads the next task ahead of this one's stores was no faster (58 against 53 then).
-template <typename T, int F>
-__global__ void __launch_bounds__(256, 3) experts_gather_kernel(const GatherArgs a) {
+// 6 us of it).  Codes leave L2 first (plain stores: 52 us).  A resident grid was
+// slower (49 to 58 us, with the next task loaded ahead of this one's stores too),
+// and so were three CTAs an SM (47.2); fp32 rows of two windows take four (spills).
+template <typename T, int F, int W>
+__global__ void __launch_bounds__(256, sizeof(T) * W == 8 ? 4 : 5)
+    experts_gather_kernel(const GatherArgs a) {
   constexpr bool kCodes = sizeof(T) == 1;
   launch_dependents();
   grid_dependency_wait();
-  const uint32_t l = lane_id();
-  const float mx = fmt_max(F);
-  for (TaskWalk w(a.K, 512); w.t < a.T; w.next()) {
-    const int64_t t = w.t, k = (int64_t)w.win * 512 + l * 16, g = k >> 7;
-    const bool in = k < a.K;
-    int32_t mine = l < a.S ? a.rows[t * a.S + l] : -1;
-    Vec16<T> v;
-    v.zero();
-    if (in) v.load(static_cast<const T *>(a.x) + t * a.ldx + k);
-    uint4 c = make_uint4(0u, 0u, 0u, 0u);
-    uint32_t scale = 0u;  // bits of the fp32 scale, or the UE8M0 byte
-    if constexpr (kCodes) {
-      c = v.w[0];
-      if (128 * g < a.K)  // (in a ragged last group also on the lanes past the row's end)
-        scale = a.sfmt == 0 ? static_cast<const uint32_t *>(a.x_scales)[g * a.T + t]
-                            : static_cast<const uint8_t *>(a.x_scales)[g * a.T + t];
-    } else if (a.q != nullptr) {
-      const float amax = __uint_as_float(group8_max(v.max_key()));
-      if (a.sfmt == 0) {
-        const float s = scale_from_amax(amax, mx);
-        scale = __float_as_uint(s);
-        c = v.template codes<F>(ScaleDiv(s));
-      } else {
-        const int e = ue8m0_exponent(amax, mx);
-        scale = (uint32_t)(e + 127);
-        c = v.template codes_pow2<F>(exp2_int(-e));
+  const uint32_t l = lane_id(), S = (uint32_t)a.S, K = (uint32_t)a.K, M = (uint32_t)a.M;
+  for (TaskWalk w(a.K, 512 * W); w.t < a.T; w.next()) {
+    const uint32_t t = (uint32_t)w.t, k0 = (uint32_t)w.win * (512 * W) + l * 16;
+    const int32_t *list = a.rows + (uint64_t)t * S;
+    uint32_t mine = l < S ? (uint32_t)list[l] : 0xffffffffu;  // (a negative row: none)
+    const T *x = static_cast<const T *>(a.x) + (uint64_t)t * (uint32_t)a.ldx + k0;
+    Vec16<T> v[W];
+    uint4 c[W];
+    uint32_t scale[W];  // bits of the fp32 scale, or the UE8M0 byte
+#pragma unroll
+    for (int u = 0; u < W; ++u) {
+      const uint32_t k = k0 + 512 * u, g = k >> 7;
+      v[u].zero();
+      scale[u] = 0u;
+      if (k < K) v[u].load(x + 512 * u);
+      if (kCodes && 128 * g < K) {  // (in a ragged last group also on the lanes past the row's end)
+        const uint64_t at = (uint64_t)g * (uint32_t)a.T + t;
+        scale[u] = a.sfmt == 0 ? static_cast<const uint32_t *>(a.x_scales)[at]
+                               : static_cast<const uint8_t *>(a.x_scales)[at];
       }
     }
-    for (int64_t s0 = 0; s0 < a.S; s0 += 32) {
-      const int n = (int)min((int64_t)32, a.S - s0);
-      if (s0 > 0) mine = (int)l < n ? a.rows[t * a.S + s0 + l] : -1;
-      if (mine >= a.M) mine = -1;
-      for (int s = 0; s < n; s += 8) {
-        int32_t row[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) row[j] = __shfl_sync(0xffffffffu, mine, s + j);
-        const int32_t lane_row = __shfl_sync(0xffffffffu, mine, s + (int)(l & 7u));
+    for (int u = 0; u < W; ++u) {
+      if constexpr (kCodes) {
+        c[u] = v[u].w[0];
+      } else if (a.q != nullptr) {
+        const float amax = __uint_as_float(group8_max(v[u].max_key()));
+        GroupScale gs = group_scale<F>(amax, a.sfmt);
+        const ScaleDiv d(gs.s);
+        if (__all_sync(0xffffffffu, gs.fast && (a.sfmt != 0 || d.fast))) {
+          c[u] = a.sfmt == 0 ? v[u].template codes_own<F>(d) : v[u].template codes_pow2<F>(gs.inv);
+        } else {
+          gs = group_scale_any<F>(amax, a.sfmt);
+          F2 y[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          if (row[j] < 0 || !in) continue;
-          if (a.q != nullptr) __stcs(reinterpret_cast<uint4 *>(a.q + row[j] * a.K + k), c);
-          if constexpr (!kCodes)
-            if (a.out != nullptr) v.store(static_cast<T *>(a.out) + row[j] * a.ld_out + k);
+          for (int i = 0; i < 8; ++i) y[i] = v[u].pair(i);
+          c[u] = codes16_any<F>(y, gs.s);
         }
-        if (a.q != nullptr && lane_row >= 0 && 128 * g < a.K)
-          store_scale(a.scales, g * a.M + lane_row, scale, a.sfmt);
+        scale[u] = gs.stored;
+      }
+    }
+    for (uint32_t s0 = 0; s0 < S; s0 += 32) {
+      const uint32_t n = min(32u, S - s0);
+      if (s0 > 0) mine = l < n ? (uint32_t)list[s0 + l] : 0xffffffffu;
+      for (uint32_t s = 0; s < n; s += 8) {
+        const uint32_t lane_row = __shfl_sync(0xffffffffu, mine, s + (l & 7u));
+#pragma unroll
+        for (uint32_t j = 0; j < 8; ++j) {
+          if (s + j >= n) break;
+          const uint32_t row = __shfl_sync(0xffffffffu, mine, s + j);
+          if (row >= M) continue;
+#pragma unroll
+          for (int u = 0; u < W; ++u) {
+            const uint32_t k = k0 + 512 * u;
+            if (k >= K) continue;
+            if (a.q != nullptr)
+              __stcs(reinterpret_cast<uint4 *>(a.q + (uint64_t)row * K + k), c[u]);
+            if constexpr (!kCodes)
+              if (a.out != nullptr)
+                v[u].store(static_cast<T *>(a.out) + (uint64_t)row * (uint32_t)a.ld_out + k);
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < W; ++u) {
+          const uint32_t k = k0 + 512 * u, g = k >> 7;
+          if (a.q != nullptr && lane_row < M && 128 * g < K)
+            store_scale(a.scales, (uint64_t)g * M + lane_row, scale[u], a.sfmt);
+        }
       }
     }
   }
@@ -345,21 +369,30 @@ static int64_t grid_of(int64_t warps, int per_block, int64_t most) {
   return blocks < 1 ? 1 : blocks < most ? blocks : most;
 }
 
+template <typename T, int F, int W>
+static cudaError_t run_gather(const GatherArgs &a, int sms, cudaStream_t st) {
+  const int64_t tasks = a.T * ((a.K + 512 * W - 1) / (512 * W));
+  return launch_serial(experts_gather_kernel<T, F, W>, grid_of(tasks, 8, (int64_t)sms * 64), 256, st,
+                       a);
+}
+// Two windows at once for short lists, when the tasks still fill the 40 warps of
+// each SM: a task's fixed instructions bound them.  7168 columns, us with one and
+// with two: 16384 tokens of one row each 77 and 65, of two 87 and 76, 8192 of four
+// 58 and 55; but 64 of two 2.2 and 2.7.
+template <typename T, int F>
+static cudaError_t run_gather(const GatherArgs &a, int sms, cudaStream_t st) {
+  const bool two = a.S <= 4 && a.K > 512 && a.T * ((a.K + 511) / 512) >= (int64_t)sms * 40;
+  return two ? run_gather<T, F, 2>(a, sms, st) : run_gather<T, F, 1>(a, sms, st);
+}
 template <typename T>
 static cudaError_t run_gather(const GatherArgs &a, int sms, cudaStream_t st) {
-  const int64_t blocks = grid_of(a.T * ((a.K + 511) / 512), 8, (int64_t)sms * 64);
-  return a.fmt == 0 ? launch_serial(experts_gather_kernel<T, 0>, blocks, 256, st, a)
-                    : launch_serial(experts_gather_kernel<T, 1>, blocks, 256, st, a);
+  return a.fmt == 0 ? run_gather<T, 0>(a, sms, st) : run_gather<T, 1>(a, sms, st);
 }
 
 cudaError_t launch_experts_gather(const GatherArgs &a, int source, int sms, cudaStream_t st) {
   if (a.T == 0 || a.M == 0) return cudaSuccess;
-  if (source == kGatherCodes) {  // the format of codes that are moved does not matter
-    GatherArgs b = a;
-    b.fmt = 0;
-    const int64_t blocks = grid_of(a.T * ((a.K + 511) / 512), 8, (int64_t)sms * 64);
-    return launch_serial(experts_gather_kernel<uint8_t, 0>, blocks, 256, st, b);
-  }
+  if (source == kGatherCodes)  // the format of codes that are moved does not matter
+    return run_gather<uint8_t, 0>(a, sms, st);
   return source == kGatherBf16 ? run_gather<__nv_bfloat16>(a, sms, st) : run_gather<float>(a, sms, st);
 }
 

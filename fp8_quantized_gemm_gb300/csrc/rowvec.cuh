@@ -198,17 +198,11 @@ struct Vec16 {
     r[1].max_abs(a, b);
     return Raw8<T>::merge_keys(a, b);
   }
-  // the exact quotients' codes under a scale formed from an amax that covers them
+  // the exact quotients' codes under a scale of the common range formed from an
+  // amax that covers them
   template <int F>
-  __device__ __forceinline__ uint4 codes(const ScaleDiv &d) const {
-    uint2 lo, hi;
-    if (d.fast) {
-      lo = quant8_own_scale<F>(r[0], d);
-      hi = quant8_own_scale<F>(r[1], d);
-    } else {
-      lo = quant8_ieee<F>(r[0], d);
-      hi = quant8_ieee<F>(r[1], d);
-    }
+  __device__ __forceinline__ uint4 codes_own(const ScaleDiv &d) const {
+    const uint2 lo = quant8_own_scale<F>(r[0], d), hi = quant8_own_scale<F>(r[1], d);
     return make_uint4(lo.x, lo.y, hi.x, hi.y);
   }
   // under the power of two 1 / inv

@@ -145,7 +145,10 @@ GATHER = [  # t, s, e, k, dt, sfmt, fmt, drop, pad, spare rows
     (3, 2, 4, 128, "f32", 1, 0, 0, 0, 5), (64, 8, 256, 2064, "bf16", 1, 1, 0.3, 8, 0),
     (77, 3, 5, 144, "f32", 0, 1, 0.5, 24, 40), (257, 6, 16, 1040, "bf16", 0, 0, 0.2, 0, 3),
     (9, 33, 40, 640, "bf16", 0, 0, 0.1, 0, 0), (5, 70, 70, 528, "f32", 1, 0, 0, 0, 0),
-    (1500, 8, 64, 4096, "bf16", 0, 0, 0, 0, 0), (4, 2, 2, 20480, "f32", 0, 0, 0, 0, 0)]
+    (1500, 8, 64, 4096, "bf16", 0, 0, 0, 0, 0), (4, 2, 2, 20480, "f32", 0, 0, 0, 0, 0),
+    # short lists of many tokens, of which two windows of columns go at once
+    (4100, 2, 8, 1040, "bf16", 0, 0, 0.1, 8, 3), (3100, 4, 16, 1296, "f32", 1, 1, 0.2, 0, 0),
+    (7000, 1, 8, 528, "bf16", 1, 1, 0, 0, 0)]
 
 
 @pytest.mark.parametrize("t,s,e,k,dt,sfmt,fmt,drop,pad,spare", GATHER)
@@ -198,6 +201,26 @@ def test_gather_non_finite():
         assert torch.equal(((q[at] & 0x7F) == 0x7F), nan)
         assert torch.equal(q[at][~nan], lq[~nan])
         assert torch.equal(sc[:, at].contiguous().view(torch.uint8), ls.view(torch.uint8))
+
+
+@pytest.mark.parametrize("s,dt", [(1, "bf16"), (8, "f32")])
+def test_gather_extreme_scales(s, dt):
+    """Rows from 2^-120 to 2^120 among others: the quantizer's bytes."""
+    F = lib()
+    t, k = 7000, 528
+    x = randn((t, k), torch.float32, 5)
+    x *= torch.exp2(torch.arange(t, device="cuda") % 241 - 120.0)[:, None]
+    x = x.to(DT[dt])
+    rows = torch.randperm(t * s, device="cuda").int().view(t, s)
+    for fmt in (0, 1):
+        for sfmt, st in ((0, torch.float32), (1, torch.uint8)):
+            q, sc = filled((t * s, k), torch.uint8), filled((5, t * s), st)
+            F.fp8_experts_gather(x, rows, q=q, scales=sc, fmt=fmt, sfmt=sfmt)
+            lq, ls = torch.empty((t, k), dtype=torch.uint8, device="cuda"), filled((5, t), st)
+            F.fp8_quantize_token_group(x, fmt, sfmt, lq, ls)
+            for j in range(s):
+                at = rows[:, j].long()
+                assert torch.equal(q[at], lq) and torch.equal(sc[:, at], ls)
 
 
 # ---------------------------------------------------------------- combine --
