@@ -630,15 +630,15 @@ cudaError_t launch_experts_combine(const CombineArgs &a, int x_dt, int out_dt, i
 }
 
 // ------------------------------------------------------- combine, gradient --
-// A CTA per token, each warp every nw-th W windows of it.  |w dy| of a group (16
-// lanes) peaks where |dy| does (rounding is monotone), so the group's maximum of dy
-// is taken once and lane j of the group forms the scale of the j-th row from it,
-// and the factor w / scale that takes dy to that row's codes.  The rows' dot
-// products stay in registers and are reduced together: a butterfly that halves the
-// rows a lane still holds at each of its first steps, then a sum over the warps in
-// their order.  4096 tokens of 7168 columns, eight bf16 rows each, codes and dw: 120
-// us, 95% of the copy rate.  Short lists are bound by the barrier of each token: two
-// choices 183 us where the copy rate allows 140 (fewer windows a step: 218).
+// A CTA per token, each warp every nw-th W windows of it (alone: a warp per token).
+// |w dy| of a group (16 lanes) peaks where |dy| does (rounding is monotone), so the
+// group's maximum of dy is taken once and lane j of the group forms the scale of
+// the j-th row from it, and the factor w / scale that takes dy to that row's codes.
+// The rows' dot products stay in registers and are reduced together: a butterfly
+// that halves the rows a lane still holds at each of its first steps, then a sum
+// over the warps in their order.  4096 tokens of 7168 columns, eight bf16 rows each,
+// codes and dw: 120 us, 95% of the copy rate; with one row each (16384 tokens, 133
+// us, 65%) the scales and reductions of a step serve only that row.
 template <typename DY, typename X, int F, int W>
 __global__ void __launch_bounds__(32 * ring_warps(ring_stage<X, DY, W>()), 3)
     experts_combine_grad_kernel(const CombineGradArgs a) {
@@ -648,8 +648,12 @@ __global__ void __launch_bounds__(32 * ring_warps(ring_stage<X, DY, W>()), 3)
   __shared__ float part[2][kWarps][kC];
   launch_dependents();
   grid_dependency_wait();
-  const uint32_t l = lane_id(), w = threadIdx.x >> 5, nw = blockDim.x >> 5;
-  uint8_t *ring = smem + w * (2 * kStage);
+  const uint32_t l = lane_id(), warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  const bool alone = a.alone != 0;
+  const uint32_t w = alone ? 0u : warp, nw = alone ? 1u : warps;
+  const int64_t first = alone ? (int64_t)blockIdx.x * warps + warp : blockIdx.x;
+  const int64_t step_t = alone ? (int64_t)gridDim.x * warps : gridDim.x;
+  uint8_t *ring = smem + warp * (2 * kStage);
   const uint32_t ring_at = smem_u32(ring);
   const DY *dy = static_cast<const DY *>(a.dy);
   const int32_t wins = (int32_t)((a.K + 256 * W - 1) / (256 * W)), S = (int32_t)a.S;
@@ -658,14 +662,15 @@ __global__ void __launch_bounds__(32 * ring_warps(ring_stage<X, DY, W>()), 3)
     int64_t t;
     int32_t s0, win;
     // true: another list of choices
-    __device__ __forceinline__ bool next(int32_t wins, int32_t w, int32_t nw, int32_t S) {
+    __device__ __forceinline__ bool next(int32_t wins, int32_t w, int32_t nw, int32_t S,
+                                         int64_t step_t) {
       win += nw;
       if (win < wins) return false;
       win = w;
       s0 += kC;
       if (s0 >= S) {
         s0 = 0;
-        t += gridDim.x;
+        t += step_t;
       }
       return true;
     }
@@ -697,20 +702,20 @@ __global__ void __launch_bounds__(32 * ring_warps(ring_stage<X, DY, W>()), 3)
   auto choices = [&](const Step &s, Choices<kC> &c) {
     c.load(a.rows, a.weights, s.t, s.s0, a.T, S, a.M);
   };
-  Step cur{(int64_t)blockIdx.x, 0, (int32_t)w};
+  Step cur{first, 0, (int32_t)w};
   Choices<kC> c_cur, c_next;
   choices(cur, c_cur);
   fetch(cur, c_cur, 0);
   Step nxt = cur;
   c_next = c_cur;
-  if (nxt.next(wins, (int32_t)w, (int32_t)nw, S)) choices(nxt, c_next);
+  if (nxt.next(wins, (int32_t)w, (int32_t)nw, S, step_t)) choices(nxt, c_next);
   F2 dot[kC];
   int phase = 0;
   for (int stage = 0; cur.t < a.T; stage ^= 1) {
     __syncwarp();  // the other lanes have read what this overwrites
     fetch(nxt, c_next, stage ^ 1);
     Step behind = nxt;
-    const bool fresh = behind.next(wins, (int32_t)w, (int32_t)nw, S);
+    const bool fresh = behind.next(wins, (int32_t)w, (int32_t)nw, S, step_t);
     const int32_t row_l = c_cur.row;
     const float w_l = c_cur.wt;
     const uint32_t kept = c_cur.kept();
@@ -805,14 +810,20 @@ __global__ void __launch_bounds__(32 * ring_warps(ring_stage<X, DY, W>()), 3)
       float sum = d[0];
 #pragma unroll
       for (int o = 16 / kC; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      // (a buffer is written again two barriers after it was read)
-      if (l % (32 / kC) == 0) part[phase][w][l / (32 / kC)] = sum;
-      __syncthreads();
-      if ((int)threadIdx.x < n) {
-        float all = 0.0f;
-        for (uint32_t i = 0; i < nw; ++i) all += part[phase][i][threadIdx.x];
-        // (a dropped pair's sum would be dy's infinities times zeros)
-        a.dw[cur.t * S + cur.s0 + threadIdx.x] = kept >> threadIdx.x & 1u ? all : 0.0f;
+      // (a dropped pair's sum would be dy's infinities times zeros)
+      const uint32_t j = l / (32 / kC);
+      if (alone) {
+        if (l % (32 / kC) == 0 && (int32_t)j < n)
+          a.dw[cur.t * S + cur.s0 + j] = kept >> j & 1u ? sum : 0.0f;
+      } else {
+        // (a buffer is written again two barriers after it was read)
+        if (l % (32 / kC) == 0) part[phase][w][j] = sum;
+        __syncthreads();
+        if ((int)threadIdx.x < n) {
+          float all = 0.0f;
+          for (uint32_t i = 0; i < nw; ++i) all += part[phase][i][threadIdx.x];
+          a.dw[cur.t * S + cur.s0 + threadIdx.x] = kept >> threadIdx.x & 1u ? all : 0.0f;
+        }
       }
       phase ^= 1;
     }
@@ -822,16 +833,23 @@ __global__ void __launch_bounds__(32 * ring_warps(ring_stage<X, DY, W>()), 3)
   copies_wait<0>();
 }
 
-// The fewest rounds of a token's steps, then as few warps as they need.
+// A CTA per token: the fewest rounds of its steps, then as few warps as they need.
+// Of many tokens (two and more for each resident warp) with one or two choices a
+// warp takes one alone, without the barrier.  7168 columns, us with a CTA and with a
+// warp per token: 16384 tokens of one choice 166 and 133, of two 184 and 156, 8192 of
+// two 97 and 82, 4096 of two 52 and 53; but of four 8192 in 134 and 161, and 16384 of
+// eight choices, 4096 columns, in 265 and 328.
 template <typename DY, typename X, int F>
 static cudaError_t run_combine_grad(const CombineGradArgs &a, int sms, cudaStream_t st) {
   return with_windows<X>(a.S, a.K, [&](auto windows) {
     constexpr int kW = windows.value, kStage = ring_stage<X, DY, kW>(), kMost = ring_warps(kStage);
     const int64_t steps = (a.K + 256 * kW - 1) / (256 * kW), rounds = (steps + kMost - 1) / kMost;
-    const int warps = (int)((steps + rounds - 1) / rounds);
+    CombineGradArgs b = a;
+    b.alone = rows_per_step<X, kW>() == 2 && a.T >= (int64_t)sms * 6 * kMost ? 1 : 0;
+    const int warps = b.alone ? kMost : (int)((steps + rounds - 1) / rounds);
     const int64_t most = (int64_t)sms * (3 * kMost / warps);  // resident at once
     return launch_serial_smem<experts_combine_grad_kernel<DY, X, F, kW>, kMost * 2 * kStage>(
-        a.T < most ? a.T : most, 32 * warps, warps * 2 * kStage, st, a);
+        a.T < most ? a.T : most, 32 * warps, warps * 2 * kStage, st, b);
   });
 }
 template <typename DY, typename X>

@@ -51,6 +51,7 @@ struct CombineGradArgs {
   void *dx;               // nullable [M, ld_dx]
   int64_t T, S, K, M, ld_dy, ldx, ld_dx;
   int fmt, sfmt, dx_dt;
+  int alone;              // a warp takes a token alone (set by the launcher)
 };
 cudaError_t launch_experts_combine_grad(const CombineGradArgs &a, int dy_dt, int x_dt, int sms,
                                         cudaStream_t st);

@@ -6,7 +6,9 @@ addition, each within 2^-24 of a partial sum that is at most the sum of the
 magnitudes; the result is rounded once to the output's type (half a step).
 dw: a lane adds four pairs per 256 columns and a CTA has at least four warps up
 to K = 16384 (16 windows each: 64 steps), then two halves, five shuffles and at
-most eight warps: 80 steps of 2^-24 on the sum of the magnitudes cover it.  Codes of w dy: one rounding each
+most eight warps: 80 steps of 2^-24 on the sum of the magnitudes cover it.  (One
+warp alone: four pairs of each 256 columns too, 20 steps up to K = 1040, and the
+same end.)  Codes of w dy: one rounding each
 of the product, the maximum's product, the scale, its reciprocal and the
 quotient, below 2^-21 together, and half a step of the format.  gather forms the
 exact quotient: the bytes themselves are checked.
@@ -301,7 +303,10 @@ GRAD = [  # t, s, e, k, dt, dydt, sfmt, fmt, dw, weights, drop, pad
     # short lists, of which several windows of columns go at once
     (90, 2, 8, 2064, "bf16", "bf16", 0, 0, True, True, 0.2, 8), (33, 1, 4, 1040, "bf16", "f32", 1, 1, True, False, 0, 0),
     (50, 3, 5, 1296, "bf16", "bf16", 0, 1, True, True, 0.3, 0), (700, 4, 9, 4112, "bf16", "f32", 0, 0, True, True, 0.1, 16),
-    (300, 1, 8, 7168, "f32", "bf16", 0, 0, True, True, 0, 8), (64, 2, 8, 16384, "bf16", "bf16", 0, 0, True, True, 0, 0)]
+    (300, 1, 8, 7168, "f32", "bf16", 0, 0, True, True, 0, 8), (64, 2, 8, 16384, "bf16", "bf16", 0, 0, True, True, 0, 0),
+    # many tokens, of which a warp takes one alone
+    (16000, 2, 8, 528, "bf16", "bf16", 0, 0, True, True, 0.1, 0), (15001, 9, 16, 144, "bf16", "f32", 1, 0, True, True, 0.2, 0),
+    (12000, 1, 8, 1040, "f32", "f32", 0, 1, True, False, 0, 8)]
 
 
 @pytest.mark.parametrize("t,s,e,k,dt,dydt,sfmt,fmt,dw,weights,drop,pad", GRAD)
