@@ -58,6 +58,10 @@ int check_tokens(int64_t T, int64_t S, int64_t K, int64_t M, const int32_t *rows
   return FP8_OK;
 }
 
+// combine and its gradient step through a token's choices in 32 signed bits, up to
+// eight behind the last one.
+int check_choices(int64_t S) { return S > kMaxDim / 2 ? FP8_ERR_UNSUPPORTED : FP8_OK; }
+
 }  // namespace
 
 extern "C" {
@@ -121,6 +125,7 @@ int fp8_experts_combine(const fp8_experts_combine_t *combine, fp8_stream_t strea
   if (combine == nullptr) return FP8_ERR_INVALID_ARG;
   const fp8_experts_combine_t &n = *combine;
   int rc = check_tokens(n.T, n.S, n.K, n.M, n.rows);
+  if (rc == FP8_OK) rc = check_choices(n.S);
   if (rc != FP8_OK) return rc;
   if (!valid_in(n.x_dt) || !valid_in(n.out_dt)) return FP8_ERR_INVALID_ARG;
   if (n.T > 0 && (n.out == nullptr || (n.M > 0 && n.x == nullptr))) return FP8_ERR_INVALID_ARG;
@@ -145,6 +150,7 @@ int fp8_experts_combine_backward(const fp8_experts_combine_grad_t *grad, fp8_str
   if (grad == nullptr) return FP8_ERR_INVALID_ARG;
   const fp8_experts_combine_grad_t &n = *grad;
   int rc = check_tokens(n.T, n.S, n.K, n.M, n.rows);
+  if (rc == FP8_OK) rc = check_choices(n.S);
   if (rc != FP8_OK) return rc;
   if (!valid_in(n.dy_dt) || !valid_in(n.x_dt) || !valid_in(n.dx_dt) || !valid_fmt(n.fmt) ||
       !valid_sfmt(n.sfmt))

@@ -722,7 +722,8 @@ FP8_API int fp8_rmsnorm_backward(const fp8_rmsnorm_grad_t *grad, fp8_stream_t st
  * rows; pitches in elements, >= K, multiples of 8 and below 2^30
  * (FP8_ERR_UNSUPPORTED from there on); K % 16 == 0.  Codes are [M, K]
  * contiguous, 16-byte aligned; group scales [ceil(K/128), M] of sfmt.
- * T == 0 or M == 0 is allowed; T * S < 2^31.  No output may overlap an input or
+ * T == 0 or M == 0 is allowed; T * S < 2^31, and S <= 2^30 in combine and its
+ * gradient (FP8_ERR_UNSUPPORTED beyond).  No output may overlap an input or
  * another output but where it says so.  No call allocates or keeps scratch; all
  * are launched with programmatic stream serialization, as the
  * per-group calls, and give the same bits on every run.
