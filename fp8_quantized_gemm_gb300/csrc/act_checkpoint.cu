@@ -13,9 +13,9 @@
 // 2 + 2.06 in, 2 out.  A CTA takes tiles of 32 rows by 128 columns, a row's
 // group on eight lanes of 16 elements each (32-byte accesses, and the scales of
 // a tile are 32 neighbours of the group-major layout); tiles go by column first.
-// 16384 x 14336 gated: forward 260 us (94% of the copy rate), backward 231 (92%).
-// Gelu is bound by its instructions (without a gate 203 us both ways, where silu
-// takes 155 and 149).
+// 16384 x 14336 gated: forward 260 us (94% of the copy rate), backward 235 (91%).
+// Gelu is bound by its instructions (without a gate 207 and 210 us, where silu
+// takes 157 and 150).
 #include "act_checkpoint.h"
 #include "activation.cuh"
 #include "common.cuh"
@@ -137,6 +137,10 @@ struct TileWalk {
       row += 32;
     }
   }
+  // how many tiles of the walk are ahead of this one (few enough for 32 bits)
+  __device__ __forceinline__ uint32_t step(uint32_t rows) const {
+    return (uint32_t)((int64_t)((rows + 31) / 32) * groups - blockIdx.x - left) / gridDim.x;
+  }
   __device__ __forceinline__ uint32_t col() const { return g * 128 + (threadIdx.x & 7u) * 16; }
   __device__ __forceinline__ int64_t at(int64_t pitch) const {
     return (int64_t)((uint64_t)row * (uint32_t)pitch + col());
@@ -148,8 +152,8 @@ struct TileWalk {
 
 // Threads of a CTA, and CTAs that share an SM.  With a gate three (85 registers a
 // thread: the next tile's operands wait in registers; 16384 x 14336 in 260 us
-// forward and 231 backward, 287 and 281 on four, which spill); without one four
-// (silu 155 us forward and 149 backward, 181 and 160 on three).
+// forward and 235 backward, 287 and 281 on four, which spill); without one four
+// (silu 157 us forward and 150 backward, 181 and 160 on three).
 constexpr int kTileThreads = 256;
 constexpr int ctas_per_sm(bool gate) { return gate ? 3 : 4; }
 
@@ -178,23 +182,35 @@ __device__ __forceinline__ void put16(uint8_t *q, const uint4 &c, bool in) {
 }
 
 // The kernels' loops hold the common case: scales far from the ends of fp32
-// (GroupScale::fast) and, backward, checkpoints of values below 2^49.  A warp whose
-// four rows of a tile are another case leaves them, and goes over its tiles again
-// behind its loop, out of line, with IEEE quotients and bounded
-// activations.  (The same code inside the loop cost the backward pass 30 us of 262:
-// registers kept across its calls.)
+// (GroupScale::fast) and, backward, checkpoints of values below 2^49.  A row's group
+// of another case is done again behind the loop, out of line, with IEEE quotients
+// and bounded activations, by the threads that have stored it before: what a row's
+// bytes are depends on the row alone.  (The same code inside the loop cost the backward
+// pass 30 us of 262: registers kept across its calls.  16384 x 14336, gated silu, forward
+// and backward: no such group 264 and 235 us, one 276 and 245, one in a hundred rows 414
+// and 370, all 1860 and 2110.)
+//
+// Which tiles of its walk those are is kept per row: a bit per tile, 32 on each of
+// the row's eight lanes; no CTA walks over more than kMostTiles.
+constexpr uint32_t kMostTiles = 256;
+__device__ __forceinline__ void note_tile(uint32_t &noted, uint32_t step) {
+  if ((threadIdx.x & 7u) == step >> 5) noted |= 1u << (step & 31u);
+}
+__device__ __forceinline__ bool tile_noted(uint32_t noted, uint32_t step) {
+  return __shfl_sync(0xffffffffu, noted, (threadIdx.x & 24u) | step >> 5) >> (step & 31u) & 1u;
+}
 
 // Codes of 16 results under the scale of their group (group: 8 lanes), stored
-// with it; false where the scale is not of the common case.
+// with it; false where the scale is not of the common case (nothing of what is
+// stored holds then).
 template <int F>
 __device__ __forceinline__ bool put_group(const F2 (&y)[8], float amax, int sfmt, uint8_t *q,
                                           void *scales, int64_t at, bool in, bool owner) {
   const float top = __uint_as_float(group8_max(__float_as_uint(amax)));
   const GroupScale g = group_scale<F>(top, sfmt);
-  if (!__all_sync(0xffffffffu, g.fast)) return false;
   if (owner) store_scale(scales, at, g.stored, sfmt);
   put16(q, codes16_times<F>(y, g.inv), in);
-  return true;
+  return g.fast;
 }
 template <int F>
 __device__ __forceinline__ void put_group_any(const F2 (&y)[8], float amax, int sfmt, uint8_t *q,
@@ -206,7 +222,7 @@ __device__ __forceinline__ void put_group_any(const F2 (&y)[8], float amax, int 
 }
 // Two results of the same group at once: the first step of the reduction leaves
 // the maximum of y to even lanes and that of z to odd ones, so that each lane
-// forms one scale instead of two.
+// forms one scale instead of two (a reciprocal of 0: not of the common case).
 template <int F>
 __device__ __forceinline__ bool put_groups(const F2 (&y)[8], const F2 (&z)[8], int sfmt,
                                            uint8_t *qy, uint8_t *qz, void *sy, void *sz, int64_t at,
@@ -218,12 +234,11 @@ __device__ __forceinline__ bool put_groups(const F2 (&y)[8], const F2 (&z)[8], i
   key = max(key, __shfl_xor_sync(0xffffffffu, key, 2));
   key = max(key, __shfl_xor_sync(0xffffffffu, key, 4));
   const GroupScale g = group_scale<F>(__uint_as_float(key), sfmt);
-  if (!__all_sync(0xffffffffu, g.fast)) return false;
-  const float other = __shfl_xor_sync(0xffffffffu, g.inv, 1);
+  const float inv = g.fast ? g.inv : 0.0f, other = __shfl_xor_sync(0xffffffffu, inv, 1);
   if (live && (threadIdx.x & 7u) < 2u) store_scale(odd ? sz : sy, at, g.stored, sfmt);
-  put16(qy, codes16_times<F>(y, odd ? other : g.inv), in);
-  put16(qz, codes16_times<F>(z, odd ? g.inv : other), in);
-  return true;
+  put16(qy, codes16_times<F>(y, odd ? other : inv), in);
+  put16(qz, codes16_times<F>(z, odd ? inv : other), in);
+  return inv != 0.0f && other != 0.0f;
 }
 // Under the tensor's scale d, the maximum into `top`.
 template <int F>
@@ -236,8 +251,10 @@ __device__ __forceinline__ void put_tensor(const F2 (&y)[8], const CodeScale &d,
 template <int F>
 __device__ __forceinline__ void put_tensor_any(const F2 (&y)[8], const CodeScale &d, float &top,
                                                uint8_t *q, bool in) {
+  if (in) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) top = max_abs2(top, y[i]);
+    for (int i = 0; i < 8; ++i) top = max_abs2(top, y[i]);
+  }
   put16(q, codes16_any<F>(y, d.s), in);
 }
 
@@ -253,20 +270,21 @@ __device__ __noinline__ uint64_t act_slope_any(uint64_t z, int act) {
   return r.v;
 }
 
-// This warp's tiles that its loop left, found by the bit TileWalk::left % 32 (tiles
-// that share it are done again, to the same values within a rounding).
+// The groups that the loop has noted, again.
 template <int F>
 __device__ __noinline__ float act_slow_walk(const ActArgs &a, uint32_t rows, float top,
-                                             uint32_t slow) {
+                                             uint32_t noted) {
   const __nv_bfloat16 *h = static_cast<const __nv_bfloat16 *>(a.h);
   const __nv_bfloat16 *u = static_cast<const __nv_bfloat16 *>(a.u);
   const uint32_t N = (uint32_t)a.N;
   const CodeScale d(a.scale != nullptr ? *a.scale : 1.0f);
+  uint32_t step = 0;
 #pragma unroll 1
-  for (TileWalk t(rows, N); t.left > 0; t.next()) {
-    if (((slow >> (t.left & 31)) & 1u) == 0u) continue;
+  for (TileWalk t(rows, N); t.left > 0; t.next(), ++step) {
+    const bool live = tile_noted(noted, step) && t.row < rows;
+    if (!__any_sync(0xffffffffu, live)) continue;
     const int64_t at = t.scale_at(a.M), flat = t.at(a.N);
-    const bool in = t.row < rows && t.col() < N, owner = t.row < rows && (threadIdx.x & 7u) == 0u;
+    const bool in = live && t.col() < N, owner = live && (threadIdx.x & 7u) == 0u;
     const Words16 hv = load16(h + t.at(a.ldh), in);
     Words16 uv = hv;
     if (u != nullptr) uv = load16(u + t.at(a.ldu), in);
@@ -304,10 +322,10 @@ __global__ void __launch_bounds__(kTileThreads, ctas_per_sm(GATE))
   const uint32_t rows = live_rows(a.valid, a.M), N = (uint32_t)a.N;
   const CodeScale d(a.scale != nullptr ? *a.scale : 1.0f);
   float top = 0.0f;
-  uint32_t slow = 0u;
+  uint32_t noted = 0u;
   TileWalk w(rows, N);
   if (!d.fast) {
-    slow = ~0u;
+    noted = ~0u;
     w.left = 0;
   }
   Words16 hn, un;  // the next tile's
@@ -350,30 +368,32 @@ __global__ void __launch_bounds__(kTileThreads, ctas_per_sm(GATE))
       put_tensor<F>(y, d, top, a.q + flat, in);
     else
       fast &= put_group<F>(y, max_abs16(y), a.sfmt, a.q + flat, a.scales, at, in, owner);
-    if (!fast) slow |= 1u << (t.left & 31);
+    if (!fast) note_tile(noted, t.step(rows));
   }
-  if (slow != 0u) top = act_slow_walk<F>(a, rows, top, slow);
+  if (__any_sync(0xffffffffu, noted != 0u)) top = act_slow_walk<F>(a, rows, top, noted);
   if (a.amax != nullptr) block_max_to(__float_as_uint(top), a.amax);
 }
 
 // The loop's forms hold for checkpoints of values up to this.
 constexpr float kKeptScaleMax = 0x1p40f;
 
-// This warp's tiles that its loop left, found by the bit TileWalk::left % 32 (tiles
-// that share it are done again, to the same values within a rounding).
+// The groups that the loop has noted, again.
 template <int F>
-__device__ __noinline__ void act_grad_slow_walk(const ActGradArgs &a, uint32_t rows, uint32_t slow,
+__device__ __noinline__ void act_grad_slow_walk(const ActGradArgs &a, uint32_t rows, uint32_t noted,
                                                 float &top_h, float &top_u) {
   const __nv_bfloat16 *da = static_cast<const __nv_bfloat16 *>(a.da);
   const uint32_t N = (uint32_t)a.N;
   const bool gate = a.uq != nullptr;
   const CodeScale dh(a.scale_h != nullptr ? *a.scale_h : 1.0f);
   const CodeScale du(a.scale_u != nullptr ? *a.scale_u : 1.0f);
+  uint32_t step = 0;
 #pragma unroll 1
-  for (TileWalk t(rows, N); t.left > 0; t.next()) {
-    if (((slow >> (t.left & 31)) & 1u) == 0u) continue;
+  for (TileWalk t(rows, N); t.left > 0; t.next(), ++step) {
+    const bool live = tile_noted(noted, step) && t.row < rows;
+    if (!__any_sync(0xffffffffu, live)) continue;
     const int64_t at = t.scale_at(a.M), flat = t.at(a.N);
-    const bool in = t.row < rows && t.col() < N, owner = t.row < rows && (threadIdx.x & 7u) == 0u;
+    const bool in = live && t.col() < N;
+    const bool owner_h = live && (threadIdx.x & 7u) == 0u, owner_u = live && (threadIdx.x & 7u) == 1u;
     const Words16 v = load16(da + t.at(a.ld_da), in);
     Vec16<uint8_t> hc, uc;
     hc.zero();
@@ -404,9 +424,9 @@ __device__ __noinline__ void act_grad_slow_walk(const ActGradArgs &a, uint32_t r
       if (a.qu != nullptr) put_tensor_any<F>(yu, du, top_u, a.qu + qat, in);
     } else {
       if (a.qh != nullptr)
-        put_group_any<F>(yh, max_abs16(yh), a.sfmt, a.qh + qat, a.sh, at, in, owner);
+        put_group_any<F>(yh, max_abs16(yh), a.sfmt, a.qh + qat, a.sh, at, in, owner_h);
       if (a.qu != nullptr)
-        put_group_any<F>(yu, max_abs16(yu), a.sfmt, a.qu + qat, a.su, at, in, owner);
+        put_group_any<F>(yu, max_abs16(yu), a.sfmt, a.qu + qat, a.su, at, in, owner_u);
     }
   }
 }
@@ -422,10 +442,10 @@ __global__ void __launch_bounds__(kTileThreads, ctas_per_sm(GATE))
   const CodeScale dh(a.scale_h != nullptr ? *a.scale_h : 1.0f);
   const CodeScale du(a.scale_u != nullptr ? *a.scale_u : 1.0f);
   float top_h = 0.0f, top_u = 0.0f;
-  uint32_t slow = 0u;
+  uint32_t noted = 0u;
   TileWalk w(rows, N);
   if (!(dh.fast && du.fast)) {
-    slow = ~0u;
+    noted = ~0u;
     w.left = 0;
   }
   Words16 vn;  // the next tile's operands
@@ -452,14 +472,21 @@ __global__ void __launch_bounds__(kTileThreads, ctas_per_sm(GATE))
     const TileWalk t = w;
     const int64_t at = t.scale_at(a.M);
     const bool in = t.row < rows && t.col() < N;
-    const Words16 v = vn;
-    const Vec16<uint8_t> hc = hn, uc = un;
-    const float hs = kept_scale<KEPT>(hsn), us = kept_scale<KEPT>(usn);
+    Words16 v = vn;
+    Vec16<uint8_t> hc = hn, uc = un;
+    float hs = kept_scale<KEPT>(hsn), us = kept_scale<KEPT>(usn);
     w.next();
     fetch();
-    if (!__all_sync(0xffffffffu, hs <= kKeptScaleMax)) {
-      slow |= 1u << (t.left & 31);
-      continue;
+    bool fast = true;
+    const uint32_t common = __ballot_sync(0xffffffffu, hs <= kKeptScaleMax);
+    if (common != 0xffffffffu) {  // zeros in the place of such a row (in no maximum)
+      fast = (common >> (threadIdx.x & 24u) & 0xFFu) == 0xFFu;
+      if (!fast) {
+        v.a = v.b = make_uint4(0u, 0u, 0u, 0u);
+        hc.zero();
+        uc.zero();
+        hs = us = 0.0f;
+      }
     }
     F2 yh[8], yu[8];
 #pragma unroll
@@ -478,24 +505,24 @@ __global__ void __launch_bounds__(kTileThreads, ctas_per_sm(GATE))
       store16(static_cast<__nv_bfloat16 *>(a.du) + t.at(a.ld_d), yu);
     const int64_t qat = t.at(a.ld_q);
     const bool live = t.row < rows;
-    bool fast = true;
     if (tensor) {
       if (a.qh != nullptr) put_tensor<F>(yh, dh, top_h, a.qh + qat, in);
       if (GATE && a.qu != nullptr) put_tensor<F>(yu, du, top_u, a.qu + qat, in);
     } else if (GATE && a.qh != nullptr && a.qu != nullptr) {
-      fast = put_groups<F>(yh, yu, a.sfmt, a.qh + qat, a.qu + qat, a.sh, a.su, at, in, live);
+      fast &= put_groups<F>(yh, yu, a.sfmt, a.qh + qat, a.qu + qat, a.sh, a.su, at, in, live);
     } else {
-      const bool owner = live && (threadIdx.x & 7u) == 0u;
+      // (the lanes that put_groups takes: whoever stores a scale stores it again)
+      const uint32_t lane = threadIdx.x & 7u;
       if (a.qh != nullptr)
-        fast = put_group<F>(yh, max_abs16(yh), a.sfmt, a.qh + qat, a.sh, at, in, owner);
+        fast &= put_group<F>(yh, max_abs16(yh), a.sfmt, a.qh + qat, a.sh, at, in, live && lane == 0u);
       if (GATE && a.qu != nullptr)
-        fast &= put_group<F>(yu, max_abs16(yu), a.sfmt, a.qu + qat, a.su, at, in, owner);
+        fast &= put_group<F>(yu, max_abs16(yu), a.sfmt, a.qu + qat, a.su, at, in, live && lane == 1u);
     }
-    if (!fast) slow |= 1u << (t.left & 31);
+    if (!fast) note_tile(noted, t.step(rows));
   }
-  if (slow != 0u) {
+  if (__any_sync(0xffffffffu, noted != 0u)) {
     float th = top_h, tu = top_u;
-    act_grad_slow_walk<F>(a, rows, slow, th, tu);
+    act_grad_slow_walk<F>(a, rows, noted, th, tu);
     top_h = th;
     top_u = tu;
   }
@@ -519,9 +546,10 @@ static cudaError_t clear_maxima(uint32_t *p, uint32_t *q, cudaStream_t st) {
   return launch_serial(clear_maxima_kernel, 1, 32, st, p, q);
 }
 
+// Resident CTAs, times as many as keep each walk within kMostTiles.
 static int64_t tile_blocks(int64_t M, int64_t N, int64_t most) {
-  const int64_t tiles = (M + 31) / 32 * ((N + 127) / 128);
-  return tiles < most ? tiles : most;
+  const int64_t tiles = (M + 31) / 32 * ((N + 127) / 128), full = most * kMostTiles;
+  return tiles < most ? tiles : most * ((tiles + full - 1) / full);
 }
 
 // Calls f with gate and format as compile-time constants.

@@ -838,7 +838,9 @@ FP8_API int fp8_experts_combine_backward(const fp8_experts_combine_grad_t *grad,
  *          itself) taken of the fp32 results; FP8_NORM_GROUP: 1x128 groups of
  *          sfmt with scales [ceil(N/128), M].  Here and in the checkpoints
  *          values times the reciprocal of a scale (within an ulp) stand in the
- *          place of the exact quotient.
+ *          place of the exact quotient, but for groups whose scale lies near the
+ *          ends of fp32.  The bytes of a row's group depend on that group alone,
+ *          not on what else the call holds.
  *   valid_rows  nullable DEVICE int32: rows at and behind valid_rows[0] are
  *          neither read nor written and are in no maximum (offsets + experts of
  *          fp8_experts_sort: the rows that hold no token).
