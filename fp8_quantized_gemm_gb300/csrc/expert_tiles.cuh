@@ -21,7 +21,7 @@ struct ExpertTiles {
 
 // Called by one whole warp (lane = lane_id()).  Row starts are clamped to
 // [0, M], so no tile reaches past the last token even if the offsets break
-// their contract (0 = offsets[0] <= ... <= offsets[E] = M).
+// their contract (0 = offsets[0] <= ... <= offsets[E] <= M).
 __device__ __forceinline__ void build_expert_tiles(const int32_t *offsets, int E, int64_t M,
                                                    int64_t tiles_n, int tile_rows, uint32_t lane,
                                                    ExpertTiles<true> &x) {
