@@ -848,8 +848,9 @@ FP8_API int fp8_experts_combine_backward(const fp8_experts_combine_grad_t *grad,
  * >= N and multiples of 8 (h and u may be halves of one [M, 2N] product); codes
  * and checkpoints 16-byte aligned; N % 16 == 0.  M == 0 writes only the maxima
  * (0).  A NaN argument is kept as one, and the rest of its group under a scale
- * of 1; a group that holds an infinity is kept as NaN (UE8M0 scales: the
- * infinity is kept, the rest of its group as zeros).  No output may overlap an
+ * of 1; a group that holds an infinity is kept as NaN (UE8M0 scales: under the
+ * largest scale, 2^127, where the infinity is the largest code, which stands for
+ * one again, and values below 2^117 are zeros).  No output may overlap an
  * input or another output.
  * Launched with programmatic stream serialization, as the per-group calls.
  *
