@@ -375,14 +375,26 @@ static cudaError_t run_gather(const GatherArgs &a, int sms, cudaStream_t st) {
   return launch_serial(experts_gather_kernel<T, F, W>, grid_of(tasks, 8, (int64_t)sms * 64), 256, st,
                        a);
 }
-// Two windows at once for short lists, when the tasks still fill the 40 warps of
-// each SM: a task's fixed instructions bound them.  7168 columns, us with one and
-// with two: 16384 tokens of one row each 77 and 65, of two 87 and 76, 8192 of four
-// 58 and 55; but 64 of two 2.2 and 2.7.
+// Two windows at once for short lists of many tasks, whose fixed instructions bound
+// them: from 100 tasks of one window an SM on (codes that are moved: 60), where codes
+// are formed only if few windows are idle behind an odd last one.  us with one and
+// with two, bf16: 7168 columns, 16384 tokens of one row 77 and 65, of two 87 and 77,
+// of four 112 and 107, 2000 of four 14.1 and 13.7, but 500 of them 5.4 and 6.3; 2048
+// columns, 4096 of one 7.0 and 6.7, but 2000 of four 5.6 and 6.7; 3584 columns, 8192
+// of two 24.3 and 22.6; but 1040 columns (three windows) 16384 of one 17.2 and 18.6.
+// fp32 gains less: 7168 columns, 8192 of two 56 and 55, 2000 of four 18.6 and 19.1.
+// Moved, 2048 columns: 3000 of one row 3.8 and 3.0, of two 4.2 and 3.8; 2000 of four
+// 4.6 and 5.4.
+template <typename T>
+static bool two_windows(const GatherArgs &a, int sms) {
+  const int64_t wins = (a.K + 511) / 512, tasks = a.T * wins;
+  if (a.S > 4 || wins < 2) return false;
+  if (sizeof(T) == 1) return tasks >= (int64_t)sms * 60;
+  return tasks >= (int64_t)sms * 100 && (wins % 2 == 0 || wins > 6);
+}
 template <typename T, int F>
 static cudaError_t run_gather(const GatherArgs &a, int sms, cudaStream_t st) {
-  const bool two = a.S <= 4 && a.K > 512 && a.T * ((a.K + 511) / 512) >= (int64_t)sms * 40;
-  return two ? run_gather<T, F, 2>(a, sms, st) : run_gather<T, F, 1>(a, sms, st);
+  return two_windows<T>(a, sms) ? run_gather<T, F, 2>(a, sms, st) : run_gather<T, F, 1>(a, sms, st);
 }
 template <typename T>
 static cudaError_t run_gather(const GatherArgs &a, int sms, cudaStream_t st) {
@@ -422,7 +434,12 @@ constexpr int ring_warps(int stage) {
   return n < 8 ? n : 8;
 }
 // The most windows a step (1, 2 or 4; fp32 rows 1 or 2) that still hold the whole
-// list, and of which more than half exist.
+// list, and of which more than half exist.  us with one, two and four, 7168 columns,
+// bf16: combine 16384 tokens of one row 179, 116, 114, of two 187, 139, 142, 1000 of
+// one 13.2, 8.3, 6.3; gradient 16384 of one 370, 213, 134, of two 380, 226, 153, 4096
+// of two 97, 60, 52; 1040 columns, 4096 of two 21, 15.2, 13.1.  What it costs: the
+// gradient of 64 decoded tokens (narrow ones 3.4, 3.8, 4.1; 7168 columns 8.2, 5.8, 6.6)
+// and fp32 sums of full size (16384 tokens of one row 219 and 232, two rows 277 and 280).
 template <typename T, typename Fn>
 static cudaError_t with_windows(int64_t S, int64_t K, Fn &&f) {
   const int64_t all = rows_per_step<T, 1>();
@@ -836,9 +853,14 @@ __global__ void __launch_bounds__(32 * ring_warps(ring_stage<X, DY, W>()), 3)
 // A CTA per token: the fewest rounds of its steps, then as few warps as they need.
 // Of many tokens (two and more for each resident warp) with one or two choices a
 // warp takes one alone, without the barrier.  7168 columns, us with a CTA and with a
-// warp per token: 16384 tokens of one choice 166 and 133, of two 184 and 156, 8192 of
-// two 97 and 82, 4096 of two 52 and 53; but of four 8192 in 134 and 161, and 16384 of
-// eight choices, 4096 columns, in 265 and 328.
+// warp per token: 16384 tokens of one choice 167 and 133, of two 184 and 152, 8192 of
+// two 98 and 79, 4096 of two 52 and 53; but of four 8192 in 134 and 161, and 16384 of
+// eight choices, 4096 columns, in 265 and 328.  Between full rounds of 2736 tokens the
+// last one is idle in part: 5472 of two choices 66 and 55, 6000 72 and 70, 8500 98 and
+// 91, 12000 138 and 120; 2048 columns 18.4 and 17.2, 22.2 and 22.9, 32.8 and 32.4, 43
+// and 42; 14336 columns 118 and 109, 131 and 133, 181 and 173, 251 and 236.  fp32, two
+// choices: 2048 columns 81 and 79, 7168 columns 257 and 266 (16384 tokens; one choice
+// 69 and 50, 185 and 171).
 template <typename DY, typename X, int F>
 static cudaError_t run_combine_grad(const CombineGradArgs &a, int sms, cudaStream_t st) {
   return with_windows<X>(a.S, a.K, [&](auto windows) {
