@@ -23,6 +23,10 @@ weights stay as they are; their transposed codes are made once, backward=True):
   fp8_gemm_group_experts       dx rows = dh | du times W13
   fp8_experts_combine          dx, each token's rows added
 
+The experts' weights get no gradient.  A call with keep=True holds h and u in 8 bits
+and y, which dw reads, in bf16: ffn 2048 and d 7168 are 4.2 KB of checkpoints and
+14.3 KB of y a row.
+
 Ids outside [0, experts) drop their choice (experts of another device, a full
 expert): it adds nothing and its gradients are zero.
 """

@@ -59,7 +59,10 @@ with a scale per 1x128 group, 2.06 bytes an element for two bf16's 4): h and u
 are two plain products into buffers that live for the forward pass only, one
 call writes the codes of a and both checkpoints, and the SwiGLU backward reads
 the checkpoints.  The gradients are those at the values the checkpoints stand
-for.
+for.  It is for steps that hold several such layers between their passes: this
+one layer alone gives up the gated epilogue (6.5 ms a step of 16384 tokens, d 4096,
+ffn 14336, instead of 6.35) and, while the bf16 h and u live, takes more memory
+(6482 MB at its peak instead of 5998; 5543 held between the passes).
 
 Buffers are allocated once (device memory through torch); `step` issues the
 calls on the current stream.

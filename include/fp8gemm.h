@@ -793,7 +793,8 @@ FP8_API int fp8_experts_combine(const fp8_experts_combine_t *combine, fp8_stream
  *   q, scales   nullable together: codes of v (fmt; E4M3 is what
  *               fp8_gemm_group_experts reads) in 1x128 groups, with dy times
  *               w times the reciprocal of a scale (within an ulp) in the place
- *               of the exact quotient
+ *               of the exact quotient (which stands where a scale of the token's
+ *               pairs nearby lies near the ends of fp32)
  *   dx          nullable [M, ld_dx] of dx_dt: v, rounded once
  *   d_weights   nullable fp32 [T, S] (x given): sum_k dy[t,k] x[r,k], in a
  *               fixed order
@@ -832,7 +833,11 @@ FP8_API int fp8_experts_combine_backward(const fp8_experts_combine_grad_t *grad,
  *                                 h and u that the checkpoints stand for
  *
  * act: fp8_act_t with its limits at infinite arguments (NONE: act(h) = h).
- * Results are formed in fp32 and rounded once per stored copy.
+ * Results are formed in fp32 and rounded once per stored copy.  (For a gated silu
+ * under a per-tensor scale with nothing kept there is fp8_swiglu_forward_quantize
+ * too: the codes of the bf16 a, by exact quotients, as the gated GEMM epilogue writes
+ * them; take that one beside the epilogue, this one with the checkpoints, group
+ * scales or another activation.)
  *   mode   FP8_NORM_TENSOR: codes under scales fixed before the call (delayed
  *          scaling), the maxima (nullable, cleared by the call, not a scale
  *          itself) taken of the fp32 results; FP8_NORM_GROUP: 1x128 groups of
