@@ -13,9 +13,9 @@
 // 2 + 2.06 in, 2 out.  A CTA takes tiles of 32 rows by 128 columns, a row's
 // group on eight lanes of 16 elements each (32-byte accesses, and the scales of
 // a tile are 32 neighbours of the group-major layout); tiles go by column first.
-// 16384 x 14336 gated: forward 260 us (94% of the copy rate), backward 235 (91%).
-// Gelu is bound by its instructions (without a gate 207 and 210 us, where silu
-// takes 157 and 150).
+// 16384 x 14336 gated: forward 260 us (94% of the copy rate), backward 231 (92%).
+// Gelu is bound by its instructions (without a gate 207 and 208 us, where silu
+// takes 158 and 149).
 #include "act_checkpoint.h"
 #include "activation.cuh"
 #include "common.cuh"
@@ -152,8 +152,8 @@ struct TileWalk {
 
 // Threads of a CTA, and CTAs that share an SM.  With a gate three (85 registers a
 // thread: the next tile's operands wait in registers; 16384 x 14336 in 260 us
-// forward and 235 backward, 287 and 281 on four, which spill); without one four
-// (silu 157 us forward and 150 backward, 181 and 160 on three).
+// forward and 231 backward, 287 and 281 on four, which spill); without one four
+// (silu 158 us forward and 149 backward, 181 and 160 on three).
 constexpr int kTileThreads = 256;
 constexpr int ctas_per_sm(bool gate) { return gate ? 3 : 4; }
 
@@ -182,27 +182,27 @@ __device__ __forceinline__ void put16(uint8_t *q, const uint4 &c, bool in) {
 }
 
 // The kernels' loops hold the common case: scales far from the ends of fp32
-// (GroupScale::fast) and, backward, checkpoints of values below 2^49.  A row's group
-// of another case is done again behind the loop, out of line, with IEEE quotients
-// and bounded activations, by the threads that have stored it before: what a row's
-// bytes are depends on the row alone.  (The same code inside the loop cost the backward
-// pass 30 us of 262: registers kept across its calls.  16384 x 14336, gated silu, forward
-// and backward: no such group 264 and 235 us, one 276 and 245, one in a hundred rows 414
-// and 370, all 1860 and 2110.)
+// (GroupScale::fast) and, backward, checkpoints of values below 2^49.  A warp with
+// another case in its four rows of a tile notes the tile and does the four again behind
+// its loop, out of line: the groups that need them with IEEE quotients and bounded
+// activations, the others as in the loop, so that what a group's bytes are depends on
+// that group alone.  (The same code inside the loop cost the backward pass 30 us of 262:
+// registers kept across its calls.  16384 x 14336, gated silu, forward and backward: no
+// such group 264 and 231 us, one 273 and 240, one in a hundred rows 371 and 341, all 1740
+// and 1940.)
 //
-// Which tiles of its walk those are is kept per row: a bit per tile, 32 on each of
-// the row's eight lanes; no CTA walks over more than kMostTiles.
-constexpr uint32_t kMostTiles = 256;
+// A bit per tile of the walk, 32 on each lane; no CTA walks over more than kMostTiles.
+constexpr uint32_t kMostTiles = 1024;
 __device__ __forceinline__ void note_tile(uint32_t &noted, uint32_t step) {
-  if ((threadIdx.x & 7u) == step >> 5) noted |= 1u << (step & 31u);
+  if ((threadIdx.x & 31u) == step >> 5) noted |= 1u << (step & 31u);
 }
 __device__ __forceinline__ bool tile_noted(uint32_t noted, uint32_t step) {
-  return __shfl_sync(0xffffffffu, noted, (threadIdx.x & 24u) | step >> 5) >> (step & 31u) & 1u;
+  return __shfl_sync(0xffffffffu, noted, step >> 5) >> (step & 31u) & 1u;
 }
 
 // Codes of 16 results under the scale of their group (group: 8 lanes), stored
-// with it; false where the scale is not of the common case (nothing of what is
-// stored holds then).
+// with it; false where the scale is not of the common case (what is stored does
+// not hold then).
 template <int F>
 __device__ __forceinline__ bool put_group(const F2 (&y)[8], float amax, int sfmt, uint8_t *q,
                                           void *scales, int64_t at, bool in, bool owner) {
@@ -212,17 +212,23 @@ __device__ __forceinline__ bool put_group(const F2 (&y)[8], float amax, int sfmt
   put16(q, codes16_times<F>(y, g.inv), in);
   return g.fast;
 }
+// The same for a group of any scale.
 template <int F>
 __device__ __forceinline__ void put_group_any(const F2 (&y)[8], float amax, int sfmt, uint8_t *q,
                                               void *scales, int64_t at, bool in, bool owner) {
-  const GroupScale g =
-      group_scale_any<F>(__uint_as_float(group8_max(__float_as_uint(amax))), sfmt);
+  const float top = __uint_as_float(group8_max(__float_as_uint(amax)));
+  GroupScale g = group_scale<F>(top, sfmt);
+  if (g.fast) {
+    put16(q, codes16_times<F>(y, g.inv), in);
+  } else {
+    g = group_scale_any<F>(top, sfmt);
+    put16(q, codes16_any<F>(y, g.s), in);
+  }
   if (owner) store_scale(scales, at, g.stored, sfmt);
-  put16(q, codes16_any<F>(y, g.s), in);
 }
 // Two results of the same group at once: the first step of the reduction leaves
 // the maximum of y to even lanes and that of z to odd ones, so that each lane
-// forms one scale instead of two (a reciprocal of 0: not of the common case).
+// forms one scale instead of two.
 template <int F>
 __device__ __forceinline__ bool put_groups(const F2 (&y)[8], const F2 (&z)[8], int sfmt,
                                            uint8_t *qy, uint8_t *qz, void *sy, void *sz, int64_t at,
@@ -234,11 +240,12 @@ __device__ __forceinline__ bool put_groups(const F2 (&y)[8], const F2 (&z)[8], i
   key = max(key, __shfl_xor_sync(0xffffffffu, key, 2));
   key = max(key, __shfl_xor_sync(0xffffffffu, key, 4));
   const GroupScale g = group_scale<F>(__uint_as_float(key), sfmt);
-  const float inv = g.fast ? g.inv : 0.0f, other = __shfl_xor_sync(0xffffffffu, inv, 1);
+  if (!__all_sync(0xffffffffu, g.fast)) return false;
+  const float other = __shfl_xor_sync(0xffffffffu, g.inv, 1);
   if (live && (threadIdx.x & 7u) < 2u) store_scale(odd ? sz : sy, at, g.stored, sfmt);
-  put16(qy, codes16_times<F>(y, odd ? other : inv), in);
-  put16(qz, codes16_times<F>(z, odd ? inv : other), in);
-  return inv != 0.0f && other != 0.0f;
+  put16(qy, codes16_times<F>(y, odd ? other : g.inv), in);
+  put16(qz, codes16_times<F>(z, odd ? g.inv : other), in);
+  return true;
 }
 // Under the tensor's scale d, the maximum into `top`.
 template <int F>
@@ -251,26 +258,34 @@ __device__ __forceinline__ void put_tensor(const F2 (&y)[8], const CodeScale &d,
 template <int F>
 __device__ __forceinline__ void put_tensor_any(const F2 (&y)[8], const CodeScale &d, float &top,
                                                uint8_t *q, bool in) {
-  if (in) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) top = max_abs2(top, y[i]);
-  }
-  put16(q, codes16_any<F>(y, d.s), in);
+  for (int i = 0; i < 8; ++i) top = max_abs2(top, y[i]);
+  put16(q, d.fast ? codes16_times<F>(y, d.inv) : codes16_any<F>(y, d.s), in);
 }
 
-// The activation by its number.
-__device__ __noinline__ uint64_t act_value_any(uint64_t z, int act) {
-  F2 r(z);
-  with_act<true>(act, [&](auto a) { r = act_value2<a.value>(F2(z)); });
+// The activation by its number: the loops' forms, and those for any argument.
+__device__ __noinline__ uint64_t act_of_word_any(uint32_t w, int act) {
+  F2 r(bf16_pair(w));
+  with_act(act, [&](auto a) { r = act_of_word<a.value>(w); });
   return r.v;
 }
-__device__ __noinline__ uint64_t act_slope_any(uint64_t z, int act) {
-  F2 r(1.0f);
-  with_act(act, [&](auto a) { r = act_slope2<a.value>(F2(z)); });
-  return r.v;
+struct BothBits {
+  uint64_t value, slope;
+};
+__device__ __noinline__ BothBits act_both_any(uint64_t z, int act, bool common) {
+  F2 value(z), slope(1.0f);
+  with_act(act, [&](auto a) {
+    if (common) {
+      act_both2<a.value>(F2(z), value, slope);
+    } else {
+      value = act_value2<a.value>(F2(z));
+      slope = act_slope2<a.value>(F2(z));
+    }
+  });
+  return BothBits{value.v, slope.v};
 }
 
-// The groups that the loop has noted, again.
+// The tiles that this warp has noted, again.
 template <int F>
 __device__ __noinline__ float act_slow_walk(const ActArgs &a, uint32_t rows, float top,
                                              uint32_t noted) {
@@ -278,20 +293,19 @@ __device__ __noinline__ float act_slow_walk(const ActArgs &a, uint32_t rows, flo
   const __nv_bfloat16 *u = static_cast<const __nv_bfloat16 *>(a.u);
   const uint32_t N = (uint32_t)a.N;
   const CodeScale d(a.scale != nullptr ? *a.scale : 1.0f);
-  uint32_t step = 0;
+  uint32_t step = 0u;
 #pragma unroll 1
   for (TileWalk t(rows, N); t.left > 0; t.next(), ++step) {
-    const bool live = tile_noted(noted, step) && t.row < rows;
-    if (!__any_sync(0xffffffffu, live)) continue;
+    if (!tile_noted(noted, step)) continue;
     const int64_t at = t.scale_at(a.M), flat = t.at(a.N);
-    const bool in = live && t.col() < N, owner = live && (threadIdx.x & 7u) == 0u;
+    const bool in = t.row < rows && t.col() < N, owner = t.row < rows && (threadIdx.x & 7u) == 0u;
     const Words16 hv = load16(h + t.at(a.ldh), in);
     Words16 uv = hv;
     if (u != nullptr) uv = load16(u + t.at(a.ldu), in);
     F2 y[8], x[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      y[i] = F2(act_value_any(hv.pair(i).v, a.act));
+      y[i] = F2(act_of_word_any(hv.word(i), a.act));
       if (u != nullptr) y[i] = y[i] * uv.pair(i);
     }
     if (a.hq != nullptr) {
@@ -368,7 +382,7 @@ __global__ void __launch_bounds__(kTileThreads, ctas_per_sm(GATE))
       put_tensor<F>(y, d, top, a.q + flat, in);
     else
       fast &= put_group<F>(y, max_abs16(y), a.sfmt, a.q + flat, a.scales, at, in, owner);
-    if (!fast) note_tile(noted, t.step(rows));
+    if (!__all_sync(0xffffffffu, fast)) note_tile(noted, t.step(rows));
   }
   if (__any_sync(0xffffffffu, noted != 0u)) top = act_slow_walk<F>(a, rows, top, noted);
   if (a.amax != nullptr) block_max_to(__float_as_uint(top), a.amax);
@@ -377,7 +391,7 @@ __global__ void __launch_bounds__(kTileThreads, ctas_per_sm(GATE))
 // The loop's forms hold for checkpoints of values up to this.
 constexpr float kKeptScaleMax = 0x1p40f;
 
-// The groups that the loop has noted, again.
+// The tiles that this warp has noted, again.
 template <int F>
 __device__ __noinline__ void act_grad_slow_walk(const ActGradArgs &a, uint32_t rows, uint32_t noted,
                                                 float &top_h, float &top_u) {
@@ -386,14 +400,12 @@ __device__ __noinline__ void act_grad_slow_walk(const ActGradArgs &a, uint32_t r
   const bool gate = a.uq != nullptr;
   const CodeScale dh(a.scale_h != nullptr ? *a.scale_h : 1.0f);
   const CodeScale du(a.scale_u != nullptr ? *a.scale_u : 1.0f);
-  uint32_t step = 0;
+  uint32_t step = 0u;
 #pragma unroll 1
   for (TileWalk t(rows, N); t.left > 0; t.next(), ++step) {
-    const bool live = tile_noted(noted, step) && t.row < rows;
-    if (!__any_sync(0xffffffffu, live)) continue;
+    if (!tile_noted(noted, step)) continue;
     const int64_t at = t.scale_at(a.M), flat = t.at(a.N);
-    const bool in = live && t.col() < N;
-    const bool owner_h = live && (threadIdx.x & 7u) == 0u, owner_u = live && (threadIdx.x & 7u) == 1u;
+    const bool in = t.row < rows && t.col() < N, owner = t.row < rows && (threadIdx.x & 7u) == 0u;
     const Words16 v = load16(da + t.at(a.ld_da), in);
     Vec16<uint8_t> hc, uc;
     hc.zero();
@@ -412,9 +424,9 @@ __device__ __noinline__ void act_grad_slow_walk(const ActGradArgs &a, uint32_t r
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const F2 z = kept_pair(hc.w[0], i, F2(hs)), g = v.pair(i);
-      yu[i] = g * F2(act_value_any(z.v, a.act));
-      const F2 slope(act_slope_any(z.v, a.act));
-      yh[i] = gate ? g * kept_pair(uc.w[0], i, F2(us)) * slope : g * slope;
+      const BothBits both = act_both_any(z.v, a.act, hs <= kKeptScaleMax);
+      yu[i] = g * F2(both.value);
+      yh[i] = gate ? g * kept_pair(uc.w[0], i, F2(us)) * F2(both.slope) : g * F2(both.slope);
     }
     if (a.dh != nullptr && in) store16(static_cast<__nv_bfloat16 *>(a.dh) + t.at(a.ld_d), yh);
     if (a.du != nullptr && in) store16(static_cast<__nv_bfloat16 *>(a.du) + t.at(a.ld_d), yu);
@@ -424,9 +436,9 @@ __device__ __noinline__ void act_grad_slow_walk(const ActGradArgs &a, uint32_t r
       if (a.qu != nullptr) put_tensor_any<F>(yu, du, top_u, a.qu + qat, in);
     } else {
       if (a.qh != nullptr)
-        put_group_any<F>(yh, max_abs16(yh), a.sfmt, a.qh + qat, a.sh, at, in, owner_h);
+        put_group_any<F>(yh, max_abs16(yh), a.sfmt, a.qh + qat, a.sh, at, in, owner);
       if (a.qu != nullptr)
-        put_group_any<F>(yu, max_abs16(yu), a.sfmt, a.qu + qat, a.su, at, in, owner_u);
+        put_group_any<F>(yu, max_abs16(yu), a.sfmt, a.qu + qat, a.su, at, in, owner);
     }
   }
 }
@@ -472,21 +484,14 @@ __global__ void __launch_bounds__(kTileThreads, ctas_per_sm(GATE))
     const TileWalk t = w;
     const int64_t at = t.scale_at(a.M);
     const bool in = t.row < rows && t.col() < N;
-    Words16 v = vn;
-    Vec16<uint8_t> hc = hn, uc = un;
-    float hs = kept_scale<KEPT>(hsn), us = kept_scale<KEPT>(usn);
+    const Words16 v = vn;
+    const Vec16<uint8_t> hc = hn, uc = un;
+    const float hs = kept_scale<KEPT>(hsn), us = kept_scale<KEPT>(usn);
     w.next();
     fetch();
-    bool fast = true;
-    const uint32_t common = __ballot_sync(0xffffffffu, hs <= kKeptScaleMax);
-    if (common != 0xffffffffu) {  // zeros in the place of such a row (in no maximum)
-      fast = (common >> (threadIdx.x & 24u) & 0xFFu) == 0xFFu;
-      if (!fast) {
-        v.a = v.b = make_uint4(0u, 0u, 0u, 0u);
-        hc.zero();
-        uc.zero();
-        hs = us = 0.0f;
-      }
+    if (!__all_sync(0xffffffffu, hs <= kKeptScaleMax)) {
+      note_tile(noted, t.step(rows));
+      continue;
     }
     F2 yh[8], yu[8];
 #pragma unroll
@@ -505,18 +510,19 @@ __global__ void __launch_bounds__(kTileThreads, ctas_per_sm(GATE))
       store16(static_cast<__nv_bfloat16 *>(a.du) + t.at(a.ld_d), yu);
     const int64_t qat = t.at(a.ld_q);
     const bool live = t.row < rows;
+    bool fast = true;
     if (tensor) {
       if (a.qh != nullptr) put_tensor<F>(yh, dh, top_h, a.qh + qat, in);
       if (GATE && a.qu != nullptr) put_tensor<F>(yu, du, top_u, a.qu + qat, in);
     } else if (GATE && a.qh != nullptr && a.qu != nullptr) {
-      fast &= put_groups<F>(yh, yu, a.sfmt, a.qh + qat, a.qu + qat, a.sh, a.su, at, in, live);
+      fast = put_groups<F>(yh, yu, a.sfmt, a.qh + qat, a.qu + qat, a.sh, a.su, at, in, live);
     } else {
-      // (the lanes that put_groups takes: whoever stores a scale stores it again)
-      const uint32_t lane = threadIdx.x & 7u;
+      const bool owner = live && (threadIdx.x & 7u) == 0u;
       if (a.qh != nullptr)
-        fast &= put_group<F>(yh, max_abs16(yh), a.sfmt, a.qh + qat, a.sh, at, in, live && lane == 0u);
+        fast = put_group<F>(yh, max_abs16(yh), a.sfmt, a.qh + qat, a.sh, at, in, owner);
       if (GATE && a.qu != nullptr)
-        fast &= put_group<F>(yu, max_abs16(yu), a.sfmt, a.qu + qat, a.su, at, in, live && lane == 1u);
+        fast &= put_group<F>(yu, max_abs16(yu), a.sfmt, a.qu + qat, a.su, at, in, owner);
+      fast = __all_sync(0xffffffffu, fast);
     }
     if (!fast) note_tile(noted, t.step(rows));
   }

@@ -137,14 +137,14 @@ def test_a_batch_and_its_rows_alone(gate, sfmt):
             assert torch.equal(t.contiguous().view(torch.uint8), one[key].view(torch.uint8)), (r, key)
 
 
-@pytest.mark.parametrize("gate", [True, False])
-def test_long_walks(gate):
-    """More tiles than resident CTAs take 256 of each: the rows of a short pattern,
+@pytest.mark.parametrize("gate,each", [(True, 256), (False, 256), (False, 1024)])
+def test_long_walks(gate, each):
+    """More tiles than resident CTAs take `each` of: the rows of a short pattern,
     repeated, with extreme ones at the walks' ends and between."""
     F = lib()
     sms = torch.cuda.get_device_properties(0).multi_processor_count
     n, period = 128, 64
-    times = (32 * (sms * (3 if gate else 4) * 256 + 5)) // period
+    times = (32 * (sms * (3 if gate else 4) * each + 5)) // period
     m = times * period
     small_h, small_u = randn((2 * period, n), 7), randn((2 * period, n), 8) if gate else None
     small_h[period:] = (small_h[period:].float() * 1e-32).to(BF)
